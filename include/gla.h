@@ -343,6 +343,134 @@ gla_status gla_chunk_bwd_from(const void* q, const void* k, const void* v, const
                               void* dk_, void* dv_, float* dg, int B, int H, int T, int dk, int dv, int chunk, int P,
                               int dtype, void* workspace, size_t workspace_size, void* stream);
 
+/*
+ * ---- A recurrent block's other operators ----
+ *
+ * What stands next to the chunked calls above in a model of recurrent blocks, trained and served:
+ * the elementwise gated linear recurrence (gla_recur_fwd, gla_recur_bwd), the join of a block's
+ * output with the residual stream (gla_join_fwd, gla_join_bwd), and the forms for single tokens
+ * over a pool of states (gla_step, gla_recur_step).
+ *
+ * The conventions above hold, with these differences:
+ *   - Outputs and states are contiguous.  The other tensors may be views whose last dimension is
+ *     contiguous (a slice of a fused projection, a permuted batch): a gla_strides argument gives
+ *     the strides of the dimensions before the last, in elements, none negative; NULL means
+ *     contiguous.  A dimension the tensor does not have is ignored (h for [B][T][D], t and h for
+ *     [B][D]).  Rows on 16 bytes are read fastest; any alignment of the element type is accepted.
+ *   - Any size >= 1 up to the limits named at each call; no multiples are required.
+ *   - lens and slots are int arrays on the device.  Their values are checked there, by the kernels.
+ */
+typedef struct {
+  long long b, h, t;
+} gla_strides;
+
+/* The input's factor in the recurrence: 1; 1 - a (an interpolation of the state and the input);
+ * sqrt(1 - a^2) (an input of unit variance keeps a state of unit variance).  a = exp(g). */
+enum { GLA_RECUR_PLAIN = 0, GLA_RECUR_LERP = 1, GLA_RECUR_NORM = 2 };
+/* Tokens between the states that gla_recur_fwd keeps for gla_recur_bwd. */
+enum { GLA_RECUR_CHUNK = 128 };
+/* The gate of gla_join: z sigmoid(z) or sigmoid(z). */
+enum { GLA_ACT_SILU = 0, GLA_ACT_SIGMOID = 1 };
+
+/*
+ * gla_recur_workspace_size -- bytes of device workspace gla_recur_fwd and gla_recur_bwd need for
+ * these sizes; 0 if none (or, with gla_last_error() set, if the sizes are rejected).
+ */
+size_t gla_recur_workspace_size(int B, int T, int D);
+
+/*
+ * gla_recur_fwd -- the elementwise gated linear recurrence, per sequence b and channel c:
+ *   h_t = a_t h_{t-1} + beta(g_t) x_t,   a_t = exp(g_t),   h_{-1} = h0 (NULL = 0)
+ * with beta by mode (GLA_RECUR_*).  x [B][T][D] (dtype), g [B][T][D] (float32, finite and <= 0, or
+ * -inf: a reset, a token that starts from no state whatever the state held, e.g. the first token
+ * of a packed document).  The state is float32.
+ * lens: int32 [B] or NULL: sequence b has lens[b] tokens (limited to 0..T).  x and g of the tokens
+ * behind are ignored whatever they hold; h is zero there.
+ * Outputs, fully overwritten: h [B][T][D] (dtype); h_final [B][D] (float32, the state after the
+ * last token, h0 for an empty sequence; may be NULL); chunk_in [B][ceil(T/128)][D] (float32, the
+ * state entering every GLA_RECUR_CHUNK tokens, for gla_recur_bwd; may be NULL in a forward-only
+ * call).  B <= 65535.  The results do not depend on the timing of the run, bit for bit.
+ * workspace: gla_recur_workspace_size bytes; rules as for gla_chunk_fwd.
+ */
+gla_status gla_recur_fwd(const void* x, const gla_strides* x_st, const float* g, const gla_strides* g_st,
+                         const float* h0, const int* lens, void* h, float* chunk_in, float* h_final, int B, int T,
+                         int D, int mode, int dtype, void* workspace, size_t workspace_size, void* stream);
+
+/*
+ * gla_recur_bwd -- its gradients, for dh [B][T][D] (dtype, the gradient of h) and dhT [B][D]
+ * (float32, the gradient of h_final; NULL = 0).  With G_t the gradient of the state after token t,
+ *   G_t = dh_t + a_{t+1} G_{t+1},   G_{len-1} = dh_{len-1} + dhT
+ *   dx_t = beta(g_t) G_t,   dg_t = a_t h_{t-1} G_t + beta'(g_t) x_t G_t,   dh0 = a_0 G_0
+ * chunk_in is the forward's, over the same x, g, h0, lens and mode; h_{t-1} is rebuilt from it in
+ * float32.  beta' at g = 0 in GLA_RECUR_NORM, where the square root has no slope, counts as 0.
+ * Outputs, fully overwritten: dx [B][T][D] (dtype), dg [B][T][D] (float32), both zero behind a
+ * sequence's end; dh0 [B][D] (float32, dhT for an empty sequence; may be NULL).  dh of the tokens
+ * behind is ignored.  An input that was broadcast over a dimension sums its gradient itself.
+ */
+gla_status gla_recur_bwd(const void* x, const gla_strides* x_st, const float* g, const gla_strides* g_st,
+                         const void* dh, const gla_strides* dh_st, const float* chunk_in, const int* lens,
+                         const float* dhT, void* dx, float* dg, float* dh0, int B, int T, int D, int mode, int dtype,
+                         void* workspace, size_t workspace_size, void* stream);
+
+/*
+ * gla_recur_step -- one token of gla_recur_fwd for every row of a batch, in place on a pool of
+ * states [n_slots][D] (float32): row b's state is state[slots[b]] (slots NULL: state[b]).
+ * x, g [B][D]; h [B][D] (dtype).  A negative slot leaves the row out: h is zero there and no state
+ * is touched (a padded batch).  A slot of n_slots or more, or one that an earlier row of the same
+ * call names, gives h = NaN and touches no state.
+ */
+gla_status gla_recur_step(const void* x, const gla_strides* x_st, const float* g, const gla_strides* g_st,
+                          float* state, const int* slots, void* h, int B, int D, int n_slots, int mode, int dtype,
+                          void* stream);
+
+/*
+ * gla_step -- the next n tokens of gated linear attention for every row of a batch, in place on a
+ * pool of states [n_slots][H][dk][dv] (float32), one or a few at a time (decoding, or the end of a
+ * prompt that fills no chunk):
+ *   S <- diag(exp(g_t)) S + k_t v_t^T,   o_t = S^T q_t,   t = 0 .. n-1
+ * q, k [B][H][n][dk], v [B][H][n][dv], o [B][H][n][dv] (dtype), g [B][H][n][dk] (float32, <= 0, or
+ * -inf for a reset); row b's state is state[slots[b]], with the rules of gla_recur_step.  A state
+ * is row-major [dk][dv]: gla_segment_scan's h_out as it stands.  dk <= 256, any dv >= 1.
+ */
+gla_status gla_step(const void* q, const gla_strides* q_st, const void* k, const gla_strides* k_st, const void* v,
+                    const gla_strides* v_st, const float* g, const gla_strides* g_st, float* state, const int* slots,
+                    void* o, int B, int H, int n, int dk, int dv, int n_slots, int dtype, void* stream);
+
+/*
+ * gla_join_fwd -- a block's output joins the residual stream, and the next block's input is normed,
+ * in one pass.  For every row (b, t) of D = H d values, y's heads side by side:
+ *   u = y rsqrt(mean_d(y^2) + eps) w_post       per head; w_post [d], NULL: u = y
+ *   m = u act(z)                                z [B][T][D], NULL: m = u
+ *   out = residual + scale m                    residual [B][T][D], NULL = 0; scale [D], NULL = 1
+ *   normed = out rsqrt(mean_D(out^2) + eps) w_pre     w_pre [D]; NULL with normed NULL: none
+ * y [B][H][T][d] (the layout of o; H = 1 for a [B][T][D] output).  y, z and normed have dtype;
+ * residual and out have stream_dtype (GLA_F32, or GLA_BF16 with a bf16 dtype); the weights are
+ * float32.  All arithmetic is float32, and normed is formed from out before its rounding.
+ * out may be the residual itself (contiguous; a forward-only call).  rstd_post [B][T][H] and
+ * rstd_pre [B][T] (float32, for gla_join_bwd) may be NULL.  eps > 0.  H d <= 8192.
+ */
+gla_status gla_join_fwd(const void* y, const gla_strides* y_st, const void* z, const gla_strides* z_st,
+                        const float* w_post, const void* residual, const gla_strides* r_st, const float* scale,
+                        const float* w_pre, void* out, void* normed, float* rstd_post, float* rstd_pre, int B, int H,
+                        int T, int d, int act, float eps, int dtype, int stream_dtype, void* stream);
+
+/* Bytes of device workspace gla_join_bwd needs when it returns a weight's gradient. */
+size_t gla_join_workspace_size(int B, int H, int T, int d);
+
+/*
+ * gla_join_bwd -- its gradients, for d_out (stream_dtype; NULL = 0) and d_normed (dtype; NULL = 0;
+ * not both NULL), over the forward's inputs and the rstd_post, rstd_pre it kept.  Outputs, fully
+ * overwritten: dy [B][H][T][d], dz (with z), d_residual (may be NULL), and the weights' gradients
+ * dw_post [d] (summed over the heads), dscale [D], dw_pre [D] (each may be NULL), summed in float32
+ * in an order that does not depend on the timing.  Strides, types and limits as gla_join_fwd.
+ */
+gla_status gla_join_bwd(const void* y, const gla_strides* y_st, const void* z, const gla_strides* z_st,
+                        const float* w_post, const void* residual, const gla_strides* r_st, const float* scale,
+                        const float* w_pre, const float* rstd_post, const float* rstd_pre, const void* d_out,
+                        const gla_strides* do_st, const void* d_normed, const gla_strides* dn_st, void* dy, void* dz,
+                        void* d_residual, float* dw_post, float* dscale, float* dw_pre, int B, int H, int T, int d,
+                        int act, int dtype, int stream_dtype, void* workspace, size_t workspace_size, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

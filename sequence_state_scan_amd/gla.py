@@ -28,6 +28,9 @@ HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))
 GLA_OK, GLA_ERR_INVALID_ARG, GLA_ERR_UNSUPPORTED, GLA_ERR_HIP = 0, 1, 2, 3
 GLA_F32, GLA_BF16 = 0, 1
 GLA_FWD, GLA_BWD = 0, 1
+RECUR_MODES = {"plain": 0, "lerp": 1, "norm": 2}
+RECUR_CHUNK = 128
+ACTS = {"silu": 0, "sigmoid": 1}
 
 _lib = None
 _lock = threading.Lock()
@@ -78,6 +81,23 @@ def load_library(path: str = LIB_PATH):
         lib.gla_chunk_dstate.restype = i
         lib.gla_chunk_bwd_from.argtypes = [vp, vp, vp, fp, vp, vp, fp, fp, vp, vp, vp, fp] + [i] * 8 + [vp, sz, vp]
         lib.gla_chunk_bwd_from.restype = i
+        fl = ctypes.c_float
+        lib.gla_recur_workspace_size.argtypes = [i] * 3
+        lib.gla_recur_workspace_size.restype = sz
+        lib.gla_recur_fwd.argtypes = [vp] * 9 + [i] * 5 + [vp, sz, vp]
+        lib.gla_recur_fwd.restype = i
+        lib.gla_recur_bwd.argtypes = [vp] * 12 + [i] * 5 + [vp, sz, vp]
+        lib.gla_recur_bwd.restype = i
+        lib.gla_recur_step.argtypes = [vp] * 7 + [i] * 5 + [vp]
+        lib.gla_recur_step.restype = i
+        lib.gla_step.argtypes = [vp] * 11 + [i] * 7 + [vp]
+        lib.gla_step.restype = i
+        lib.gla_join_workspace_size.argtypes = [i] * 4
+        lib.gla_join_workspace_size.restype = sz
+        lib.gla_join_fwd.argtypes = [vp] * 13 + [i] * 5 + [fl, i, i, vp]
+        lib.gla_join_fwd.restype = i
+        lib.gla_join_bwd.argtypes = [vp] * 21 + [i] * 7 + [vp, sz, vp]
+        lib.gla_join_bwd.restype = i
         if path == LIB_PATH:
             _lib = lib
         return lib
@@ -468,31 +488,344 @@ def gla_chunk_bwd_from(q, k, v, g, do, chunk_states, seg_in, seg_grad, chunk: in
     return dq, dk, dv, dg
 
 
+# --------------------------------------------------------------- a recurrent block's other operators
+
+def _view(t, name, shape, dtype, device):
+    """(pointer, strides) of an input that may be a view with a contiguous last dimension, after
+    checking it as _expect does; strides are None for a contiguous tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.dtype != dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.is_contiguous():
+        return t.data_ptr(), None
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] != 1:
+        raise ValueError("%s must be contiguous in its last dimension (strides %s)" % (name, st))
+    if len(st) == 4:
+        return t.data_ptr(), (ctypes.c_longlong * 3)(st[0], st[1], st[2])
+    return t.data_ptr(), (ctypes.c_longlong * 3)(st[0], 0, st[1] if len(st) == 3 else 0)
+
+
+def _out(t, name, shape, dtype, device, optional=False):
+    """Pointer of a contiguous tensor (None for an optional one that is not given), checked."""
+    if t is None and optional:
+        return None
+    _expect(t, name, shape, dtype, device)
+    return t.data_ptr()
+
+
+def _on_gpu(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("libgla works on device tensors only (got a %s tensor)" % t.device)
+
+
+def _code(table, key, name):
+    if key not in table:
+        raise ValueError("unknown %s %r (one of %s)" % (name, key, ", ".join(sorted(table))))
+    return table[key]
+
+
+def _launch(fn, device, *args):
+    """The C call on torch's current stream of ``device``, with that device current (a kernel is
+    launched on the current one)."""
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream)
+    if status != GLA_OK:
+        _check(status)
+
+
+def recur_workspace_size(B: int, T: int, D: int) -> int:
+    """Bytes of workspace gla_recur_fwd and gla_recur_bwd need (0: none)."""
+    lib = load_library()
+    n = lib.gla_recur_workspace_size(B, T, D)
+    if n == 0 and lib.gla_last_error():
+        raise GLAError(GLA_ERR_INVALID_ARG, lib.gla_last_error().decode())
+    return int(n)
+
+
+def join_workspace_size(B: int, H: int, T: int, d: int) -> int:
+    """Bytes of workspace gla_join_bwd needs for the weights' gradients."""
+    lib = load_library()
+    n = lib.gla_join_workspace_size(B, H, T, d)
+    if n == 0:
+        raise GLAError(GLA_ERR_INVALID_ARG, lib.gla_last_error().decode())
+    return int(n)
+
+
+def _scratch(ws, need, device):
+    """(tensor to keep alive, pointer, bytes) of a workspace: the caller's, or one of ``need`` bytes."""
+    if ws is None:
+        if need == 0:
+            return None, None, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    if not isinstance(ws, torch.Tensor) or ws.device != device or not ws.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on %s" % device)
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _recur_dims(x):
+    _on_gpu(x, "x")
+    if x.dim() != 3:
+        raise ValueError("x must be a [B, T, D] tensor")
+    return x.shape
+
+
+def gla_recur_fwd(x, g, h0=None, lens=None, mode: str = "plain", h=None, chunk_in=None, h_final=None, workspace=None,
+                  keep_chunk_states: bool = True):
+    """Elementwise gated linear recurrence h_t = exp(g_t) h_{t-1} + beta(g_t) x_t over x [B, T, D]
+    (bf16 or float32) and log-gates g [B, T, D] (float32, <= 0, or -inf for a reset), from h0
+    [B, D] (float32, default zero).  mode: the input's factor beta, "plain" (1), "lerp" (1 - a) or
+    "norm" (sqrt(1 - a^2)).  lens: int32 [B], the sequences' lengths in a padded batch (h is zero
+    behind them).  x and g may be views whose last dimension is contiguous.
+    Returns (h [B, T, D] in x's dtype, chunk_in [B, ceil(T/128), D], h_final [B, D], float32).
+    chunk_in is what gla_recur_bwd rebuilds the states from; None with keep_chunk_states=False."""
+    B, T, D = _recur_dims(x)
+    dev, f32 = x.device, torch.float32
+    m, dt = _code(RECUR_MODES, mode, "mode"), _dtype_code(x.dtype)
+    xp, xs = _view(x, "x", (B, T, D), x.dtype, dev)
+    gp, gs = _view(g, "g", (B, T, D), f32, dev)
+    h0p = _out(h0, "h0", (B, D), f32, dev, optional=True)
+    lp = _out(lens, "lens", (B,), torch.int32, dev, optional=True)
+    if h is None:
+        h = torch.empty((B, T, D), dtype=x.dtype, device=dev)
+    if h_final is None:
+        h_final = torch.empty((B, D), dtype=f32, device=dev)
+    cs_shape = (B, (T + RECUR_CHUNK - 1) // RECUR_CHUNK, D)
+    if not keep_chunk_states:
+        if chunk_in is not None:
+            raise ValueError("chunk_in given with keep_chunk_states=False")
+    elif chunk_in is None:
+        chunk_in = torch.empty(cs_shape, dtype=f32, device=dev)
+    hp = _out(h, "h", (B, T, D), x.dtype, dev)
+    cp = _out(chunk_in, "chunk_in", cs_shape, f32, dev, optional=True)
+    fp = _out(h_final, "h_final", (B, D), f32, dev)
+    workspace, wp, wn = _scratch(workspace, recur_workspace_size(B, T, D), dev)
+    _launch(load_library().gla_recur_fwd, dev, xp, xs, gp, gs, h0p, lp, hp, cp, fp, B, T, D, m, dt, wp, wn)
+    return h, chunk_in, h_final
+
+
+def gla_recur_bwd(x, g, dh, chunk_in, lens=None, dhT=None, mode: str = "plain", dx=None, dg=None, dh0=None,
+                  workspace=None):
+    """Gradients of gla_recur_fwd for dh [B, T, D] (the gradient of h, x's dtype) and dhT [B, D]
+    (of h_final, float32, default zero), over the forward's x, g, lens, mode and the chunk_in it
+    returned.  Returns (dx [B, T, D] in x's dtype, dg [B, T, D], dh0 [B, D], float32)."""
+    B, T, D = _recur_dims(x)
+    dev, f32 = x.device, torch.float32
+    m, dt = _code(RECUR_MODES, mode, "mode"), _dtype_code(x.dtype)
+    xp, xs = _view(x, "x", (B, T, D), x.dtype, dev)
+    gp, gs = _view(g, "g", (B, T, D), f32, dev)
+    dp, ds = _view(dh, "dh", (B, T, D), x.dtype, dev)
+    cp = _out(chunk_in, "chunk_in", (B, (T + RECUR_CHUNK - 1) // RECUR_CHUNK, D), f32, dev)
+    lp = _out(lens, "lens", (B,), torch.int32, dev, optional=True)
+    tp = _out(dhT, "dhT", (B, D), f32, dev, optional=True)
+    if dx is None:
+        dx = torch.empty((B, T, D), dtype=x.dtype, device=dev)
+    if dg is None:
+        dg = torch.empty((B, T, D), dtype=f32, device=dev)
+    if dh0 is None:
+        dh0 = torch.empty((B, D), dtype=f32, device=dev)
+    dxp, dgp = _out(dx, "dx", (B, T, D), x.dtype, dev), _out(dg, "dg", (B, T, D), f32, dev)
+    d0p = _out(dh0, "dh0", (B, D), f32, dev)
+    workspace, wp, wn = _scratch(workspace, recur_workspace_size(B, T, D), dev)
+    _launch(load_library().gla_recur_bwd, dev, xp, xs, gp, gs, dp, ds, cp, lp, tp, dxp, dgp, d0p, B, T, D, m, dt, wp, wn)
+    return dx, dg, dh0
+
+
+def _pool(state, slots, B, shape, dev):
+    """(pointer of the pool, pointer of the slots, states in the pool), checked."""
+    if not isinstance(state, torch.Tensor) or state.dim() != len(shape) + 1:
+        raise ValueError("state must be a [slots%s] tensor" % "".join(", %d" % n for n in shape))
+    n = state.shape[0]
+    sp = _out(state, "state", (n,) + shape, torch.float32, dev)
+    if slots is None and n < B:
+        raise ValueError("state holds %d states, the batch has %d rows" % (n, B))
+    return sp, _out(slots, "slots", (B,), torch.int32, dev, optional=True), n
+
+
+def gla_recur_step(x, g, state, slots=None, mode: str = "plain", h=None):
+    """One token of gla_recur_fwd for every row of x [B, D], in place on the pool ``state``
+    [n_slots, D] (float32): row b's state is state[slots[b]] (slots int32; default state[b]).  A
+    negative slot leaves its row out (h is zero there); a slot outside the pool, or one that an
+    earlier row names, gives NaN and touches no state.  Returns h [B, D] in x's dtype."""
+    _on_gpu(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be a [B, D] tensor")
+    B, D = x.shape
+    dev = x.device
+    m, dt = _code(RECUR_MODES, mode, "mode"), _dtype_code(x.dtype)
+    xp, xs = _view(x, "x", (B, D), x.dtype, dev)
+    gp, gs = _view(g, "g", (B, D), torch.float32, dev)
+    sp, ip, n = _pool(state, slots, B, (D,), dev)
+    if h is None:
+        h = torch.empty((B, D), dtype=x.dtype, device=dev)
+    hp = _out(h, "h", (B, D), x.dtype, dev)
+    _launch(load_library().gla_recur_step, dev, xp, xs, gp, gs, sp, ip, hp, B, D, n, m, dt)
+    return h
+
+
+def gla_step(q, k, v, g, state, slots=None, o=None):
+    """The next n tokens of gated linear attention for every row of a batch (n = 1: decoding), in
+    place on the pool ``state`` [n_slots, H, dk, dv] (float32; a forward chain's h_final is B such
+    states): q, k [B, H, n, dk], v [B, H, n, dv] (bf16 or float32), g [B, H, n, dk] (float32).
+    Row b's state is state[slots[b]], with the rules of gla_recur_step.  q, k, v and g may be views
+    whose last dimension is contiguous.  Returns o [B, H, n, dv]."""
+    _on_gpu(q, "q")
+    if q.dim() != 4 or not isinstance(v, torch.Tensor) or v.dim() != 4:
+        raise ValueError("q and v must be [B, H, n, d] tensors")
+    B, H, n, dk = q.shape
+    dv, dev, dt = v.shape[3], q.device, _dtype_code(q.dtype)
+    qp, qs = _view(q, "q", (B, H, n, dk), q.dtype, dev)
+    kp, ks = _view(k, "k", (B, H, n, dk), q.dtype, dev)
+    vp, vs = _view(v, "v", (B, H, n, dv), q.dtype, dev)
+    gp, gs = _view(g, "g", (B, H, n, dk), torch.float32, dev)
+    sp, ip, n_slots = _pool(state, slots, B, (H, dk, dv), dev)
+    if o is None:
+        o = torch.empty((B, H, n, dv), dtype=q.dtype, device=dev)
+    op = _out(o, "o", (B, H, n, dv), q.dtype, dev)
+    _launch(load_library().gla_step, dev, qp, qs, kp, ks, vp, vs, gp, gs, sp, ip, op, B, H, n, dk, dv, n_slots, dt)
+    return o
+
+
+def _join_args(y, z, w_post, residual, scale, w_pre):
+    _on_gpu(y, "y")
+    if y.dim() != 4:
+        raise ValueError("y must be a [B, H, T, d] tensor")
+    B, H, T, d = y.shape
+    dev, D, f32 = y.device, H * d, torch.float32
+    dt = _dtype_code(y.dtype)
+    yp, ys = _view(y, "y", (B, H, T, d), y.dtype, dev)
+    zp, zs = (None, None) if z is None else _view(z, "z", (B, T, D), y.dtype, dev)
+    wp = _out(w_post, "w_post", (d,), f32, dev, optional=True)
+    st = y.dtype
+    rp = rs = None
+    if residual is not None:
+        if not isinstance(residual, torch.Tensor):
+            raise TypeError("residual must be a torch.Tensor")
+        st = residual.dtype
+        rp, rs = _view(residual, "residual", (B, T, D), st, dev)
+    sp = _out(scale, "scale", (D,), f32, dev, optional=True)
+    np_ = _out(w_pre, "w_pre", (D,), f32, dev, optional=True)
+    return (B, H, T, d), st, dt, (yp, ys, zp, zs, wp, rp, rs, sp, np_)
+
+
+def gla_join_fwd(y, z=None, w_post=None, residual=None, scale=None, w_pre=None, act: str = "silu", eps: float = 1e-6,
+                 out=None, normed=None, keep_rstd: bool = True):
+    """A block's output y [B, H, T, d] (the layout of o; H = 1 for a [B, T, D] output, y[:, None])
+    joins the residual stream, in one pass: per-head RMS norm with w_post [d], gate act(z) with z
+    [B, T, H d] ("silu" or "sigmoid"), out = residual + scale * that, and the next block's input
+    normed = RMS norm of out with w_pre [H d].  Each of z, w_post, residual, scale and w_pre may be
+    None (that step is then left out).  The weights are float32; residual and out have one dtype
+    (float32 or y's), without a residual out has y's.  out may be the residual tensor itself.
+    Returns a dict: out, normed (None without w_pre), and rstd_post [B, T, H], rstd_pre [B, T] for
+    gla_join_bwd (None with keep_rstd=False)."""
+    (B, H, T, d), st, dt, ptrs = _join_args(y, z, w_post, residual, scale, w_pre)
+    dev, D, f32 = y.device, H * d, torch.float32
+    if out is None:
+        out = torch.empty((B, T, D), dtype=st, device=dev)
+    if w_pre is None:
+        if normed is not None:
+            raise ValueError("normed given without w_pre")
+    elif normed is None:
+        normed = torch.empty((B, T, D), dtype=y.dtype, device=dev)
+    op = _out(out, "out", (B, T, D), st, dev)
+    np_ = _out(normed, "normed", (B, T, D), y.dtype, dev, optional=True)
+    r_post = torch.empty((B, T, H), dtype=f32, device=dev) if keep_rstd and w_post is not None else None
+    r_pre = torch.empty((B, T), dtype=f32, device=dev) if keep_rstd and w_pre is not None else None
+    _launch(load_library().gla_join_fwd, dev, *ptrs, op, np_, None if r_post is None else r_post.data_ptr(),
+            None if r_pre is None else r_pre.data_ptr(), B, H, T, d, _code(ACTS, act, "act"), eps, dt, _dtype_code(st))
+    return {"out": out, "normed": normed, "rstd_post": r_post, "rstd_pre": r_pre}
+
+
+def gla_join_bwd(y, fwd: dict, d_out=None, d_normed=None, z=None, w_post=None, residual=None, scale=None, w_pre=None,
+                 act: str = "silu", workspace=None):
+    """Gradients of gla_join_fwd for d_out (the gradient of out, out's dtype) and d_normed (of
+    normed, y's dtype), at least one of them given, over the forward's inputs and the dict it
+    returned.  Returns a dict: dy [B, H, T, d], dz, d_residual, dw_post [d], dscale [H d], dw_pre
+    [H d] (weights' gradients float32; None for the inputs that were not given)."""
+    (B, H, T, d), st, dt, ptrs = _join_args(y, z, w_post, residual, scale, w_pre)
+    dev, D, f32 = y.device, H * d, torch.float32
+    if d_out is None and d_normed is None:
+        raise ValueError("one of d_out and d_normed is required")
+    if d_normed is not None and w_pre is None:
+        raise ValueError("d_normed given without w_pre")
+    rpost = None if w_post is None else _out(fwd["rstd_post"], "fwd['rstd_post']", (B, T, H), f32, dev)
+    rpre = None if d_normed is None else _out(fwd["rstd_pre"], "fwd['rstd_pre']", (B, T), f32, dev)
+    dop, dos = (None, None) if d_out is None else _view(d_out, "d_out", (B, T, D), st, dev)
+    dnp, dns = (None, None) if d_normed is None else _view(d_normed, "d_normed", (B, T, D), y.dtype, dev)
+    dy = torch.empty((B, H, T, d), dtype=y.dtype, device=dev)
+    dz = None if z is None else torch.empty((B, T, D), dtype=y.dtype, device=dev)
+    dr = None if residual is None else torch.empty((B, T, D), dtype=st, device=dev)
+    dwo = None if w_post is None else torch.empty(d, dtype=f32, device=dev)
+    dsc = None if scale is None else torch.empty(D, dtype=f32, device=dev)
+    dwp = None if w_pre is None else torch.empty(D, dtype=f32, device=dev)
+    sums = not (w_post is None and scale is None and w_pre is None)
+    workspace, wp, wn = _scratch(workspace, join_workspace_size(B, H, T, d) if sums else 0, dev)
+    _launch(load_library().gla_join_bwd, dev, *ptrs, rpost, rpre, dop, dos, dnp, dns, dy.data_ptr(),
+            *(None if t is None else t.data_ptr() for t in (dz, dr, dwo, dsc, dwp)), B, H, T, d,
+            _code(ACTS, act, "act"), dt, _dtype_code(st), wp, wn)
+    return {"dy": dy, "dz": dz, "d_residual": dr, "dw_post": dwo, "dscale": dsc, "dw_pre": dwp}
+
+
 # ------------------------------------------------------------------------------ method chains
 
+def _join_backward(do, fwd, join, d_out, d_normed):
+    """(do, gla_join_bwd's dict) of a backward chain: the gradient of o, through the join where the
+    forward had one."""
+    if join is None:
+        if d_out is not None or d_normed is not None:
+            raise ValueError("d_out and d_normed go with join")
+        return do, None
+    if do is not None:
+        raise ValueError("with join the gradients come in as d_out and d_normed, not as do")
+    args = {n: t for n, t in join.items() if n in ("z", "w_post", "residual", "scale", "w_pre", "act")}
+    b = gla_join_bwd(fwd["o"], fwd["join"], d_out=d_out, d_normed=d_normed, **args)
+    return b["dy"], b
+
+
 def zeco_forward(q, k, v, g, chunk: int, P: int, K: int, h0=None, scan: str = "chain",
-                 keep_chunk_states: bool = True):
+                 keep_chunk_states: bool = True, join: dict | None = None):
     """Local pass -> forward segment scan -> correction.  Returns a dict of tensors:
     o (global output), chunk_states (global state after every chunk; None with
     keep_chunk_states=False, for a forward-only caller), seg_in (state entering each segment),
     h_final (state after the last token), seg_state / seg_logdecay (local pass).
-    scan: "chain" (gla_segment_scan) or "allgather" (gla_segment_scan_allgather)."""
+    scan: "chain" (gla_segment_scan) or "allgather" (gla_segment_scan_allgather).
+    join: gla_join_fwd's arguments besides y (z, w_post, residual, scale, w_pre, act, eps): o then
+    joins the residual stream, and the dict holds gla_join_fwd's under "join"."""
     o, chunk_states, seg_state, seg_logdecay = gla_chunk_fwd(q, k, v, g, chunk, P,
                                                              keep_chunk_states=keep_chunk_states)
     seg_in, h_final = _scan(scan, seg_state, seg_logdecay, K, h0, False)
     gla_segment_correct(GLA_FWD, chunk, P, q=q, g=g, seg_in=seg_in, o=o, chunk_states=chunk_states)
-    return {"o": o, "chunk_states": chunk_states, "seg_in": seg_in, "h_final": h_final, "seg_state": seg_state,
-            "seg_logdecay": seg_logdecay}
+    res = {"o": o, "chunk_states": chunk_states, "seg_in": seg_in, "h_final": h_final, "seg_state": seg_state,
+           "seg_logdecay": seg_logdecay}
+    if join is not None:
+        res["join"] = gla_join_fwd(o, **join)
+    return res
 
 
-def zeco_backward(q, k, v, g, do, fwd: dict, chunk: int, P: int, K: int, dhT=None, scan: str = "chain"):
+def zeco_backward(q, k, v, g, do, fwd: dict, chunk: int, P: int, K: int, dhT=None, scan: str = "chain",
+                  join: dict | None = None, d_out=None, d_normed=None):
     """Local backward -> reverse segment scan -> gradient correction.  ``fwd`` is the dict
-    zeco_forward returned.  Returns dq, dk, dv, dg, dh0 (and the intermediates)."""
+    zeco_forward returned.  Returns dq, dk, dv, dg, dh0 (and the intermediates).
+    join: the forward's; the gradients then come in as d_out and d_normed (of the join's out and
+    normed) with do None, and the dict holds gla_join_bwd's under "join"."""
+    do, joined = _join_backward(do, fwd, join, d_out, d_normed)
     dq, dk, dv, dg, seg_dstate = gla_chunk_bwd(q, k, v, g, do, fwd["chunk_states"], fwd["seg_in"], chunk, P)
     seg_grad, dh0 = _scan(scan, seg_dstate, fwd["seg_logdecay"], K, dhT, True)
     gla_segment_correct(GLA_BWD, chunk, P, k=k, v=v, g=g, seg_in=fwd["seg_in"], seg_grad=seg_grad,
                         chunk_states=fwd["chunk_states"], dk=dk, dv=dv, dg=dg)
-    return {"dq": dq, "dk": dk, "dv": dv, "dg": dg, "dh0": dh0, "seg_dstate": seg_dstate, "seg_grad": seg_grad}
+    res = {"dq": dq, "dk": dk, "dv": dv, "dg": dg, "dh0": dh0, "seg_dstate": seg_dstate, "seg_grad": seg_grad}
+    return res if joined is None else dict(res, join=joined)
 
 
 def states_first_segments(B: int, H: int, T: int, chunk: int, P: int) -> int:
@@ -510,31 +843,37 @@ def states_first_segments(B: int, H: int, T: int, chunk: int, P: int) -> int:
 
 
 def states_first_forward(q, k, v, g, chunk: int, P: int, K: int, h0=None, scan: str = "chain",
-                         keep_chunk_states: bool = True, fill: bool = True):
+                         keep_chunk_states: bool = True, fill: bool = True, join: dict | None = None):
     """The same forward with the incoming states first: state pass -> forward segment scan ->
     local pass from each segment's true incoming state (no correction).  With fill, the segments
     are first cut to fill the chip (states_first_segments); the per-segment results then count
     those segments, whose number the dict holds as "P".  Returns the dict zeco_forward returns
-    (o, chunk_states, seg_in, h_final, seg_state, seg_logdecay) plus "P"."""
+    (o, chunk_states, seg_in, h_final, seg_state, seg_logdecay) plus "P".  join as in zeco_forward."""
     if fill:
         P = states_first_segments(q.shape[0], q.shape[1], q.shape[2], chunk, P)
     seg_state, seg_logdecay = gla_chunk_state(k, v, g, chunk, P)
     seg_in, h_final = _scan(scan, seg_state, seg_logdecay, K, h0, False)
     o, chunk_states = gla_chunk_fwd_from(q, k, v, g, seg_in, chunk, P, keep_chunk_states=keep_chunk_states)
-    return {"o": o, "chunk_states": chunk_states, "seg_in": seg_in, "h_final": h_final, "seg_state": seg_state,
-            "seg_logdecay": seg_logdecay, "P": P}
+    res = {"o": o, "chunk_states": chunk_states, "seg_in": seg_in, "h_final": h_final, "seg_state": seg_state,
+           "seg_logdecay": seg_logdecay, "P": P}
+    if join is not None:
+        res["join"] = gla_join_fwd(o, **join)
+    return res
 
 
-def states_first_backward(q, k, v, g, do, fwd: dict, chunk: int, K: int, dhT=None, scan: str = "chain"):
+def states_first_backward(q, k, v, g, do, fwd: dict, chunk: int, K: int, dhT=None, scan: str = "chain",
+                          join: dict | None = None, d_out=None, d_normed=None):
     """The same backward with the incoming gradients first: state-gradient pass -> reverse segment
     scan -> local backward from each segment's true outgoing gradient (no correction), over the
     segments of ``fwd``, the dict states_first_forward returned.  Returns the dict zeco_backward
-    returns."""
+    returns; join, d_out and d_normed as there."""
+    do, joined = _join_backward(do, fwd, join, d_out, d_normed)
     P = fwd["P"]
     seg_dstate = gla_chunk_dstate(q, g, do, chunk, P)
     seg_grad, dh0 = _scan(scan, seg_dstate, fwd["seg_logdecay"], K, dhT, True)
     dq, dk, dv, dg = gla_chunk_bwd_from(q, k, v, g, do, fwd["chunk_states"], fwd["seg_in"], seg_grad, chunk, P)
-    return {"dq": dq, "dk": dk, "dv": dv, "dg": dg, "dh0": dh0, "seg_dstate": seg_dstate, "seg_grad": seg_grad}
+    res = {"dq": dq, "dk": dk, "dv": dv, "dg": dg, "dh0": dh0, "seg_dstate": seg_dstate, "seg_grad": seg_grad}
+    return res if joined is None else dict(res, join=joined)
 
 
 # ------------------------------------------------------------------------ several streams at once
