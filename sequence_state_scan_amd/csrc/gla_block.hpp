@@ -26,6 +26,8 @@ struct RecurArgs {
   float* h_final;         // [B][D] or null; backward: dh0
   const float* dhT;       // backward: [B][D] or null
   float* dg;              // backward [B][T][D]
+  unsigned long long* words;  // the workspace; in the kernels, the tiles' words (null for one tile)
+  unsigned* ticket;
   Strides xs, gs, dhs;
   int B, T, D, mode, dtype;
 };
@@ -67,6 +69,7 @@ struct JoinArgs {
 
 hipError_t launch_recur_fwd(const RecurArgs& a, hipStream_t s);
 hipError_t launch_recur_bwd(const RecurArgs& a, hipStream_t s);
+size_t recur_workspace_words(int B, int T, int D);  // 8-byte words both need
 hipError_t launch_recur_step(const RecurStepArgs& a, hipStream_t s);
 hipError_t launch_step(const StepArgs& a, hipStream_t s);
 hipError_t launch_join_fwd(const JoinArgs& a, hipStream_t s);

@@ -10,7 +10,7 @@ namespace {
 using gla::set_error;
 using gla::Strides;
 
-constexpr long long kMaxGrid = 1LL << 23;  // workgroups of a launch: at most 2^31 lanes of up to 256
+constexpr long long kMaxGrid = (1LL << 22) - 1;  // workgroups of a launch: fewer than 2^32 lanes at up to 1024 each
 
 gla_status launched(const char* fn, hipError_t e) {
   if (e != hipSuccess) return set_error(GLA_ERR_HIP, "%s: launch failed: %s", fn, hipGetErrorString(e));
@@ -52,7 +52,23 @@ gla_status check_recur(const char* fn, int B, int T, int D, int mode, int dtype)
   if (mode < GLA_RECUR_PLAIN || mode > GLA_RECUR_NORM)
     return set_error(GLA_ERR_INVALID_ARG, "%s: unknown mode %d", fn, mode);
   GLA_TRY(check_dtype(fn, dtype));
-  if (B > 65535) return set_error(GLA_ERR_UNSUPPORTED, "%s: B=%d is above 65535", fn, B);
+  const long long tiles = (long long)B * ((D + 63) / 64);
+  if (B > 65535 || tiles > kMaxGrid || tiles * ((T + gla::kRecurChunk - 1) / gla::kRecurChunk) > kMaxGrid)
+    return set_error(GLA_ERR_UNSUPPORTED, "%s: B=%d, T=%d, D=%d are too many for one call", fn, B, T, D);
+  return GLA_OK;
+}
+
+size_t recur_bytes(int B, int T, int D) {
+  return (gla::recur_workspace_words(B, T, D) * sizeof(unsigned long long) + 255) / 256 * 256;
+}
+
+// The scan's workspace: recur_bytes, on 8 bytes.
+gla_status check_recur_workspace(const char* fn, int B, int T, int D, void* ws, size_t bytes) {
+  const size_t need = recur_bytes(B, T, D);
+  if (need && (!ws || bytes < need))
+    return set_error(GLA_ERR_INVALID_ARG, "%s: needs a workspace of %zu bytes, got %zu", fn, need, ws ? bytes : (size_t)0);
+  if (need && (unsigned long long)ws % 8 != 0)
+    return set_error(GLA_ERR_INVALID_ARG, "%s: the workspace must lie on 8 bytes", fn);
   return GLA_OK;
 }
 
@@ -63,7 +79,7 @@ extern "C" {
 size_t gla_recur_workspace_size(int B, int T, int D) {
   if (check_recur("gla_recur_workspace_size", B, T, D, GLA_RECUR_PLAIN, GLA_F32) != GLA_OK) return 0;
   set_error(GLA_OK, "");
-  return 0;
+  return recur_bytes(B, T, D);
 }
 
 gla_status gla_recur_fwd(const void* x, const gla_strides* x_st, const float* g, const gla_strides* g_st,
@@ -89,7 +105,8 @@ gla_status gla_recur_fwd(const void* x, const gla_strides* x_st, const float* g,
   a.D = D;
   a.mode = mode;
   a.dtype = dtype;
-  (void)workspace_size;
+  GLA_TRY(check_recur_workspace(fn, B, T, D, workspace, workspace_size));
+  a.words = static_cast<unsigned long long*>(workspace);
   return launched(fn, gla::launch_recur_fwd(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -121,7 +138,8 @@ gla_status gla_recur_bwd(const void* x, const gla_strides* x_st, const float* g,
   a.D = D;
   a.mode = mode;
   a.dtype = dtype;
-  (void)workspace_size;
+  GLA_TRY(check_recur_workspace(fn, B, T, D, workspace, workspace_size));
+  a.words = static_cast<unsigned long long*>(workspace);
   return launched(fn, gla::launch_recur_bwd(a, static_cast<hipStream_t>(stream)));
 }
 

@@ -666,6 +666,13 @@ def test_offsets_past_32_bits():
     x[:, -500:] = tail
     h, _, last = gla.gla_recur_fwd(x, g, keep_chunk_states=False)
     ref, _, want = gla.gla_recur_fwd(tail, g[:, :500])
-    assert torch.allclose(last, want, rtol=1e-4, atol=1e-6) and torch.allclose(
-        h[:, -500:].float(), ref.float(), rtol=1e-2, atol=1e-4)
+    # the two runs' chunks lie apart by part of a chunk, so the same terms are combined in other groups:
+    # each is within U (8 H + W) of the recurrence, H its sum of absolute terms, and with one decay a for
+    # all tokens W_t = a (W_{t-1} + 5.02 H_{t-1}) stays below 5.02 H_max / (1 - a) (H_max the largest H)
+    H = gla.gla_recur_fwd(tail.float().abs(), g[:, :500])[0].amax(1).double()
+    tol = 2 * U * (8 + 5.02 / (1 - math.exp(-0.01))) * H
+    assert ((last.double() - want.double()).abs() <= tol).all()
+    step = half_step(BF16)
+    diff = (h[:, -500:].double() - ref.double()).abs()
+    assert (diff <= tol[:, None] + 2 * step * (ref.double().abs() + tol[:, None])).all()
     assert not h[:, :-500].any()
