@@ -193,7 +193,7 @@ __global__ __launch_bounds__(1024) void join_fwd_kernel(JoinArgs a, JoinShape p)
 template <typename E, typename R, int VEC, int NV>
 __global__ __launch_bounds__(1024) void join_bwd_kernel(JoinArgs a, JoinShape p) {
   extern __shared__ float lds[];
-  float* red = lds;  // 16 * NV floats, then blockDim.x * VEC for the sums over the rows
+  float* red = lds;  // 16 * NV floats, then RPB rows for the sums over rows and heads
   const int D = a.H * a.d;
   const int lane = threadIdx.x % p.TPR, sub = threadIdx.x / p.TPR;
   const long rows = (long)a.B * a.T;
@@ -318,49 +318,60 @@ __global__ __launch_bounds__(1024) void join_bwd_kernel(JoinArgs a, JoinShape p)
     }
   }
   if (!a.partial) return;
-  float* rowsum = lds + 16 * NV;
+  // the workgroup's sums, through LDS where several rows (and for w_post heads) add up
+  float* sums = lds + 16 * NV;  // [RPB][D]
 #pragma unroll
   for (int which = 0; which < 3; ++which) {
     if (!(which == 0 ? (void*)a.dw_pre : which == 1 ? (void*)a.dscale : (void*)a.dw_post)) continue;
+    const int cols = which == 2 ? a.d : D, terms = which == 2 ? p.RPB * a.H : p.RPB;
+    float* to = a.partial + ((long)blockIdx.x * 3 + which) * D;
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      float* acc = which == 0 ? spre[j] : which == 1 ? sscale[j] : spost[j];
-      if (p.RPB > 1) {
-        __syncthreads();
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) rowsum[threadIdx.x * VEC + v] = acc[v];
-        __syncthreads();
-        if (sub == 0)
-          for (int r = 1; r < p.RPB; ++r)
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) acc[v] += rowsum[(r * p.TPR + lane) * VEC + v];
-      }
-      if (sub == 0 && in[j] >= 0) {
-        float* to = a.partial + ((long)blockIdx.x * 3 + which) * D + at[j];
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) to[v] = acc[v];
-      }
+      if (in[j] < 0) continue;
+      const float* acc = which == 0 ? spre[j] : which == 1 ? sscale[j] : spost[j];
+      store_row<float, VEC>((terms > 1 ? sums + sub * D : to) + at[j], *(const float(*)[VEC])acc);
+    }
+    if (terms == 1) continue;
+    __syncthreads();
+    for (int c = threadIdx.x; c < cols; c += blockDim.x) {
+      float v = 0.f;
+      for (int i = 0; i < terms; ++i) v += sums[i * cols + c];
+      to[c] = v;
     }
   }
 }
 
 // The weights' gradients from the workgroups' partial sums, each added up in one order whatever
-// the timing.  256 lanes: 64 columns, 4 runs of the G partial rows each.  dw_post adds the heads'
-// columns too.
-__global__ __launch_bounds__(256) void join_sum_kernel(JoinArgs a, int G) {
+// the timing.  A workgroup has 64 columns of one gradient; each of its 16 waves adds every 16th
+// of the G partial rows, 8 loads in flight.
+__global__ __launch_bounds__(1024) void join_sum_kernel(JoinArgs a, int G) {
   const int D = a.H * a.d, which = blockIdx.y;
   float* out = which == 0 ? a.dw_pre : which == 1 ? a.dscale : a.dw_post;
-  if (!out) return;
-  const int cols = which == 2 ? a.d : D, heads = which == 2 ? a.H : 1;
-  const int c = blockIdx.x * 64 + (threadIdx.x & 63), part = threadIdx.x >> 6;
-  __shared__ float red[4][64];
+  const int cols = which == 2 ? a.d : D;
+  const int lane = threadIdx.x & 63, c = blockIdx.x * 64 + lane, part = threadIdx.x >> 6;
+  if (!out || (int)blockIdx.x * 64 >= cols) return;
+  __shared__ float red[16][64];
   float s = 0.f;
-  if (c < cols)
-    for (int g = part; g < G; g += 4)
-      for (int h = 0; h < heads; ++h) s += a.partial[((long)g * 3 + which) * D + h * a.d + c];
-  red[part][threadIdx.x & 63] = s;
+  const float* from = a.partial + (long)which * D + c;
+  if (c < cols) {
+    int g = part;
+    for (; g + 7 * 16 < G; g += 8 * 16) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = from[(long)(g + 16 * i) * 3 * D];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i];
+    }
+    for (; g < G; g += 16) s += from[(long)g * 3 * D];
+  }
+  red[part][lane] = s;
   __syncthreads();
-  if (part == 0 && c < cols) out[c] = (red[0][c & 63] + red[1][c & 63]) + (red[2][c & 63] + red[3][c & 63]);
+  if (part == 0 && c < cols) {
+#pragma unroll
+    for (int i = 1; i < 16; ++i) s += red[i][lane];
+    out[c] = s;
+  }
 }
 
 static bool rows_aligned(const void* p, const Strides& s, int bytes) {
@@ -402,9 +413,9 @@ static void join_run(const JoinArgs& a, const JoinShape& p, hipStream_t s) {
     join_fwd_kernel<E, R, VEC, NV><<<(unsigned)(n < 4096 ? n : 4096), threads, 0, s>>>(a, p);
   } else {
     const int G = join_groups(rows, p.RPB);
-    const size_t lds = (16 * NV + (p.RPB > 1 ? threads * VEC : 0)) * sizeof(float);
+    const size_t lds = (16 * NV + (a.partial && (p.RPB > 1 || a.dw_post) ? p.RPB * a.H * a.d : 0)) * sizeof(float);
     join_bwd_kernel<E, R, VEC, NV><<<G, threads, lds, s>>>(a, p);
-    if (a.partial) join_sum_kernel<<<dim3((a.H * a.d + 63) / 64, 3), 256, 0, s>>>(a, G);
+    if (a.partial) join_sum_kernel<<<dim3((a.H * a.d + 63) / 64, 3), 1024, 0, s>>>(a, G);
   }
 }
 
