@@ -15,7 +15,8 @@
 namespace gla {
 
 struct JoinShape {
-  int VEC, LPH, slots, TPR, NV, RPB;  // RPB rows per workgroup of TPR * RPB lanes
+  int LPH, slots, TPR, NV, RPB;  // RPB rows per workgroup of TPR * RPB lanes
+  float inv_d, inv_D;
 };
 
 static int pow2_up(int n) {
@@ -24,16 +25,18 @@ static int pow2_up(int n) {
   return p;
 }
 
-static JoinShape join_shape(int H, int d, int vec) {
+// threads: of a workgroup, where a row takes fewer.
+static JoinShape join_shape(int H, int d, int vec, int threads) {
   JoinShape s;
-  s.VEC = vec;
   const int n = (d + vec - 1) / vec;
   s.LPH = n <= 64 ? pow2_up(n) : (n + 63) / 64 * 64;
   s.slots = H * s.LPH;
   s.TPR = pow2_up(s.slots);
   if (s.TPR > 1024) s.TPR = 1024;
   s.NV = pow2_up((s.slots + s.TPR - 1) / s.TPR);
-  s.RPB = s.TPR >= 256 ? 1 : 256 / s.TPR;
+  s.RPB = s.TPR >= threads ? 1 : threads / s.TPR;
+  s.inv_d = 1.f / d;
+  s.inv_D = 1.f / (H * d);
   return s;
 }
 
@@ -43,12 +46,13 @@ __device__ __forceinline__ float lane_sum(float v, int width) {
   return v;
 }
 
-// The sum of a row's slots in every lane of the row.  red: 16 floats of LDS; every lane of the
-// workgroup calls it.
-__device__ __forceinline__ float row_sum(float v, int TPR, float* red) {
+// The sum of a row's slots in every lane of the row.  red: 2 x 16 floats of LDS, used in turn
+// (`turn` 0, 1, 0, ..), so that one barrier a call is enough: who writes a half again has passed
+// the barrier of the call between, behind every read of it.  Every lane of the workgroup calls it.
+__device__ __forceinline__ float row_sum(float v, int TPR, float* red, int turn) {
   if (TPR <= 64) return lane_sum(v, TPR);
   v = lane_sum(v, 64);
-  __syncthreads();
+  red += turn * 16;
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
   const int w = TPR / 64, first = (threadIdx.x >> 6) / w * w;
@@ -57,15 +61,15 @@ __device__ __forceinline__ float row_sum(float v, int TPR, float* red) {
   return s;
 }
 
-// Every slot's head sum, in place.  red: NV * 16 floats of LDS, red[j * 16 + wave] a wave's sum.
+// Every slot's head sum, in place.  red: 2 x NV * 16 floats of LDS, in turn as above.
 template <int NV>
-__device__ __forceinline__ void head_sums(float (&v)[NV], const JoinShape& p, int lane, float* red) {
+__device__ __forceinline__ void head_sums(float (&v)[NV], const JoinShape& p, int lane, float* red, int turn) {
   if (p.LPH <= 64) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) v[j] = lane_sum(v[j], p.LPH);
     return;
   }
-  __syncthreads();
+  red += turn * 16 * NV;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const float s = lane_sum(v[j], 64);
@@ -83,102 +87,153 @@ __device__ __forceinline__ void head_sums(float (&v)[NV], const JoinShape& p, in
   }
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + __expf(-z)); }
+__device__ __forceinline__ float sigmoid(float z) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896340736f));
+}
 
-// act(z) and its slope.
-__device__ __forceinline__ void gate(int act, float z, float& f, float& df) {
-  const float s = sigmoid(z);
-  if (act == GLA_ACT_SILU) {
-    f = z * s;
-    df = s * fmaf(z, 1.f - s, 1.f);
-  } else {
-    f = s;
-    df = s * (1.f - s);
+// A lane's slots of a row: the same for every row.
+template <int NV>
+struct Slots {
+  int at[NV], in[NV], head[NV];  // column in the row, column in the head (-1: an empty slot), head
+};
+template <int VEC, int NV>
+__device__ __forceinline__ Slots<NV> row_slots(const JoinArgs& a, const JoinShape& p, int lane) {
+  Slots<NV> r;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int s = lane + j * p.TPR, h = s / p.LPH, i = (s - h * p.LPH) * VEC;
+    r.in[j] = h < a.H && i < a.d ? i : -1;
+    r.at[j] = h * a.d + i;
+    r.head[j] = h;
+  }
+  return r;
+}
+
+// w's values at a lane's slots (`one` where there is no w).
+template <int VEC, int NV>
+__device__ __forceinline__ void load_weights(const float* w, const int (&at)[NV], const int (&in)[NV], float (&v)[NV][VEC]) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[j][i] = 1.f;
+    if (w && in[j] >= 0) load_row<float, VEC>(w + at[j], v[j]);
   }
 }
 
-template <typename E, typename R, int VEC, int NV>
-__global__ __launch_bounds__(1024) void join_fwd_kernel(JoinArgs a, JoinShape p) {
-  __shared__ float red[16 * NV];
-  const int D = a.H * a.d;
-  const int lane = threadIdx.x % p.TPR, sub = threadIdx.x / p.TPR;
-  const long rows = (long)a.B * a.T;
-  for (long row0 = (long)blockIdx.x * p.RPB; row0 < rows; row0 += (long)gridDim.x * p.RPB) {
-    const long row = row0 + sub;
-    const bool live = row < rows;
-    const long b = live ? row / a.T : 0, t = live ? row - b * a.T : 0;
-    float y[NV][VEC], hs[NV];
-    int at[NV], in[NV], head[NV];  // column in the row, in the head (-1: an empty slot), head
+// The row a workgroup's lane group is at: (b, t) stepped without a division.
+struct RowStep {
+  long row;
+  int b, t, db, dt;
+  __device__ RowStep(long first, int T, long step) {
+    row = first;
+    b = (int)(first / T);
+    t = (int)(first - (long)b * T);
+    db = (int)(step / T);
+    dt = (int)(step - (long)db * T);
+  }
+  __device__ void next(int T, long step) {
+    row += step;
+    b += db;
+    t += dt;
+    if (t >= T) {
+      t -= T;
+      ++b;
+    }
+  }
+};
+
+// One row's inputs as they lie in memory (bf16 stays packed), loaded a row ahead of their use.
+template <typename E, typename R, int VEC, int NV, bool BWD>
+struct RowIn {
+  typename Vec<E, VEC>::raw y[NV], z[NV], dn[BWD ? NV : 1];
+  typename Vec<R, VEC>::raw r[NV], dout[BWD ? NV : 1];
+  float ry[BWD ? NV : 1], rp;
+  __device__ __forceinline__ void load(const JoinArgs& a, const Slots<NV>& s, const RowStep& at) {
+    const long b = at.b, t = at.t;
+    if constexpr (BWD) rp = a.d_normed ? a.rstd_pre[at.row] : 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int s = lane + j * p.TPR, h = s / p.LPH, i = (s - h * p.LPH) * VEC;
-      in[j] = live && h < a.H && i < a.d ? i : -1;
-      at[j] = h * a.d + i;
-      head[j] = h;
+      if (s.in[j] < 0) continue;
+      y[j] = *(const typename Vec<E, VEC>::raw*)((const E*)a.y + b * a.ys.b + s.head[j] * a.ys.h + t * a.ys.t + s.in[j]);
+      if (a.z) z[j] = *(const typename Vec<E, VEC>::raw*)((const E*)a.z + b * a.zs.b + t * a.zs.t + s.at[j]);
+      if (a.residual)
+        r[j] = *(const typename Vec<R, VEC>::raw*)((const R*)a.residual + b * a.rs.b + t * a.rs.t + s.at[j]);
+      if constexpr (BWD) {
+        ry[j] = a.w_post ? a.rstd_post[at.row * a.H + s.head[j]] : 1.f;
+        if (a.d_normed)
+          dn[j] = *(const typename Vec<E, VEC>::raw*)((const E*)a.d_normed + b * a.dns.b + t * a.dns.t + s.at[j]);
+        if (a.d_out)
+          dout[j] = *(const typename Vec<R, VEC>::raw*)((const R*)a.d_out + b * a.dos.b + t * a.dos.t + s.at[j]);
+      }
+    }
+  }
+};
+
+template <typename E, typename R, int VEC, int NV, int NT>
+__global__ __launch_bounds__(NT) void join_fwd_kernel(JoinArgs a, JoinShape p) {
+  __shared__ float red[2 * 16], hred[2 * 16 * NV];
+  const int D = a.H * a.d;
+  const int lane = threadIdx.x % p.TPR, sub = threadIdx.x / p.TPR;
+  const long rows = (long)a.B * a.T, step = (long)gridDim.x * p.RPB;
+  const Slots<NV> s = row_slots<VEC, NV>(a, p, lane);
+  float wpost[NV][VEC], scale[NV][VEC], wpre[NV][VEC];
+  load_weights<VEC, NV>(a.w_post, s.in, s.in, wpost);
+  load_weights<VEC, NV>(a.scale, s.at, s.in, scale);
+  load_weights<VEC, NV>(a.w_pre, s.at, s.in, wpre);
+  RowStep at((long)blockIdx.x * p.RPB + sub, a.T, step);
+  RowIn<E, R, VEC, NV, false> in, next;
+  if (at.row < rows) in.load(a, s, at);
+  int turn = 0;
+  for (long row0 = (long)blockIdx.x * p.RPB; row0 < rows; row0 += step, turn ^= 1, in = next) {
+    const RowStep here = at;
+    const bool live = here.row < rows;
+    at.next(a.T, step);
+    if (at.row < rows) next.load(a, s, at);
+    float y[NV][VEC], hs[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
       hs[j] = 0.f;
-      if (in[j] >= 0) {
-        load_row<E, VEC>((const E*)a.y + b * a.ys.b + h * a.ys.h + t * a.ys.t + i, y[j]);
+      const bool have = live && s.in[j] >= 0;
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) hs[j] = fmaf(y[j][v], y[j][v], hs[j]);
-      } else {
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) y[j][v] = 0.f;
+      for (int v = 0; v < VEC; ++v) {
+        y[j][v] = have ? (float)in.y[j][v] : 0.f;
+        hs[j] = fmaf(y[j][v], y[j][v], hs[j]);
       }
     }
     if (a.w_post) {
-      head_sums<NV>(hs, p, lane, red);
+      head_sums<NV>(hs, p, lane, hred, turn);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        if (in[j] < 0) continue;
-        const float r = rsqrtf(hs[j] / a.d + a.eps);
-        if (a.rstd_post && in[j] == 0) a.rstd_post[row * a.H + head[j]] = r;
-        float w[VEC];
-        load_row<float, VEC>(a.w_post + in[j], w);
+        const float r = rsqrtf(hs[j] * p.inv_d + a.eps);
+        if (a.rstd_post && live && s.in[j] == 0) a.rstd_post[here.row * a.H + s.head[j]] = r;
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) y[j][v] *= r * w[v];
+        for (int v = 0; v < VEC; ++v) y[j][v] *= r * wpost[j][v];
       }
     }
     float sq = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (in[j] < 0) continue;
-      if (a.z) {
-        float z[VEC];
-        load_row<E, VEC>((const E*)a.z + b * a.zs.b + t * a.zs.t + at[j], z);
+      if (!live || s.in[j] < 0) continue;
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          float f, df;
-          gate(a.act, z[v], f, df);
-          y[j][v] *= f;
+      for (int v = 0; v < VEC; ++v) {
+        if (a.z) {
+          const float z = (float)in.z[j][v], g = sigmoid(z);
+          y[j][v] *= a.act == GLA_ACT_SILU ? z * g : g;
         }
+        y[j][v] = fmaf(scale[j][v], y[j][v], a.residual ? (float)in.r[j][v] : 0.f);
+        sq = fmaf(y[j][v], y[j][v], sq);
       }
-      if (a.scale) {
-        float w[VEC];
-        load_row<float, VEC>(a.scale + at[j], w);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) y[j][v] *= w[v];
-      }
-      if (a.residual) {
-        float r[VEC];
-        load_row<R, VEC>((const R*)a.residual + b * a.rs.b + t * a.rs.t + at[j], r);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) y[j][v] += r[v];
-      }
-      store_row<R, VEC>((R*)a.out + row * D + at[j], y[j]);
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) sq = fmaf(y[j][v], y[j][v], sq);
+      store_row<R, VEC>((R*)a.out + here.row * D + s.at[j], y[j]);
     }
     if (a.w_pre) {
-      const float r = rsqrtf(row_sum(sq, p.TPR, red) / D + a.eps);
-      if (a.rstd_pre && live && lane == 0) a.rstd_pre[row] = r;
+      const float r = rsqrtf(row_sum(sq, p.TPR, red, turn) * p.inv_D + a.eps);
+      if (a.rstd_pre && live && lane == 0) a.rstd_pre[here.row] = r;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        if (in[j] < 0) continue;
-        float w[VEC];
-        load_row<float, VEC>(a.w_pre + at[j], w);
+        if (!live || s.in[j] < 0) continue;
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) w[v] *= y[j][v] * r;
-        store_row<E, VEC>((E*)a.normed + row * D + at[j], w);
+        for (int v = 0; v < VEC; ++v) y[j][v] *= r * wpre[j][v];
+        store_row<E, VEC>((E*)a.normed + here.row * D + s.at[j], y[j]);
       }
     }
   }
@@ -189,137 +244,98 @@ __global__ __launch_bounds__(1024) void join_fwd_kernel(JoinArgs a, JoinShape p)
 //   dz = dO scale yn w_post act'(z),  du = dO scale act(z),  e' = du w_post
 //   dy = ry (e' - yn mean_d(e' yn))
 // and adds up the weights' gradients dn n, dO m, du yn over its rows in registers, then over the
-// workgroup's RPB rows in LDS; partial: [workgroup][3][D], summed in order by join_sum_kernel.
-template <typename E, typename R, int VEC, int NV>
-__global__ __launch_bounds__(1024) void join_bwd_kernel(JoinArgs a, JoinShape p) {
+// workgroup's RPB rows and for w_post the heads in LDS; partial: [workgroup][3][D], summed in
+// order by join_sum_kernel.
+template <typename E, typename R, int VEC, int NV, int NT>
+__global__ __launch_bounds__(NT) void join_bwd_kernel(JoinArgs a, JoinShape p) {
   extern __shared__ float lds[];
-  float* red = lds;  // 16 * NV floats, then RPB rows for the sums over rows and heads
+  float *red = lds, *hred = lds + 32;  // 2 x 16, 2 x 16 NV floats, then RPB rows for the last sums
   const int D = a.H * a.d;
   const int lane = threadIdx.x % p.TPR, sub = threadIdx.x / p.TPR;
-  const long rows = (long)a.B * a.T;
+  const long rows = (long)a.B * a.T, step = (long)gridDim.x * p.RPB;
+  const Slots<NV> s = row_slots<VEC, NV>(a, p, lane);
+  float wpost[NV][VEC], scale[NV][VEC], wpre[NV][VEC];
+  load_weights<VEC, NV>(a.w_post, s.in, s.in, wpost);
+  load_weights<VEC, NV>(a.scale, s.at, s.in, scale);
+  load_weights<VEC, NV>(a.w_pre, s.at, s.in, wpre);
   float spre[NV][VEC] = {}, sscale[NV][VEC] = {}, spost[NV][VEC] = {};
-  int at[NV], in[NV], head[NV];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int s = lane + j * p.TPR, h = s / p.LPH, i = (s - h * p.LPH) * VEC;
-    in[j] = h < a.H && i < a.d ? i : -1;
-    at[j] = h * a.d + i;
-    head[j] = h;
-  }
-  for (long row0 = (long)blockIdx.x * p.RPB; row0 < rows; row0 += (long)gridDim.x * p.RPB) {
-    const long row = row0 + sub;
-    const bool live = row < rows;
-    const long b = live ? row / a.T : 0, t = live ? row - b * a.T : 0;
-    float yn[NV][VEC], f[NV][VEC], m[NV][VEC], out[NV][VEC], dn[NV][VEC], ry[NV], rp = 0.f;
+  RowStep at((long)blockIdx.x * p.RPB + sub, a.T, step);
+  RowIn<E, R, VEC, NV, true> in, next;
+  if (at.row < rows) in.load(a, s, at);
+  int turn = 0;
+  for (long row0 = (long)blockIdx.x * p.RPB; row0 < rows; row0 += step, turn ^= 1, in = next) {
+    const RowStep here = at;
+    const bool live = here.row < rows;
+    at.next(a.T, step);
+    if (at.row < rows) next.load(a, s, at);
+    float yn[NV][VEC], f[NV][VEC], n[NV][VEC], e[NV][VEC];  // f: sigmoid(z)
     float dot = 0.f;
-    if (a.d_normed && live) rp = a.rstd_pre[row];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      ry[j] = 1.f;
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) yn[j][v] = f[j][v] = m[j][v] = out[j][v] = dn[j][v] = 0.f;
-      if (in[j] < 0 || !live) continue;
-      load_row<E, VEC>((const E*)a.y + b * a.ys.b + head[j] * a.ys.h + t * a.ys.t + in[j], yn[j]);
-      float w[VEC];
-      if (a.w_post) {
-        ry[j] = a.rstd_post[row * a.H + head[j]];
-        load_row<float, VEC>(a.w_post + in[j], w);
-      }
+      const bool have = live && s.in[j] >= 0;
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
-        yn[j][v] *= ry[j];
-        m[j][v] = a.w_post ? yn[j][v] * w[v] : yn[j][v];
-        f[j][v] = 1.f;
-      }
-      if (a.z) {
-        float z[VEC];
-        load_row<E, VEC>((const E*)a.z + b * a.zs.b + t * a.zs.t + at[j], z);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          float df;
-          gate(a.act, z[v], f[j][v], df);
-          m[j][v] *= f[j][v];
-        }
-      }
-      if (a.d_normed) {
-        float sc[VEC];
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) sc[v] = 1.f;
-        if (a.scale) load_row<float, VEC>(a.scale + at[j], sc);
-        if (a.residual) load_row<R, VEC>((const R*)a.residual + b * a.rs.b + t * a.rs.t + at[j], out[j]);
-        load_row<E, VEC>((const E*)a.d_normed + b * a.dns.b + t * a.dns.t + at[j], dn[j]);
-        load_row<float, VEC>(a.w_pre + at[j], w);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          out[j][v] = fmaf(sc[v], m[j][v], out[j][v]) * rp;  // n
-          spre[j][v] = fmaf(dn[j][v], out[j][v], spre[j][v]);
-          dn[j][v] *= w[v];
-          dot = fmaf(dn[j][v], out[j][v], dot);
+        yn[j][v] = have ? (float)in.y[j][v] * in.ry[j] : 0.f;
+        f[j][v] = a.z && have ? sigmoid((float)in.z[j][v]) : 1.f;
+        n[j][v] = e[j][v] = 0.f;
+        if (a.d_normed && have) {
+          float m = yn[j][v] * wpost[j][v] * f[j][v];
+          if (a.z && a.act == GLA_ACT_SILU) m *= (float)in.z[j][v];
+          n[j][v] = fmaf(scale[j][v], m, a.residual ? (float)in.r[j][v] : 0.f) * in.rp;
+          const float dn = (float)in.dn[j][v];
+          spre[j][v] = fmaf(dn, n[j][v], spre[j][v]);
+          e[j][v] = dn * wpre[j][v];
+          dot = fmaf(e[j][v], n[j][v], dot);
         }
       }
     }
-    if (a.d_normed) dot = row_sum(dot, p.TPR, red) / D;
+    if (a.d_normed) dot = row_sum(dot, p.TPR, red, turn) * p.inv_D;
     float hs[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       hs[j] = 0.f;
-      if (in[j] < 0 || !live) continue;
-      float dO[VEC];
-      if (a.d_out) load_row<R, VEC>((const R*)a.d_out + b * a.dos.b + t * a.dos.t + at[j], dO);
-      else
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) dO[v] = 0.f;
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) dO[v] = fmaf(rp, dn[j][v] - out[j][v] * dot, dO[v]);
-      if (a.d_residual) store_row<R, VEC>((R*)a.d_residual + row * D + at[j], dO);
-      if (a.scale) {
-        float sc[VEC];
-        load_row<float, VEC>(a.scale + at[j], sc);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          sscale[j][v] = fmaf(dO[v], m[j][v], sscale[j][v]);
-          dO[v] *= sc[v];
-        }
-      }
-      float w[VEC];
-      if (a.w_post) load_row<float, VEC>(a.w_post + in[j], w);
-      else
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) w[v] = 1.f;
-      if (a.z) {
-        float z[VEC];
-        load_row<E, VEC>((const E*)a.z + b * a.zs.b + t * a.zs.t + at[j], z);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          float g, dg;
-          gate(a.act, z[v], g, dg);
-          z[v] = dO[v] * yn[j][v] * w[v] * dg;
-        }
-        store_row<E, VEC>((E*)a.dz + row * D + at[j], z);
-      }
+      if (!live || s.in[j] < 0) continue;
+      float dO[VEC], dz[VEC];
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
-        dO[v] *= f[j][v];  // du
-        if (a.w_post) spost[j][v] = fmaf(dO[v], yn[j][v], spost[j][v]);
-        f[j][v] = dO[v] * w[v];
-        hs[j] = fmaf(f[j][v], yn[j][v], hs[j]);
+        dO[v] = a.d_out ? (float)in.dout[j][v] : 0.f;
+        if (a.d_normed) dO[v] = fmaf(in.rp, fmaf(-n[j][v], dot, e[j][v]), dO[v]);
       }
+      if (a.d_residual) store_row<R, VEC>((R*)a.d_residual + here.row * D + s.at[j], dO);
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        const float u = yn[j][v] * wpost[j][v];
+        float act = 1.f, slope = 0.f;
+        if (a.z) {
+          const float z = (float)in.z[j][v], g = f[j][v];
+          act = a.act == GLA_ACT_SILU ? z * g : g;
+          slope = a.act == GLA_ACT_SILU ? g * fmaf(z, 1.f - g, 1.f) : g * (1.f - g);
+        }
+        sscale[j][v] = fmaf(dO[v], u * act, sscale[j][v]);
+        dO[v] *= scale[j][v];
+        dz[v] = dO[v] * u * slope;
+        dO[v] *= act;  // du
+        spost[j][v] = fmaf(dO[v], yn[j][v], spost[j][v]);
+        e[j][v] = dO[v] * wpost[j][v];
+        hs[j] = fmaf(e[j][v], yn[j][v], hs[j]);
+      }
+      if (a.z) store_row<E, VEC>((E*)a.dz + here.row * D + s.at[j], dz);
     }
-    if (a.w_post) head_sums<NV>(hs, p, lane, red);
+    if (a.w_post) head_sums<NV>(hs, p, lane, hred, turn);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (in[j] < 0 || !live) continue;
+      if (!live || s.in[j] < 0) continue;
       if (a.w_post) {
-        const float mean = hs[j] / a.d;
+        const float mean = hs[j] * p.inv_d;
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) f[j][v] = ry[j] * (f[j][v] - yn[j][v] * mean);
+        for (int v = 0; v < VEC; ++v) e[j][v] = in.ry[j] * fmaf(-yn[j][v], mean, e[j][v]);
       }
-      store_row<E, VEC>((E*)a.dy + (((long)b * a.H + head[j]) * a.T + t) * a.d + in[j], f[j]);
+      store_row<E, VEC>((E*)a.dy + (((long)here.b * a.H + s.head[j]) * a.T + here.t) * a.d + s.in[j], e[j]);
     }
   }
   if (!a.partial) return;
   // the workgroup's sums, through LDS where several rows (and for w_post heads) add up
-  float* sums = lds + 16 * NV;  // [RPB][D]
+  float* sums = lds + 32 + 32 * NV;  // [RPB][D]
 #pragma unroll
   for (int which = 0; which < 3; ++which) {
     if (!(which == 0 ? (void*)a.dw_pre : which == 1 ? (void*)a.dscale : (void*)a.dw_post)) continue;
@@ -328,9 +344,9 @@ __global__ __launch_bounds__(1024) void join_bwd_kernel(JoinArgs a, JoinShape p)
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (in[j] < 0) continue;
-      const float* acc = which == 0 ? spre[j] : which == 1 ? sscale[j] : spost[j];
-      store_row<float, VEC>((terms > 1 ? sums + sub * D : to) + at[j], *(const float(*)[VEC])acc);
+      if (s.in[j] < 0) continue;
+      const float(&acc)[VEC] = which == 0 ? spre[j] : which == 1 ? sscale[j] : spost[j];
+      store_row<float, VEC>((terms > 1 ? sums + sub * D : to) + s.at[j], acc);
     }
     if (terms == 1) continue;
     __syncthreads();
@@ -389,61 +405,64 @@ static bool join_wide(const JoinArgs& a) {
          rows_aligned(a.residual, a.rs, 16) && rows_aligned(a.d_out, a.dos, 16) && rows_aligned(a.d_normed, a.dns, 16);
 }
 
-static int join_groups(long long rows, int RPB) {
+// Lanes of a workgroup: 256 forward; 512 backward, where every workgroup leaves a row of partial
+// sums, so that half as many workgroups hold as many waves.
+constexpr int kFwdThreads = 256, kBwdThreads = 512, kBwdGroups = 512, kFwdGroups = 2048;
+
+static int join_groups(long long rows, int RPB, int most) {
   const long long n = (rows + RPB - 1) / RPB;
-  return (int)(n < 512 ? n : 512);
+  return (int)(n < most ? n : most);
 }
 
 size_t join_partial_floats(int B, int H, int T, int d) {
-  const long long rows = (long long)B * T;
   int G = 0;
   for (int vec : {1, 8}) {
-    const int g = join_groups(rows, join_shape(H, d, vec).RPB);
+    const int g = join_groups((long long)B * T, join_shape(H, d, vec, kBwdThreads).RPB, kBwdGroups);
     if (g > G) G = g;
   }
   return (size_t)G * 3 * H * d;
 }
 
-template <typename E, typename R, int VEC, int NV, bool BWD>
-static void join_run(const JoinArgs& a, const JoinShape& p, hipStream_t s) {
+template <typename E, typename R, int VEC, int NV, int NT>
+static void join_run(const JoinArgs& a, const JoinShape& p, bool bwd, hipStream_t s) {
   const long long rows = (long long)a.B * a.T;
   const int threads = p.TPR * p.RPB;
-  if constexpr (!BWD) {
-    const long long n = (rows + p.RPB - 1) / p.RPB;
-    join_fwd_kernel<E, R, VEC, NV><<<(unsigned)(n < 4096 ? n : 4096), threads, 0, s>>>(a, p);
+  if (!bwd) {
+    join_fwd_kernel<E, R, VEC, NV, NT><<<join_groups(rows, p.RPB, kFwdGroups), threads, 0, s>>>(a, p);
   } else {
-    const int G = join_groups(rows, p.RPB);
-    const size_t lds = (16 * NV + (a.partial && (p.RPB > 1 || a.dw_post) ? p.RPB * a.H * a.d : 0)) * sizeof(float);
-    join_bwd_kernel<E, R, VEC, NV><<<G, threads, lds, s>>>(a, p);
+    const int G = join_groups(rows, p.RPB, kBwdGroups);
+    const size_t lds = (32 + 32 * NV + (a.partial && (p.RPB > 1 || a.dw_post) ? p.RPB * a.H * a.d : 0)) * sizeof(float);
+    join_bwd_kernel<E, R, VEC, NV, NT><<<G, threads, lds, s>>>(a, p);
     if (a.partial) join_sum_kernel<<<dim3((a.H * a.d + 63) / 64, 3), 1024, 0, s>>>(a, G);
   }
 }
 
-template <typename E, typename R, bool BWD>
-static void join_vec(const JoinArgs& a, hipStream_t s) {
+template <typename E, typename R>
+static void join_vec(const JoinArgs& a, bool bwd, hipStream_t s) {
+  const int threads = bwd ? kBwdThreads : kFwdThreads;
   if (join_wide(a)) {
-    const JoinShape p = join_shape(a.H, a.d, 8);
-    if (p.NV == 1) join_run<E, R, 8, 1, BWD>(a, p, s);
-    else join_run<E, R, 8, 2, BWD>(a, p, s);
+    const JoinShape p = join_shape(a.H, a.d, 8, threads);
+    if (p.TPR <= 512) join_run<E, R, 8, 1, 512>(a, p, bwd, s);
+    else if (p.NV == 1) join_run<E, R, 8, 1, 1024>(a, p, bwd, s);
+    else join_run<E, R, 8, 2, 1024>(a, p, bwd, s);
   } else {
-    const JoinShape p = join_shape(a.H, a.d, 1);
-    if (p.NV == 1) join_run<E, R, 1, 1, BWD>(a, p, s);
-    else if (p.NV == 2) join_run<E, R, 1, 2, BWD>(a, p, s);
-    else if (p.NV == 4) join_run<E, R, 1, 4, BWD>(a, p, s);
-    else if (p.NV == 8) join_run<E, R, 1, 8, BWD>(a, p, s);
-    else join_run<E, R, 1, 16, BWD>(a, p, s);
+    const JoinShape p = join_shape(a.H, a.d, 1, threads);
+    if (p.NV == 1) join_run<E, R, 1, 1, 1024>(a, p, bwd, s);
+    else if (p.NV == 2) join_run<E, R, 1, 2, 1024>(a, p, bwd, s);
+    else if (p.NV == 4) join_run<E, R, 1, 4, 1024>(a, p, bwd, s);
+    else if (p.NV == 8) join_run<E, R, 1, 8, 1024>(a, p, bwd, s);
+    else join_run<E, R, 1, 16, 1024>(a, p, bwd, s);
   }
 }
 
-template <bool BWD>
-static hipError_t join_launch(const JoinArgs& a, hipStream_t s) {
-  if (a.dtype == GLA_F32) join_vec<float, float, BWD>(a, s);
-  else if (a.stream_dtype == GLA_F32) join_vec<bf16, float, BWD>(a, s);
-  else join_vec<bf16, bf16, BWD>(a, s);
+static hipError_t join_launch(const JoinArgs& a, bool bwd, hipStream_t s) {
+  if (a.dtype == GLA_F32) join_vec<float, float>(a, bwd, s);
+  else if (a.stream_dtype == GLA_F32) join_vec<bf16, float>(a, bwd, s);
+  else join_vec<bf16, bf16>(a, bwd, s);
   return hipGetLastError();
 }
 
-hipError_t launch_join_fwd(const JoinArgs& a, hipStream_t s) { return join_launch<false>(a, s); }
-hipError_t launch_join_bwd(const JoinArgs& a, hipStream_t s) { return join_launch<true>(a, s); }
+hipError_t launch_join_fwd(const JoinArgs& a, hipStream_t s) { return join_launch(a, false, s); }
+hipError_t launch_join_bwd(const JoinArgs& a, hipStream_t s) { return join_launch(a, true, s); }
 
 }  // namespace gla
