@@ -40,9 +40,28 @@ static JoinShape join_shape(int H, int d, int vec, int threads) {
   return s;
 }
 
-// Sum over the lanes of aligned groups of `width` lanes (a power of 2 up to 64).
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+
+// Sum over the lanes of aligned groups of `width` lanes (a power of 2 up to 64), the same in every
+// lane of a group: the neighbour's, the other pair's, the other four's (mirrored: by then four
+// lanes hold one value), the other eight's, then rows of 16 and halves of 32 swapped.  All in the
+// vector unit; lane exchanges through LDS cost a trip there each.
 __device__ __forceinline__ float lane_sum(float v, int width) {
-  for (int o = 1; o < width; o *= 2) v += __shfl_xor(v, o);
+  if (width > 1) v += dpp<0xB1>(v);   // quad_perm 1 0 3 2
+  if (width > 2) v += dpp<0x4E>(v);   // quad_perm 2 3 0 1
+  if (width > 4) v += dpp<0x141>(v);  // row_half_mirror
+  if (width > 8) v += dpp<0x140>(v);  // row_mirror
+  if (width > 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  if (width > 32) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
   return v;
 }
 
@@ -405,9 +424,11 @@ static bool join_wide(const JoinArgs& a) {
          rows_aligned(a.residual, a.rs, 16) && rows_aligned(a.d_out, a.dos, 16) && rows_aligned(a.d_normed, a.dns, 16);
 }
 
-// Lanes of a workgroup: 256 forward; 512 backward, where every workgroup leaves a row of partial
-// sums, so that half as many workgroups hold as many waves.
-constexpr int kFwdThreads = 256, kBwdThreads = 512, kBwdGroups = 512, kFwdGroups = 2048;
+// Lanes of a workgroup (more where a row needs them) and the most workgroups.  Measured on
+// 16k rows of 2048, forward and backward together: backward 512 x 256 lanes 184 us, 256 x 256 238,
+// 384 202, 768 208, 1024 189, 512 x 512 198; on 32k rows of 1024 forward: 1024 x 256 38.2 us,
+// 2048 41.8, 4096 42.9.
+constexpr int kFwdThreads = 256, kBwdThreads = 256, kBwdGroups = 512, kFwdGroups = 1024;
 
 static int join_groups(long long rows, int RPB, int most) {
   const long long n = (rows + RPB - 1) / RPB;

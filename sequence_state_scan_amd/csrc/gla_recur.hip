@@ -23,7 +23,7 @@
 namespace gla {
 
 constexpr int kTw = 16;           // tokens of a wave's run
-constexpr int kLook = 8;          // predecessors' words a look-back step loads at once
+constexpr int kLook = 4;          // predecessors' words a look-back step loads at once
 static_assert(kRecurChunk == 8 * kTw, "a full tile of 8 waves is a chunk");
 
 typedef unsigned long long word;
@@ -49,55 +49,48 @@ __device__ __forceinline__ int seq_len(const RecurArgs& a, int b) {
   return n < 0 ? 0 : n > a.T ? a.T : n;
 }
 
-// The state entering tile `at` of `first` .. (words [tile][stride] at w, for V adjacent channels):
-// `state0` enters tile `first`.  Tiles first .. at - 1 have published or will.
+// The state entering tile `at` (words [tile][stride] at w, for V adjacent channels): `state0`
+// enters tile 0, tiles 0 .. at - 1 have published or will.  It needs one known state among the
+// kLook tiles before; where there is none yet it waits for the oldest of them, which comes first:
+// a state that becomes known so serves kLook tiles at once.
 template <int V>
-__device__ __forceinline__ void look_back(const word* w, long stride, int first, int at, const float (&state0)[V],
-                                          float (&state)[V]) {
+__device__ __forceinline__ void look_back(const word* w, long stride, int at, const float (&state0)[V], float (&state)[V]) {
   word win[kLook][V];
-  int hi = at;  // the window is tiles hi - kLook .. hi - 1
+#pragma unroll
+  for (int i = 0; i < kLook; ++i) {
+    const int p = at - 1 - i;
+#pragma unroll
+    for (int v = 0; v < V; ++v) win[i][v] = p >= 0 ? peek(w + p * stride + v) : pack(-1.f, state0[v]);
+  }
   for (;;) {
-#pragma unroll
-    for (int i = 0; i < kLook; ++i) {
-      const int p = hi - 1 - i;
-#pragma unroll
-      for (int v = 0; v < V; ++v) win[i][v] = p >= first ? peek(w + p * stride + v) : pack(-1.f, state0[v]);
-    }
-    bool known[V], all = true;
+    bool all = true;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      known[v] = false;
+      bool known = false;
 #pragma unroll
-      for (int i = 0; i < kLook; ++i) known[v] |= word_a(win[i][v]) < 0.f;
-      all &= known[v];
+      for (int i = 0; i < kLook; ++i) known |= word_a(win[i][v]) < 0.f;
+      all &= known;
     }
     if (__all(all)) break;
-    hi -= kLook;
+    __builtin_amdgcn_s_sleep(1);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (at >= kLook) win[kLook - 1][v] = peek(w + (at - kLook) * stride + v);
   }
 #pragma unroll
-  for (int v = 0; v < V; ++v) state[v] = 0.f;  // replaced by the first known state below
-  for (;;) {
+  for (int v = 0; v < V; ++v) state[v] = 0.f;  // replaced by the first known state
 #pragma unroll
-    for (int i = kLook - 1; i >= 0; --i) {
-      const int p = hi - 1 - i;
+  for (int i = kLook - 1; i >= 0; --i)
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        word x = win[i][v];
-        while (x == kEmpty) {
-          __builtin_amdgcn_s_sleep(1);
-          x = peek(w + p * stride + v);
-        }
-        const float A = word_a(x), Bv = word_b(x);
-        state[v] = A < 0.f ? Bv : advance(A, state[v], Bv);
+    for (int v = 0; v < V; ++v) {
+      word x = win[i][v];
+      while (x == kEmpty) {
+        __builtin_amdgcn_s_sleep(1);
+        x = peek(w + (at - 1 - i) * stride + v);
       }
+      const float A = word_a(x), Bv = word_b(x);
+      state[v] = A < 0.f ? Bv : advance(A, state[v], Bv);
     }
-    if (hi == at) return;
-    hi += kLook;
-#pragma unroll
-    for (int i = 0; i < kLook; ++i)
-#pragma unroll
-      for (int v = 0; v < V; ++v) win[i][v] = peek(w + (hi - 1 - i) * stride + v);
-  }
 }
 
 // Number of the tile a workgroup serves: its ticket where tiles wait for each other (the counter
@@ -110,46 +103,47 @@ __device__ __forceinline__ unsigned tile_number(unsigned* ticket, unsigned* shar
   return __builtin_amdgcn_readfirstlane(*shared);
 }
 
-template <typename E, int MODE, int V, int NW>
+template <typename E, int MODE, int V, int NW, int TW>
 __global__ __launch_bounds__(64 * NW) void recur_fwd_kernel(RecurArgs a) {
-  constexpr int NC = 64 * V;
+  constexpr int NC = 64 * V, TILE = TW * NW;
   __shared__ float runA[NW][NC], runB[NW][NC], enter[NC];
   __shared__ unsigned num;
   const int ncb = (a.D + NC - 1) / NC;
   const unsigned tile = tile_number(a.ticket, &num);
-  const int cb = tile % ncb, b = tile / ncb % a.B, n = tile / ncb / a.B;  // channel block, sequence, chunk
+  const int cb = tile % ncb, b = tile / ncb % a.B, n = tile / ncb / a.B;  // channel block, sequence, tile of it
   const int nch = (a.T + kRecurChunk - 1) / kRecurChunk;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = cb * NC + lane * V, len = seq_len(a, b);
-  const int t0 = n * kRecurChunk + wave * kTw, left = len - t0;
+  const int t0 = n * TILE + wave * TW, left = len - t0;
   const bool live = c < a.D;
   E* h = (E*)a.h + ((long)b * a.T + t0) * a.D + c;
   float zero[V] = {};
-  if (n * kRecurChunk >= len && n > 0) {  // behind the sequence's end: no tile waits for this one
+  if (n * TILE >= len && n > 0) {  // behind the sequence's end: no tile waits for this one
     if (live) {
-      for (int i = 0; i < kTw && t0 + i < a.T; ++i) store_row<E, V>(h + (long)i * a.D, zero);
-      if (a.chunk_in && wave == 0) store_row<float, V>(a.chunk_in + ((long)b * nch + n) * a.D + c, zero);
+      for (int i = 0; i < TW && t0 + i < a.T; ++i) store_row<E, V>(h + (long)i * a.D, zero);
+      if (a.chunk_in && t0 % kRecurChunk == 0 && t0 < a.T)
+        store_row<float, V>(a.chunk_in + ((long)b * nch + t0 / kRecurChunk) * a.D + c, zero);
     }
     return;
   }
-  typename Vec<E, V>::raw xr[kTw];
-  typename Vec<float, V>::raw gr[kTw];
+  typename Vec<E, V>::raw xr[TW];
+  typename Vec<float, V>::raw gr[TW];
   const E* x = (const E*)a.x + b * a.xs.b + t0 * a.xs.t + c;
   const float* g = a.g + b * a.gs.b + t0 * a.gs.t + c;
 #pragma unroll
-  for (int i = 0; i < kTw; ++i)
+  for (int i = 0; i < TW; ++i)
     if (live && i < left) {
       xr[i] = *(const typename Vec<E, V>::raw*)(x + i * a.xs.t);
       gr[i] = *(const typename Vec<float, V>::raw*)(g + i * a.gs.t);
     }
-  float at[kTw][V], bt[kTw][V], A[V], Bv[V];
+  float at[TW][V], bt[TW][V], A[V], Bv[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     A[v] = 1.f;
     Bv[v] = 0.f;
   }
 #pragma unroll
-  for (int i = 0; i < kTw; ++i)
+  for (int i = 0; i < TW; ++i)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       at[i][v] = 1.f;
@@ -182,10 +176,10 @@ __global__ __launch_bounds__(64 * NW) void recur_fwd_kernel(RecurArgs a) {
     if (live) {
       const long stride = (long)a.B * a.D, col = (long)b * a.D + c;
       if (a.words && n > 0) {
-        if ((n + 1) * kRecurChunk < len)
+        if ((n + 1) * TILE < len)
 #pragma unroll
           for (int v = 0; v < V; ++v) publish(a.words + n * stride + col + v, pack(A[v], Bv[v]));
-        look_back<V>(a.words + col, stride, 0, n, first, in);
+        look_back<V>(a.words + col, stride, n, first, in);
       } else {
 #pragma unroll
         for (int v = 0; v < V; ++v) in[v] = first[v];
@@ -194,11 +188,10 @@ __global__ __launch_bounds__(64 * NW) void recur_fwd_kernel(RecurArgs a) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         out[v] = advance(A[v], in[v], Bv[v]);
-        if (a.words && (n + 1) * kRecurChunk < len) publish(a.words + n * stride + col + v, pack(-1.f, out[v]));
+        if (a.words && (n + 1) * TILE < len) publish(a.words + n * stride + col + v, pack(-1.f, out[v]));
         enter[lane * V + v] = in[v];
       }
-      if (a.chunk_in) store_row<float, V>(a.chunk_in + ((long)b * nch + n) * a.D + c, in);
-      if (a.h_final && (n + 1) * kRecurChunk >= len) store_row<float, V>(a.h_final + col, out);
+      if (a.h_final && (n + 1) * TILE >= len) store_row<float, V>(a.h_final + col, out);
     }
   }
   __syncthreads();
@@ -209,8 +202,10 @@ __global__ __launch_bounds__(64 * NW) void recur_fwd_kernel(RecurArgs a) {
     s[v] = enter[lane * V + v];
     for (int w = 0; w < wave; ++w) s[v] = advance(runA[w][lane * V + v], s[v], runB[w][lane * V + v]);
   }
+  if (a.chunk_in && t0 % kRecurChunk == 0 && t0 < a.T)
+    store_row<float, V>(a.chunk_in + ((long)b * nch + t0 / kRecurChunk) * a.D + c, left > 0 || t0 == 0 ? s : zero);
 #pragma unroll
-  for (int i = 0; i < kTw; ++i) {
+  for (int i = 0; i < TW; ++i) {
 #pragma unroll
     for (int v = 0; v < V; ++v) s[v] = advance(at[i][v], s[v], bt[i][v]);
     if (t0 + i < a.T) store_row<E, V>(h + (long)i * a.D, i < left ? s : zero);
@@ -220,37 +215,37 @@ __global__ __launch_bounds__(64 * NW) void recur_fwd_kernel(RecurArgs a) {
 // The backward: G_t the gradient of the state after token t, u_t = a_t G_t what of it reaches the
 // state before (u = A u + B over a run from its end, with the same A as the forward's), and
 // h_{t-1} rebuilt from the chunk's incoming state.  Tiles go from the end.
-template <typename E, int MODE, int V, int NW>
+template <typename E, int MODE, int V, int NW, int TW>
 __global__ __launch_bounds__(64 * NW) void recur_bwd_kernel(RecurArgs a) {
-  constexpr int NC = 64 * V;
+  constexpr int NC = 64 * V, TILE = TW * NW;
   __shared__ float runA[NW][NC], runH[NW][NC], runU[NW][NC], enter[NC];
   __shared__ unsigned num;
   const int ncb = (a.D + NC - 1) / NC;
   const unsigned tile = tile_number(a.ticket, &num);
-  const int nch = (a.T + kRecurChunk - 1) / kRecurChunk;
-  const int cb = tile % ncb, b = tile / ncb % a.B, n = nch - 1 - (int)(tile / ncb / a.B);
+  const int nch = (a.T + kRecurChunk - 1) / kRecurChunk, tiles = (a.T + TILE - 1) / TILE;
+  const int cb = tile % ncb, b = tile / ncb % a.B, n = tiles - 1 - (int)(tile / ncb / a.B);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = cb * NC + lane * V, len = seq_len(a, b);
-  const int t0 = n * kRecurChunk + wave * kTw, left = len - t0;
+  const int t0 = n * TILE + wave * TW, left = len - t0;
   const bool live = c < a.D;
   E* dx = (E*)a.h + ((long)b * a.T + t0) * a.D + c;
   float* dg = a.dg + ((long)b * a.T + t0) * a.D + c;
   float zero[V] = {};
-  if (n * kRecurChunk >= len && n > 0) {
+  if (n * TILE >= len && n > 0) {
     if (live)
-      for (int i = 0; i < kTw && t0 + i < a.T; ++i) {
+      for (int i = 0; i < TW && t0 + i < a.T; ++i) {
         store_row<E, V>(dx + (long)i * a.D, zero);
         store_row<float, V>(dg + (long)i * a.D, zero);
       }
     return;
   }
-  typename Vec<E, V>::raw xr[kTw], dr[kTw];
-  typename Vec<float, V>::raw gr[kTw];
+  typename Vec<E, V>::raw xr[TW], dr[TW];
+  typename Vec<float, V>::raw gr[TW];
   const E* x = (const E*)a.x + b * a.xs.b + t0 * a.xs.t + c;
   const E* dh = (const E*)a.dh + b * a.dhs.b + t0 * a.dhs.t + c;
   const float* g = a.g + b * a.gs.b + t0 * a.gs.t + c;
 #pragma unroll
-  for (int i = 0; i < kTw; ++i) {
+  for (int i = 0; i < TW; ++i) {
     xr[i] = dr[i] = typename Vec<E, V>::raw{};
     gr[i] = typename Vec<float, V>::raw{};
     if (live && i < left) {
@@ -261,19 +256,19 @@ __global__ __launch_bounds__(64 * NW) void recur_bwd_kernel(RecurArgs a) {
   }
   // tokens behind the end hold zeros: a = exp(0) = 1 and no terms, the map that changes nothing
   // (beta = 1 in the plain mode, of x = 0)
-  float A[V], Hv[V], U[V], hb[kTw][V];
+  float A[V], Hv[V], U[V], hb[TW][V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     A[v] = 1.f;
     Hv[v] = U[v] = 0.f;
 #pragma unroll
-    for (int i = 0; i < kTw; ++i) {
+    for (int i = 0; i < TW; ++i) {
       const float at = decay(gr[i][v]);
       A[v] *= at;
       Hv[v] = advance(at, Hv[v], input_factor<MODE>(gr[i][v], at) * (float)xr[i][v]);
     }
 #pragma unroll
-    for (int i = kTw - 1; i >= 0; --i) {
+    for (int i = TW - 1; i >= 0; --i) {
       const float at = decay(gr[i][v]);
       U[v] = at == 0.f ? 0.f : at * ((float)dr[i][v] + U[v]);
     }
@@ -297,12 +292,12 @@ __global__ __launch_bounds__(64 * NW) void recur_bwd_kernel(RecurArgs a) {
       }
     }
     const long stride = (long)a.B * a.D, col = (long)b * a.D + c;
-    const int end = len > 0 ? (len - 1) / kRecurChunk : 0;  // the sequence's last chunk; words count from it
+    const int end = len > 0 ? (len - 1) / TILE : 0;  // the sequence's last tile; words count from it
     if (a.words && n < end) {
       if (n > 0)
 #pragma unroll
         for (int v = 0; v < V; ++v) publish(a.words + (end - n) * stride + col + v, pack(A[v], U[v]));
-      look_back<V>(a.words + col, stride, 0, end - n, last, in);
+      look_back<V>(a.words + col, stride, end - n, last, in);
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) in[v] = last[v];
@@ -317,12 +312,13 @@ __global__ __launch_bounds__(64 * NW) void recur_bwd_kernel(RecurArgs a) {
     if (a.h_final && n == 0) store_row<float, V>(a.h_final + col, out);
   }
   float s[V] = {}, u[V];
-  if (live) load_row<float, V>(a.chunk_in + ((long)b * nch + n) * a.D + c, s);
+  const int chunk = t0 / kRecurChunk, lead = (chunk * kRecurChunk - n * TILE) / TW;  // its first wave
+  if (live && chunk < nch) load_row<float, V>(a.chunk_in + ((long)b * nch + chunk) * a.D + c, s);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    for (int w = 0; w < wave; ++w) s[v] = advance(runA[w][lane * V + v], s[v], runH[w][lane * V + v]);
+    for (int w = lead; w < wave; ++w) s[v] = advance(runA[w][lane * V + v], s[v], runH[w][lane * V + v]);
 #pragma unroll
-    for (int i = 0; i < kTw; ++i) {
+    for (int i = 0; i < TW; ++i) {
       const float at = decay(gr[i][v]);
       hb[i][v] = s[v];
       s[v] = advance(at, s[v], input_factor<MODE>(gr[i][v], at) * (float)xr[i][v]);
@@ -336,7 +332,7 @@ __global__ __launch_bounds__(64 * NW) void recur_bwd_kernel(RecurArgs a) {
     for (int w = NW - 1; w > wave; --w) u[v] = advance(runA[w][lane * V + v], u[v], runU[w][lane * V + v]);
   }
 #pragma unroll
-  for (int i = kTw - 1; i >= 0; --i) {
+  for (int i = TW - 1; i >= 0; --i) {
     float vx[V], vg[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -380,12 +376,13 @@ static bool recur_pairs(const RecurArgs& a) {
          pairs_aligned(a.h, none, e);
 }
 
-template <typename E, int MODE, int V, int NW>
+template <typename E, int MODE, int V, int NW, int TW>
 static void recur_run(RecurArgs a, bool bwd, hipStream_t s) {
-  const unsigned ncb = (a.D + 64 * V - 1) / (64 * V), nch = (a.T + kRecurChunk - 1) / kRecurChunk;
-  if (nch > 1) {
+  const int TILE = NW * TW;
+  const unsigned ncb = (a.D + 64 * V - 1) / (64 * V), tiles = (a.T + TILE - 1) / TILE;
+  if (tiles > 1) {
     word* ws = (word*)a.words;
-    const long n = (long)recur_workspace_words(a.B, a.T, a.D);
+    const long n = kTicketWords + (long)tiles * a.B * a.D;
     const long blocks = (n + 1023) / 1024;
     recur_clear_kernel<<<(unsigned)(blocks < 1024 ? blocks : 1024), 256, 0, s>>>(ws, n);
     a.ticket = (unsigned*)ws;
@@ -393,23 +390,30 @@ static void recur_run(RecurArgs a, bool bwd, hipStream_t s) {
   } else {
     a.words = nullptr;
   }
-  const unsigned grid = ncb * a.B * nch;
-  if (bwd) recur_bwd_kernel<E, MODE, V, NW><<<grid, 64 * NW, 0, s>>>(a);
-  else recur_fwd_kernel<E, MODE, V, NW><<<grid, 64 * NW, 0, s>>>(a);
+  const unsigned grid = ncb * a.B * tiles;
+  if (bwd) recur_bwd_kernel<E, MODE, V, NW, TW><<<grid, 64 * NW, 0, s>>>(a);
+  else recur_fwd_kernel<E, MODE, V, NW, TW><<<grid, 64 * NW, 0, s>>>(a);
 }
 
 template <typename E, int MODE>
 static void recur_shape(const RecurArgs& a, bool bwd, hipStream_t s) {
-  const bool two = recur_pairs(a) && !(bwd && sizeof(E) == 4);
-  if (a.T > 4 * kTw) {
-    if (two) recur_run<E, MODE, 2, 8>(a, bwd, s);
-    else recur_run<E, MODE, 1, 8>(a, bwd, s);
-  } else if (a.T > kTw) {
-    if (two) recur_run<E, MODE, 2, 4>(a, bwd, s);
-    else recur_run<E, MODE, 1, 4>(a, bwd, s);
+  if (bwd) {
+    const bool two = recur_pairs(a) && sizeof(E) == 2;
+    if (a.T > 4 * kTw) {
+      if (two) recur_run<E, MODE, 2, 8, 16>(a, bwd, s);
+      else recur_run<E, MODE, 1, 8, 16>(a, bwd, s);
+    } else if (a.T > kTw) {
+      if (two) recur_run<E, MODE, 2, 4, 16>(a, bwd, s);
+      else recur_run<E, MODE, 1, 4, 16>(a, bwd, s);
+    } else {
+      if (two) recur_run<E, MODE, 2, 1, 16>(a, bwd, s);
+      else recur_run<E, MODE, 1, 1, 16>(a, bwd, s);
+    }
   } else {
-    if (two) recur_run<E, MODE, 2, 1>(a, bwd, s);
-    else recur_run<E, MODE, 1, 1>(a, bwd, s);
+    if (a.T > 128) recur_run<E, MODE, 1, 8, 32>(a, bwd, s);
+    else if (a.T > 64) recur_run<E, MODE, 1, 8, 16>(a, bwd, s);
+    else if (a.T > 16) recur_run<E, MODE, 1, 4, 16>(a, bwd, s);
+    else recur_run<E, MODE, 1, 1, 16>(a, bwd, s);
   }
 }
 
