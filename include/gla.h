@@ -389,7 +389,7 @@ size_t gla_recur_workspace_size(int B, int T, int D);
  * Outputs, fully overwritten: h [B][T][D] (dtype); h_final [B][D] (float32, the state after the
  * last token, h0 for an empty sequence; may be NULL); chunk_in [B][ceil(T/128)][D] (float32, the
  * state entering every GLA_RECUR_CHUNK tokens, for gla_recur_bwd, zero for those behind a sequence's
- * end; may be NULL in a forward-only call).  B <= 65535.  The results do not depend on the timing of the run, bit for bit.
+ * end; may be NULL in a forward-only call). do not depend on the timing of the run, bit for bit.
  * workspace: gla_recur_workspace_size bytes; rules as for gla_chunk_fwd.
  */
 gla_status gla_recur_fwd(const void* x, const gla_strides* x_st, const float* g, const gla_strides* g_st,

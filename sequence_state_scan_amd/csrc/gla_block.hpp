@@ -8,6 +8,8 @@
 namespace gla {
 
 constexpr int kRecurChunk = 128;  // tokens between the states gla_recur_fwd keeps (GLA_RECUR_CHUNK)
+// Token strides and D of the recurrence stay below this, so that 32 tokens span less than 2^31 bytes.
+constexpr int kMaxStride = 1 << 24;
 constexpr int kStepMaxDk = 256;   // key rows a gla_step workgroup can hold
 constexpr int kJoinMaxRow = 8192; // H * d a gla_join row may have
 
@@ -136,17 +138,18 @@ template <int MODE>
 __device__ __forceinline__ float input_factor(float g, float a) {
   if constexpr (MODE == GLA_RECUR_PLAIN) return 1.f;
   if constexpr (MODE == GLA_RECUR_LERP) return one_minus_decay(g, a);
-  return sqrtf(one_minus_decay(2.f * g, a * a));
+  return __builtin_amdgcn_sqrtf(one_minus_decay(2.f * g, a * a));  // the instruction's: one step off at most
 }
 // Its derivative by g (zero where the norm's factor is zero, at g = 0).
 template <int MODE>
 __device__ __forceinline__ float input_factor_slope(float a, float beta) {
   if constexpr (MODE == GLA_RECUR_PLAIN) return 0.f;
   if constexpr (MODE == GLA_RECUR_LERP) return -a;
-  return beta > 0.f ? -a * a / beta : 0.f;
+  return beta > 0.f ? -a * a * __builtin_amdgcn_rcpf(beta) : 0.f;
 }
 
-// a * h + b, where a decay of zero (a reset, or an underflow) drops h whatever it holds.
+// a * h and a * h + b, where a decay of zero (a reset, or an underflow) drops h whatever it holds.
+__device__ __forceinline__ float pass(float a, float h) { return a == 0.f ? 0.f : a * h; }
 __device__ __forceinline__ float advance(float a, float h, float b) { return a == 0.f ? b : fmaf(a, h, b); }
 
 // Slot of row b: the row itself without slots; -1 for a row that is left out (a negative slot);

@@ -3,8 +3,8 @@
 // and its backward, in one pass over the data each (2e + 4 and 3e + 8 bytes per element at e
 // bytes of dtype), bound by HBM.
 //
-// A tile is NW waves of kTw tokens each by 64 V channels; a lane holds its wave's kTw tokens of V
-// channels in registers.  The recurrence over a run of tokens is the map h -> A h + B with A the
+// A tile is NW waves of TW tokens each by 64 channels; a lane holds its wave's TW tokens of a
+// channel in registers.  The recurrence over a run of tokens is the map h -> A h + B with A the
 // product of the a's and B the run's end state from zero.  A lane forms its run's (A, B), the
 // waves' pairs meet in LDS, and a tile's pair goes to the workspace, where the later tiles of the
 // sequence read it: a tile looks back over its predecessors' words to the nearest whose state is
@@ -21,10 +21,6 @@
 #include "gla_block.hpp"
 
 namespace gla {
-
-constexpr int kTw = 16;           // tokens of a wave's run
-constexpr int kLook = 4;          // predecessors' words a look-back step loads at once
-static_assert(kRecurChunk == 8 * kTw, "a full tile of 8 waves is a chunk");
 
 typedef unsigned long long word;
 constexpr word kEmpty = ~0ull;
@@ -49,48 +45,34 @@ __device__ __forceinline__ int seq_len(const RecurArgs& a, int b) {
   return n < 0 ? 0 : n > a.T ? a.T : n;
 }
 
-// The state entering tile `at` (words [tile][stride] at w, for V adjacent channels): `state0`
+// The state entering tile `at` (its channel's words, `stride` apart, from w): `state0`
 // enters tile 0, tiles 0 .. at - 1 have published or will.  It needs one known state among the
-// kLook tiles before; where there is none yet it waits for the oldest of them, which comes first:
-// a state that becomes known so serves kLook tiles at once.
-template <int V>
-__device__ __forceinline__ void look_back(const word* w, long stride, int at, const float (&state0)[V], float (&state)[V]) {
-  word win[kLook][V];
+// LOOK tiles before; where there is none yet it waits for the oldest of them, which comes first:
+// a state that becomes known so serves LOOK tiles at once.
+template <int LOOK>
+__device__ __forceinline__ float look_back(const word* w, long stride, int at, float state0) {
+  word win[LOOK];
 #pragma unroll
-  for (int i = 0; i < kLook; ++i) {
-    const int p = at - 1 - i;
-#pragma unroll
-    for (int v = 0; v < V; ++v) win[i][v] = p >= 0 ? peek(w + p * stride + v) : pack(-1.f, state0[v]);
-  }
+  for (int i = 0; i < LOOK; ++i) win[i] = at - 1 - i >= 0 ? peek(w + (at - 1 - i) * stride) : pack(-1.f, state0);
   for (;;) {
-    bool all = true;
+    bool known = false;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      bool known = false;
-#pragma unroll
-      for (int i = 0; i < kLook; ++i) known |= word_a(win[i][v]) < 0.f;
-      all &= known;
-    }
-    if (__all(all)) break;
+    for (int i = 0; i < LOOK; ++i) known |= word_a(win[i]) < 0.f;
+    if (__all(known)) break;
     __builtin_amdgcn_s_sleep(1);
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (at >= kLook) win[kLook - 1][v] = peek(w + (at - kLook) * stride + v);
+    if (at >= LOOK) win[LOOK - 1] = peek(w + (at - LOOK) * stride);
   }
+  float state = 0.f;  // replaced by the first known one
 #pragma unroll
-  for (int v = 0; v < V; ++v) state[v] = 0.f;  // replaced by the first known state
-#pragma unroll
-  for (int i = kLook - 1; i >= 0; --i)
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      word x = win[i][v];
-      while (x == kEmpty) {
-        __builtin_amdgcn_s_sleep(1);
-        x = peek(w + (at - 1 - i) * stride + v);
-      }
-      const float A = word_a(x), Bv = word_b(x);
-      state[v] = A < 0.f ? Bv : advance(A, state[v], Bv);
+  for (int i = LOOK - 1; i >= 0; --i) {
+    while (win[i] == kEmpty) {
+      __builtin_amdgcn_s_sleep(1);
+      win[i] = peek(w + (at - 1 - i) * stride);
     }
+    const float A = word_a(win[i]), B = word_b(win[i]);
+    state = A < 0.f ? B : advance(A, state, B);
+  }
+  return state;
 }
 
 // Number of the tile a workgroup serves: its ticket where tiles wait for each other (the counter
@@ -103,248 +85,220 @@ __device__ __forceinline__ unsigned tile_number(unsigned* ticket, unsigned* shar
   return __builtin_amdgcn_readfirstlane(*shared);
 }
 
-template <typename E, int MODE, int V, int NW, int TW>
+// A channel's element of token i of a run that starts at `row`, the same in every lane: its address
+// is two scalar registers and one 32-bit offset a lane (kMaxStride keeps the offset inside), so
+// that a run's loads in flight hold few registers.
+template <typename E>
+__device__ __forceinline__ E& element(E* row, unsigned stride, unsigned i, unsigned c) {
+  return *reinterpret_cast<E*>(reinterpret_cast<char*>(row) + (i * stride + c) * (unsigned)sizeof(E));
+}
+
+// A channel's TW tokens; those past the `left` live ones repeat the last (their addresses stay inside).
+template <typename E, int TW>
+__device__ __forceinline__ void load_run(const E* row, long stride, int left, unsigned c, E (&r)[TW]) {
+  E* p = const_cast<E*>(row);
+  if (left >= TW) {
+#pragma unroll
+    for (int i = 0; i < TW; ++i) r[i] = element(p, (unsigned)stride, i, c);
+  } else {
+#pragma unroll
+    for (int i = 0; i < TW; ++i) r[i] = element(p, (unsigned)stride, i < left ? i : left - 1, c);
+  }
+}
+
+template <typename E, int MODE, int NW, int TW, int LOOK>
 __global__ __launch_bounds__(64 * NW) void recur_fwd_kernel(RecurArgs a) {
-  constexpr int NC = 64 * V, TILE = TW * NW;
-  __shared__ float runA[NW][NC], runB[NW][NC], enter[NC];
+  constexpr int TILE = TW * NW;
+  __shared__ float runA[NW][64], runB[NW][64], enter[64];
   __shared__ unsigned num;
-  const int ncb = (a.D + NC - 1) / NC;
+  const int ncb = (a.D + 63) / 64, nch = (a.T + kRecurChunk - 1) / kRecurChunk;
   const unsigned tile = tile_number(a.ticket, &num);
   const int cb = tile % ncb, b = tile / ncb % a.B, n = tile / ncb / a.B;  // channel block, sequence, tile of it
-  const int nch = (a.T + kRecurChunk - 1) / kRecurChunk;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = cb * NC + lane * V, len = seq_len(a, b);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = cb * 64 + lane, len = seq_len(a, b);
   const int t0 = n * TILE + wave * TW, left = len - t0;
   const bool live = c < a.D;
-  E* h = (E*)a.h + ((long)b * a.T + t0) * a.D + c;
-  float zero[V] = {};
+  const unsigned cl = live ? c : 0;  // lanes past the last channel load the first, and store nothing
+  E* h = (E*)a.h + ((long)b * a.T + t0) * a.D;
+  float* chunk_in = a.chunk_in && t0 % kRecurChunk == 0 && t0 < a.T
+                        ? a.chunk_in + ((long)b * nch + t0 / kRecurChunk) * a.D : nullptr;
   if (n * TILE >= len && n > 0) {  // behind the sequence's end: no tile waits for this one
     if (live) {
-      for (int i = 0; i < TW && t0 + i < a.T; ++i) store_row<E, V>(h + (long)i * a.D, zero);
-      if (a.chunk_in && t0 % kRecurChunk == 0 && t0 < a.T)
-        store_row<float, V>(a.chunk_in + ((long)b * nch + t0 / kRecurChunk) * a.D + c, zero);
+      for (int i = 0; i < TW && t0 + i < a.T; ++i) element(h, a.D, i, cl) = (E)0.f;
+      if (chunk_in) chunk_in[cl] = 0.f;
     }
     return;
   }
-  typename Vec<E, V>::raw xr[TW];
-  typename Vec<float, V>::raw gr[TW];
-  const E* x = (const E*)a.x + b * a.xs.b + t0 * a.xs.t + c;
-  const float* g = a.g + b * a.gs.b + t0 * a.gs.t + c;
+  float at[TW], bt[TW];
+  if (left > 0) {
+    E xr[TW];
+    float gr[TW];
+    load_run<float, TW>(a.g + b * a.gs.b + t0 * a.gs.t, a.gs.t, left, cl, gr);
+    load_run<E, TW>((const E*)a.x + b * a.xs.b + t0 * a.xs.t, a.xs.t, left, cl, xr);
 #pragma unroll
-  for (int i = 0; i < TW; ++i)
-    if (live && i < left) {
-      xr[i] = *(const typename Vec<E, V>::raw*)(x + i * a.xs.t);
-      gr[i] = *(const typename Vec<float, V>::raw*)(g + i * a.gs.t);
+    for (int i = 0; i < TW; ++i) {
+      at[i] = decay(gr[i]);
+      bt[i] = input_factor<MODE>(gr[i], at[i]) * (float)xr[i];
     }
-  float at[TW][V], bt[TW][V], A[V], Bv[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    A[v] = 1.f;
-    Bv[v] = 0.f;
   }
+  if (left < TW) {  // tokens behind the end change nothing
 #pragma unroll
-  for (int i = 0; i < TW; ++i)
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      at[i][v] = 1.f;
-      bt[i][v] = 0.f;
-      if (live && i < left) {
-        at[i][v] = decay(gr[i][v]);
-        bt[i][v] = input_factor<MODE>(gr[i][v], at[i][v]) * (float)xr[i][v];
+    for (int i = 0; i < TW; ++i)
+      if (i >= left) {
+        at[i] = 1.f;
+        bt[i] = 0.f;
       }
-      A[v] *= at[i][v];
-      Bv[v] = advance(at[i][v], Bv[v], bt[i][v]);
-    }
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    runA[wave][lane * V + v] = A[v];
-    runB[wave][lane * V + v] = Bv[v];
   }
+  float A = 1.f, B = 0.f;
+#pragma unroll
+  for (int i = 0; i < TW; ++i) {
+    A *= at[i];
+    B = advance(at[i], B, bt[i]);
+  }
+  runA[wave][lane] = A;
+  runB[wave][lane] = B;
   __syncthreads();
-  if (wave == 0) {
-    float in[V], first[V];
+  if (wave == 0 && live) {
+    const long stride = (long)a.B * a.D, col = (long)b * a.D + c;
+    float in = a.h0 ? a.h0[col] : 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) first[v] = a.h0 && live ? a.h0[(long)b * a.D + c + v] : 0.f;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-      for (int w = 1; w < NW; ++w) {
-        const float wa = runA[w][lane * V + v];
-        A[v] *= wa;
-        Bv[v] = advance(wa, Bv[v], runB[w][lane * V + v]);
-      }
-    if (live) {
-      const long stride = (long)a.B * a.D, col = (long)b * a.D + c;
-      if (a.words && n > 0) {
-        if ((n + 1) * TILE < len)
-#pragma unroll
-          for (int v = 0; v < V; ++v) publish(a.words + n * stride + col + v, pack(A[v], Bv[v]));
-        look_back<V>(a.words + col, stride, n, first, in);
-      } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) in[v] = first[v];
-      }
-      float out[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        out[v] = advance(A[v], in[v], Bv[v]);
-        if (a.words && (n + 1) * TILE < len) publish(a.words + n * stride + col + v, pack(-1.f, out[v]));
-        enter[lane * V + v] = in[v];
-      }
-      if (a.h_final && (n + 1) * TILE >= len) store_row<float, V>(a.h_final + col, out);
+    for (int w = 1; w < NW; ++w) {
+      const float wa = runA[w][lane];
+      A *= wa;
+      B = advance(wa, B, runB[w][lane]);
     }
+    const bool wanted = a.words && (n + 1) * TILE < len;  // a later tile of the sequence reads this one's word
+    if (a.words && n > 0) {
+      if (wanted) publish(a.words + n * stride + col, pack(A, B));
+      in = look_back<LOOK>(a.words + col, stride, n, in);
+    }
+    const float out = advance(A, in, B);
+    if (wanted) publish(a.words + n * stride + col, pack(-1.f, out));
+    enter[lane] = in;
+    if (a.h_final && (n + 1) * TILE >= len) a.h_final[col] = out;
   }
   __syncthreads();
   if (!live) return;
-  float s[V];
+  float s = enter[lane];
+  for (int w = 0; w < wave; ++w) s = advance(runA[w][lane], s, runB[w][lane]);
+  if (chunk_in) chunk_in[cl] = left > 0 || t0 == 0 ? s : 0.f;
+  if (left >= TW) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    s[v] = enter[lane * V + v];
-    for (int w = 0; w < wave; ++w) s[v] = advance(runA[w][lane * V + v], s[v], runB[w][lane * V + v]);
-  }
-  if (a.chunk_in && t0 % kRecurChunk == 0 && t0 < a.T)
-    store_row<float, V>(a.chunk_in + ((long)b * nch + t0 / kRecurChunk) * a.D + c, left > 0 || t0 == 0 ? s : zero);
+    for (int i = 0; i < TW; ++i) {
+      s = advance(at[i], s, bt[i]);
+      element(h, a.D, i, cl) = (E)s;
+    }
+  } else {
 #pragma unroll
-  for (int i = 0; i < TW; ++i) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = advance(at[i][v], s[v], bt[i][v]);
-    if (t0 + i < a.T) store_row<E, V>(h + (long)i * a.D, i < left ? s : zero);
+    for (int i = 0; i < TW; ++i) {
+      s = advance(at[i], s, bt[i]);
+      if (t0 + i < a.T) element(h, a.D, i, cl) = (E)(i < left ? s : 0.f);
+    }
   }
 }
 
 // The backward: G_t the gradient of the state after token t, u_t = a_t G_t what of it reaches the
 // state before (u = A u + B over a run from its end, with the same A as the forward's), and
-// h_{t-1} rebuilt from the chunk's incoming state.  Tiles go from the end.
-template <typename E, int MODE, int V, int NW, int TW>
+// h_{t-1} rebuilt from the chunk's incoming state.  Tiles go from the end.  The inputs stay as they
+// were loaded, and a and beta are formed again in each of the three walks: held, they would take
+// the registers of a second workgroup on the CU.
+template <typename E, int MODE, int NW, int TW, int LOOK>
 __global__ __launch_bounds__(64 * NW) void recur_bwd_kernel(RecurArgs a) {
-  constexpr int NC = 64 * V, TILE = TW * NW;
-  __shared__ float runA[NW][NC], runH[NW][NC], runU[NW][NC], enter[NC];
+  constexpr int TILE = TW * NW;
+  __shared__ float runA[NW][64], runH[NW][64], runU[NW][64], enter[64];
   __shared__ unsigned num;
-  const int ncb = (a.D + NC - 1) / NC;
+  const int ncb = (a.D + 63) / 64, nch = (a.T + kRecurChunk - 1) / kRecurChunk, tiles = (a.T + TILE - 1) / TILE;
   const unsigned tile = tile_number(a.ticket, &num);
-  const int nch = (a.T + kRecurChunk - 1) / kRecurChunk, tiles = (a.T + TILE - 1) / TILE;
   const int cb = tile % ncb, b = tile / ncb % a.B, n = tiles - 1 - (int)(tile / ncb / a.B);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = cb * NC + lane * V, len = seq_len(a, b);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = cb * 64 + lane, len = seq_len(a, b);
   const int t0 = n * TILE + wave * TW, left = len - t0;
   const bool live = c < a.D;
-  E* dx = (E*)a.h + ((long)b * a.T + t0) * a.D + c;
-  float* dg = a.dg + ((long)b * a.T + t0) * a.D + c;
-  float zero[V] = {};
+  const unsigned cl = live ? c : 0;
+  E* dx = (E*)a.h + ((long)b * a.T + t0) * a.D;
+  float* dg = a.dg + ((long)b * a.T + t0) * a.D;
   if (n * TILE >= len && n > 0) {
     if (live)
       for (int i = 0; i < TW && t0 + i < a.T; ++i) {
-        store_row<E, V>(dx + (long)i * a.D, zero);
-        store_row<float, V>(dg + (long)i * a.D, zero);
+        element(dx, a.D, i, cl) = (E)0.f;
+        element(dg, a.D, i, cl) = 0.f;
       }
     return;
   }
-  typename Vec<E, V>::raw xr[TW], dr[TW];
-  typename Vec<float, V>::raw gr[TW];
-  const E* x = (const E*)a.x + b * a.xs.b + t0 * a.xs.t + c;
-  const E* dh = (const E*)a.dh + b * a.dhs.b + t0 * a.dhs.t + c;
-  const float* g = a.g + b * a.gs.b + t0 * a.gs.t + c;
+  E xr[TW], dr[TW];
+  float gr[TW], s = 0.f;
+  const int chunk = t0 / kRecurChunk, lead = (chunk * kRecurChunk - n * TILE) / TW;  // its first wave
+  if (left > 0) {
+    load_run<float, TW>(a.g + b * a.gs.b + t0 * a.gs.t, a.gs.t, left, cl, gr);
+    load_run<E, TW>((const E*)a.x + b * a.xs.b + t0 * a.xs.t, a.xs.t, left, cl, xr);
+    load_run<E, TW>((const E*)a.dh + b * a.dhs.b + t0 * a.dhs.t, a.dhs.t, left, cl, dr);
+    s = a.chunk_in[((long)b * nch + chunk) * a.D + cl];
+  }
+  if (left < TW) {
+    // tokens behind the end hold zeros: a = exp(0) = 1 and no terms, the map that changes nothing
+    // (beta = 1 in the plain mode, of x = 0)
+#pragma unroll
+    for (int i = 0; i < TW; ++i)
+      if (i >= left) {
+        xr[i] = dr[i] = (E)0.f;
+        gr[i] = 0.f;
+      }
+  }
+  float A = 1.f, H = 0.f, U = 0.f, before[TW];
 #pragma unroll
   for (int i = 0; i < TW; ++i) {
-    xr[i] = dr[i] = typename Vec<E, V>::raw{};
-    gr[i] = typename Vec<float, V>::raw{};
-    if (live && i < left) {
-      xr[i] = *(const typename Vec<E, V>::raw*)(x + i * a.xs.t);
-      gr[i] = *(const typename Vec<float, V>::raw*)(g + i * a.gs.t);
-      dr[i] = *(const typename Vec<E, V>::raw*)(dh + i * a.dhs.t);
-    }
+    const float at = decay(gr[i]);
+    A *= at;
+    H = advance(at, H, input_factor<MODE>(gr[i], at) * (float)xr[i]);
   }
-  // tokens behind the end hold zeros: a = exp(0) = 1 and no terms, the map that changes nothing
-  // (beta = 1 in the plain mode, of x = 0)
-  float A[V], Hv[V], U[V], hb[TW][V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    A[v] = 1.f;
-    Hv[v] = U[v] = 0.f;
-#pragma unroll
-    for (int i = 0; i < TW; ++i) {
-      const float at = decay(gr[i][v]);
-      A[v] *= at;
-      Hv[v] = advance(at, Hv[v], input_factor<MODE>(gr[i][v], at) * (float)xr[i][v]);
-    }
-#pragma unroll
-    for (int i = TW - 1; i >= 0; --i) {
-      const float at = decay(gr[i][v]);
-      U[v] = at == 0.f ? 0.f : at * ((float)dr[i][v] + U[v]);
-    }
-    runA[wave][lane * V + v] = A[v];
-    runH[wave][lane * V + v] = Hv[v];
-    runU[wave][lane * V + v] = U[v];
-  }
+  for (int i = TW - 1; i >= 0; --i) U = pass(decay(gr[i]), (float)dr[i] + U);
+  runA[wave][lane] = A;
+  runH[wave][lane] = H;
+  runU[wave][lane] = U;
   __syncthreads();
   if (wave == 0 && live) {
-    float in[V], last[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      last[v] = a.dhT ? a.dhT[(long)b * a.D + c + v] : 0.f;
-      A[v] = runA[NW - 1][lane * V + v];
-      U[v] = runU[NW - 1][lane * V + v];
-#pragma unroll
-      for (int w = NW - 2; w >= 0; --w) {
-        const float wa = runA[w][lane * V + v];
-        A[v] *= wa;
-        U[v] = advance(wa, U[v], runU[w][lane * V + v]);
-      }
-    }
     const long stride = (long)a.B * a.D, col = (long)b * a.D + c;
+    float in = a.dhT ? a.dhT[col] : 0.f;
+    A = runA[NW - 1][lane];
+    U = runU[NW - 1][lane];
+#pragma unroll
+    for (int w = NW - 2; w >= 0; --w) {
+      const float wa = runA[w][lane];
+      A *= wa;
+      U = advance(wa, U, runU[w][lane]);
+    }
     const int end = len > 0 ? (len - 1) / TILE : 0;  // the sequence's last tile; words count from it
     if (a.words && n < end) {
-      if (n > 0)
-#pragma unroll
-        for (int v = 0; v < V; ++v) publish(a.words + (end - n) * stride + col + v, pack(A[v], U[v]));
-      look_back<V>(a.words + col, stride, end - n, last, in);
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v) in[v] = last[v];
+      if (n > 0) publish(a.words + (end - n) * stride + col, pack(A, U));
+      in = look_back<LOOK>(a.words + col, stride, end - n, in);
     }
-    float out[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      out[v] = advance(A[v], in[v], U[v]);
-      if (a.words && n > 0) publish(a.words + (end - n) * stride + col + v, pack(-1.f, out[v]));
-      enter[lane * V + v] = in[v];
-    }
-    if (a.h_final && n == 0) store_row<float, V>(a.h_final + col, out);
+    const float out = advance(A, in, U);
+    if (a.words && n > 0) publish(a.words + (end - n) * stride + col, pack(-1.f, out));
+    enter[lane] = in;
+    if (a.h_final && n == 0) a.h_final[col] = out;
   }
-  float s[V] = {}, u[V];
-  const int chunk = t0 / kRecurChunk, lead = (chunk * kRecurChunk - n * TILE) / TW;  // its first wave
-  if (live && chunk < nch) load_row<float, V>(a.chunk_in + ((long)b * nch + chunk) * a.D + c, s);
+  for (int w = lead; w < wave; ++w) s = advance(runA[w][lane], s, runH[w][lane]);
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    for (int w = lead; w < wave; ++w) s[v] = advance(runA[w][lane * V + v], s[v], runH[w][lane * V + v]);
-#pragma unroll
-    for (int i = 0; i < TW; ++i) {
-      const float at = decay(gr[i][v]);
-      hb[i][v] = s[v];
-      s[v] = advance(at, s[v], input_factor<MODE>(gr[i][v], at) * (float)xr[i][v]);
-    }
+  for (int i = 0; i < TW; ++i) {
+    const float at = decay(gr[i]);
+    before[i] = s;
+    s = advance(at, s, input_factor<MODE>(gr[i], at) * (float)xr[i]);
   }
   __syncthreads();
   if (!live) return;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    u[v] = enter[lane * V + v];
-    for (int w = NW - 1; w > wave; --w) u[v] = advance(runA[w][lane * V + v], u[v], runU[w][lane * V + v]);
-  }
+  float u = enter[lane];
+  for (int w = NW - 1; w > wave; --w) u = advance(runA[w][lane], u, runU[w][lane]);
+  const bool full = left >= TW;
 #pragma unroll
   for (int i = TW - 1; i >= 0; --i) {
-    float vx[V], vg[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float at = decay(gr[i][v]), be = input_factor<MODE>(gr[i][v], at), G = (float)dr[i][v] + u[v];
-      u[v] = at == 0.f ? 0.f : at * G;
-      vx[v] = be * G;
-      vg[v] = fmaf(input_factor_slope<MODE>(at, be) * (float)xr[i][v], G, at == 0.f ? 0.f : u[v] * hb[i][v]);
-      if (i >= left) vx[v] = vg[v] = 0.f;
-    }
-    if (t0 + i < a.T) {
-      store_row<E, V>(dx + (long)i * a.D, vx);
-      store_row<float, V>(dg + (long)i * a.D, vg);
+    const float at = decay(gr[i]), be = input_factor<MODE>(gr[i], at), G = (float)dr[i] + u;
+    u = pass(at, G);
+    const float vx = be * G;
+    const float vg = fmaf(input_factor_slope<MODE>(at, be) * (float)xr[i], G, at == 0.f ? 0.f : u * before[i]);
+    if (full || t0 + i < a.T) {
+      element(dx, a.D, i, cl) = (E)(full || i < left ? vx : 0.f);
+      element(dg, a.D, i, cl) = full || i < left ? vg : 0.f;
     }
   }
 }
@@ -355,81 +309,72 @@ __global__ __launch_bounds__(256) void recur_clear_kernel(word* p, long n) {
 }
 
 constexpr size_t kTicketWords = 32;  // the counter's own 256 bytes
+constexpr int kTile = 256;           // tokens of a tile where there are several
 
 size_t recur_workspace_words(int B, int T, int D) {
-  const size_t nch = ((size_t)T + kRecurChunk - 1) / kRecurChunk;
-  return nch > 1 ? kTicketWords + nch * B * D : 0;
+  const size_t tiles = ((size_t)T + kTile - 1) / kTile;
+  return tiles > 1 ? kTicketWords + tiles * B * D : 0;
 }
 
-static bool pairs_aligned(const void* p, const Strides& s, int bytes) {
-  return (uintptr_t)p % (2 * bytes) == 0 && s.b % 2 == 0 && s.t % 2 == 0;
-}
-
-// Two channels a lane where every row allows it, one otherwise.
-static bool recur_pairs(const RecurArgs& a) {
-  const int e = a.dtype == GLA_BF16 ? 2 : 4;
-  const Strides none{0, 0, 0};
-  const void* f32s[] = {a.chunk_in, a.h_final, a.dg};
-  for (const void* p : f32s)
-    if (!pairs_aligned(p, none, 4)) return false;
-  return a.D % 2 == 0 && pairs_aligned(a.x, a.xs, e) && pairs_aligned(a.g, a.gs, 4) && pairs_aligned(a.dh, a.dhs, e) &&
-         pairs_aligned(a.h, none, e);
-}
-
-template <typename E, int MODE, int V, int NW, int TW>
-static void recur_run(RecurArgs a, bool bwd, hipStream_t s) {
-  const int TILE = NW * TW;
-  const unsigned ncb = (a.D + 64 * V - 1) / (64 * V), tiles = (a.T + TILE - 1) / TILE;
+template <bool BWD, typename E, int MODE, int NW, int TW, int LOOK>
+static void recur_run(RecurArgs a, hipStream_t s) {
+  const unsigned ncb = (a.D + 63) / 64, tiles = (a.T + NW * TW - 1) / (NW * TW);
   if (tiles > 1) {
-    word* ws = (word*)a.words;
-    const long n = kTicketWords + (long)tiles * a.B * a.D;
-    const long blocks = (n + 1023) / 1024;
-    recur_clear_kernel<<<(unsigned)(blocks < 1024 ? blocks : 1024), 256, 0, s>>>(ws, n);
+    static_assert(LOOK == 1 || NW * TW == kTile, "the workspace is laid out for tiles of kTile tokens");
+    word* ws = a.words;
+    const long n = (long)recur_workspace_words(a.B, a.T, a.D), blocks = (n + 255) / 256;
+    recur_clear_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(ws, n);
     a.ticket = (unsigned*)ws;
     a.words = ws + kTicketWords;
   } else {
     a.words = nullptr;
   }
   const unsigned grid = ncb * a.B * tiles;
-  if (bwd) recur_bwd_kernel<E, MODE, V, NW, TW><<<grid, 64 * NW, 0, s>>>(a);
-  else recur_fwd_kernel<E, MODE, V, NW, TW><<<grid, 64 * NW, 0, s>>>(a);
+  if constexpr (BWD) recur_bwd_kernel<E, MODE, NW, TW, LOOK><<<grid, 64 * NW, 0, s>>>(a);
+  else recur_fwd_kernel<E, MODE, NW, TW, LOOK><<<grid, 64 * NW, 0, s>>>(a);
 }
 
-template <typename E, int MODE>
-static void recur_shape(const RecurArgs& a, bool bwd, hipStream_t s) {
-  if (bwd) {
-    const bool two = recur_pairs(a) && sizeof(E) == 2;
-    if (a.T > 4 * kTw) {
-      if (two) recur_run<E, MODE, 2, 8, 16>(a, bwd, s);
-      else recur_run<E, MODE, 1, 8, 16>(a, bwd, s);
-    } else if (a.T > kTw) {
-      if (two) recur_run<E, MODE, 2, 4, 16>(a, bwd, s);
-      else recur_run<E, MODE, 1, 4, 16>(a, bwd, s);
-    } else {
-      if (two) recur_run<E, MODE, 2, 1, 16>(a, bwd, s);
-      else recur_run<E, MODE, 1, 1, 16>(a, bwd, s);
-    }
+// The tile and the look back by size.  Up to 128 tokens one tile does, of as many waves as have
+// tokens.  Beyond, a tile is 256 tokens: forward 8 waves of 32, whose 64 loads a lane are in flight
+// at once (4 x 4096 x 2048 bf16 64 us; 128-token tiles of 64 channels 112, of 128 channels 82).
+// With few columns of 64 channels (cols) the tiles of one column wait for each other in a chain of
+// T / (256 LOOK) hops of about 1.5 us each, and a longer look pays; with many the words' reads do
+// not: 65536 x 256 bf16 44 us with 16 waves of 16 and 16 tiles back, 83 with 8 of 32 and 4; 131072
+// x 64 45 with 32 back, 56 with 16; 65536 x 1024 112 with 8 back, 118 with 16 waves and 16, 165 with
+// 32.  Backward 16 waves of 16 everywhere, which leaves a lane's three inputs in its registers: 4 x
+// 4096 x 2048 107 us, 65536 x 256 62 (8 waves of 8 pairs of channels: 119 and 171).
+template <bool BWD, typename E, int MODE>
+static void recur_shape(const RecurArgs& a, hipStream_t s) {
+  const long long cols = (long long)a.B * ((a.D + 63) / 64);
+  if (a.T <= 16) {
+    recur_run<BWD, E, MODE, 1, 16, 1>(a, s);
+  } else if (a.T <= 64) {
+    recur_run<BWD, E, MODE, 4, 16, 1>(a, s);
+  } else if (a.T <= 128) {
+    recur_run<BWD, E, MODE, 8, 16, 1>(a, s);
+  } else if constexpr (!BWD) {
+    if (cols >= 8) recur_run<BWD, E, MODE, 8, 32, 8>(a, s);
+    else if (cols >= 3) recur_run<BWD, E, MODE, 16, 16, 16>(a, s);
+    else recur_run<BWD, E, MODE, 16, 16, 32>(a, s);
   } else {
-    if (a.T > 128) recur_run<E, MODE, 1, 8, 32>(a, bwd, s);
-    else if (a.T > 64) recur_run<E, MODE, 1, 8, 16>(a, bwd, s);
-    else if (a.T > 16) recur_run<E, MODE, 1, 4, 16>(a, bwd, s);
-    else recur_run<E, MODE, 1, 1, 16>(a, bwd, s);
+    if (cols >= 3) recur_run<BWD, E, MODE, 16, 16, 8>(a, s);
+    else recur_run<BWD, E, MODE, 16, 16, 16>(a, s);
   }
 }
 
-template <typename E>
-static hipError_t recur_mode(const RecurArgs& a, bool bwd, hipStream_t s) {
-  if (a.mode == GLA_RECUR_PLAIN) recur_shape<E, GLA_RECUR_PLAIN>(a, bwd, s);
-  else if (a.mode == GLA_RECUR_LERP) recur_shape<E, GLA_RECUR_LERP>(a, bwd, s);
-  else recur_shape<E, GLA_RECUR_NORM>(a, bwd, s);
+template <bool BWD, typename E>
+static hipError_t recur_mode(const RecurArgs& a, hipStream_t s) {
+  if (a.mode == GLA_RECUR_PLAIN) recur_shape<BWD, E, GLA_RECUR_PLAIN>(a, s);
+  else if (a.mode == GLA_RECUR_LERP) recur_shape<BWD, E, GLA_RECUR_LERP>(a, s);
+  else recur_shape<BWD, E, GLA_RECUR_NORM>(a, s);
   return hipGetLastError();
 }
 
 hipError_t launch_recur_fwd(const RecurArgs& a, hipStream_t s) {
-  return a.dtype == GLA_BF16 ? recur_mode<bf16>(a, false, s) : recur_mode<float>(a, false, s);
+  return a.dtype == GLA_BF16 ? recur_mode<false, bf16>(a, s) : recur_mode<false, float>(a, s);
 }
 hipError_t launch_recur_bwd(const RecurArgs& a, hipStream_t s) {
-  return a.dtype == GLA_BF16 ? recur_mode<bf16>(a, true, s) : recur_mode<float>(a, true, s);
+  return a.dtype == GLA_BF16 ? recur_mode<true, bf16>(a, s) : recur_mode<true, float>(a, s);
 }
 
 #define GLA_RECUR_DISPATCH(KERNEL, A, GRID, BLOCK, S)                                              \
