@@ -116,6 +116,21 @@ __device__ __forceinline__ void store_row(E* p, const float (&v)[N]) {
   }
 }
 
+// The same for data that one pass reads or writes once and no cache should keep.
+template <typename E, int N>
+__device__ __forceinline__ void load_stream(const E* p, float (&v)[N]) {
+  const auto r = __builtin_nontemporal_load(reinterpret_cast<const typename Vec<E, N>::raw*>(p));
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = (float)r[i];
+}
+template <typename E, int N>
+__device__ __forceinline__ void store_stream(E* p, const float (&v)[N]) {
+  typename Vec<E, N>::raw r;
+#pragma unroll
+  for (int i = 0; i < N; ++i) r[i] = (E)v[i];
+  __builtin_nontemporal_store(r, reinterpret_cast<typename Vec<E, N>::raw*>(p));
+}
+
 // exp(g) through the hardware's base-2 exponential; exp(-inf) = 0.
 __device__ __forceinline__ float decay(float g) { return __builtin_amdgcn_exp2f(g * 1.44269504088896340736f); }
 
@@ -152,17 +167,19 @@ __device__ __forceinline__ float input_factor_slope(float a, float beta) {
 __device__ __forceinline__ float pass(float a, float h) { return a == 0.f ? 0.f : a * h; }
 __device__ __forceinline__ float advance(float a, float h, float b) { return a == 0.f ? b : fmaf(a, h, b); }
 
-// Slot of row b: the row itself without slots; -1 for a row that is left out (a negative slot);
-// -2 for a slot outside the pool or one that an earlier row of the call names.  Every lane of the
-// wave calls it.
+// Slot of row b: the row itself without slots, -1 for a row that is left out (a negative slot), -2
+// for a slot outside the pool.
 __device__ __forceinline__ int row_slot(const int* slots, int b, int n_slots) {
-  if (!slots) return b;
-  const int s = slots[b];
-  if (s < 0) return -1;
-  if (s >= n_slots) return -2;
+  const int s = slots ? slots[b] : b;
+  return s < 0 ? -1 : s >= n_slots ? -2 : s;
+}
+// Whether an earlier row of the call names row b's slot.  Every lane of the wave calls it; apart from
+// row_slot, so that the row's loads are on their way meanwhile.
+__device__ __forceinline__ bool slot_taken(const int* slots, int b, int slot) {
+  if (!slots || slot < 0) return false;
   bool dup = false;
-  for (int i = threadIdx.x & 63; i < b; i += 64) dup |= slots[i] == s;
-  return __any(dup) ? -2 : s;
+  for (int i = threadIdx.x & 63; i < b; i += 64) dup |= slots[i] == slot;
+  return __any(dup);
 }
 
 }  // namespace gla

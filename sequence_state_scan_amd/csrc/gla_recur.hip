@@ -94,12 +94,13 @@ __device__ __forceinline__ E& element(E* row, unsigned stride, unsigned i, unsig
 }
 
 // A channel's TW tokens; those past the `left` live ones repeat the last (their addresses stay inside).
+// Read once, past the caches (4 x 4096 x 2048 bf16 forward 60.9 us, 63.5 through them; backward 105.7, 107.5).
 template <typename E, int TW>
 __device__ __forceinline__ void load_run(const E* row, long stride, int left, unsigned c, E (&r)[TW]) {
   E* p = const_cast<E*>(row);
   if (left >= TW) {
 #pragma unroll
-    for (int i = 0; i < TW; ++i) r[i] = element(p, (unsigned)stride, i, c);
+    for (int i = 0; i < TW; ++i) r[i] = __builtin_nontemporal_load(&element(p, (unsigned)stride, i, c));
   } else {
 #pragma unroll
     for (int i = 0; i < TW; ++i) r[i] = element(p, (unsigned)stride, i < left ? i : left - 1, c);
@@ -377,40 +378,53 @@ hipError_t launch_recur_bwd(const RecurArgs& a, hipStream_t s) {
   return a.dtype == GLA_BF16 ? recur_mode<true, bf16>(a, s) : recur_mode<true, float>(a, s);
 }
 
-#define GLA_RECUR_DISPATCH(KERNEL, A, GRID, BLOCK, S)                                              \
-  do {                                                                                             \
-    if ((A).dtype == GLA_BF16) {                                                                   \
-      if ((A).mode == GLA_RECUR_PLAIN) KERNEL<bf16, GLA_RECUR_PLAIN><<<GRID, BLOCK, 0, S>>>(A);    \
-      else if ((A).mode == GLA_RECUR_LERP) KERNEL<bf16, GLA_RECUR_LERP><<<GRID, BLOCK, 0, S>>>(A); \
-      else KERNEL<bf16, GLA_RECUR_NORM><<<GRID, BLOCK, 0, S>>>(A);                                 \
-    } else {                                                                                       \
-      if ((A).mode == GLA_RECUR_PLAIN) KERNEL<float, GLA_RECUR_PLAIN><<<GRID, BLOCK, 0, S>>>(A);   \
-      else if ((A).mode == GLA_RECUR_LERP) KERNEL<float, GLA_RECUR_LERP><<<GRID, BLOCK, 0, S>>>(A);\
-      else KERNEL<float, GLA_RECUR_NORM><<<GRID, BLOCK, 0, S>>>(A);                                \
-    }                                                                                              \
-  } while (0)
-
-// One token for each row of a batch, the rows' states in a pool.  Every workgroup (64 channels of
-// one row) looks its slot up and checks it against the earlier rows' by itself.
-template <typename E, int MODE>
+// One token for each row of a batch, the rows' states in a pool.  A wave has 64 V channels of one
+// row; it looks the row's slot up and checks it against the earlier rows' by itself, while its
+// loads are on their way.
+template <typename E, int MODE, int V>
 __global__ __launch_bounds__(64) void recur_step_kernel(RecurStepArgs a) {
-  const int c = blockIdx.x * 64 + threadIdx.x, b = blockIdx.y;
+  const int c = (blockIdx.x * 64 + threadIdx.x) * V, b = blockIdx.y;
+  const bool live = c < a.D;
+  float x[V] = {}, g[V] = {}, st[V] = {};
   const int slot = row_slot(a.slots, b, a.n_slots);
-  if (c >= a.D) return;
-  E* h = (E*)a.h + (long)b * a.D + c;
-  if (slot < 0) {
-    *h = (E)(slot == -1 ? 0.f : __builtin_nanf(""));
-    return;
+  float* state = a.state + (long)slot * a.D + c;
+  if (live) {
+    load_row<float, V>(a.g + b * a.gs.b + c, g);
+    load_row<E, V>((const E*)a.x + b * a.xs.b + c, x);
+    if (slot >= 0) load_row<float, V>(state, st);
   }
-  const float g = a.g[b * a.gs.b + c], at = decay(g);
-  float* st = a.state + (long)slot * a.D + c;
-  const float s = advance(at, *st, input_factor<MODE>(g, at) * (float)((const E*)a.x)[b * a.xs.b + c]);
-  *st = s;
-  *h = (E)s;
+  const bool good = slot >= 0 && !slot_taken(a.slots, b, slot);
+  if (!live) return;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const float at = decay(g[v]);
+    st[v] = advance(at, st[v], input_factor<MODE>(g[v], at) * x[v]);
+    if (!good) st[v] = slot == -1 ? 0.f : __builtin_nanf("");
+  }
+  if (good) store_row<float, V>(state, st);
+  store_row<E, V>((E*)a.h + (long)b * a.D + c, st);
+}
+
+template <typename E, int MODE>
+static void recur_step_run(const RecurStepArgs& a, hipStream_t s) {
+  const int e = sizeof(E);
+  // four channels a lane where the rows allow it: 256 x 4096 bf16 in 5.2 us, 7.6 with one
+  const bool four = a.D % 4 == 0 && a.xs.b % 4 == 0 && a.gs.b % 4 == 0 && (uintptr_t)a.x % (4 * e) == 0 &&
+                    (uintptr_t)a.h % (4 * e) == 0 && (uintptr_t)a.g % 16 == 0 && (uintptr_t)a.state % 16 == 0;
+  if (four) recur_step_kernel<E, MODE, 4><<<dim3((a.D + 255) / 256, a.B), 64, 0, s>>>(a);
+  else recur_step_kernel<E, MODE, 1><<<dim3((a.D + 63) / 64, a.B), 64, 0, s>>>(a);
+}
+
+template <typename E>
+static void recur_step_mode(const RecurStepArgs& a, hipStream_t s) {
+  if (a.mode == GLA_RECUR_PLAIN) recur_step_run<E, GLA_RECUR_PLAIN>(a, s);
+  else if (a.mode == GLA_RECUR_LERP) recur_step_run<E, GLA_RECUR_LERP>(a, s);
+  else recur_step_run<E, GLA_RECUR_NORM>(a, s);
 }
 
 hipError_t launch_recur_step(const RecurStepArgs& a, hipStream_t s) {
-  GLA_RECUR_DISPATCH(recur_step_kernel, a, dim3((a.D + 63) / 64, a.B), dim3(64), s);
+  if (a.dtype == GLA_BF16) recur_step_mode<bf16>(a, s);
+  else recur_step_mode<float>(a, s);
   return hipGetLastError();
 }
 

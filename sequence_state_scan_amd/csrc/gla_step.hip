@@ -6,6 +6,12 @@
 // the 16 x 16 lanes has rows rg + 16 i and VEC adjacent columns, so that a row of the tile is one
 // 256-byte access of 16 lanes.  o sums over the rows: within a lane, over the 4 row groups of a
 // wave by lane exchange, over the 4 waves through LDS.
+// The state goes past the caches: a layer's states come back only a whole model's states later.
+// Measured over enough states of 16 heads of 128 x 128 that none is still cached, us a call: 1 row
+// 5.05 (cached accesses 5.46), 8 rows 5.98 (7.63), 32 rows 13.99 (18.45), 256 rows 96.7 (112.8, 5.6
+// TB/s); where the same states do come back at once, cached accesses win between 32 rows (11.2
+// against 13.1) and 96 (33.5 against 36.8).  Tiles of 128 columns measured the same, of 256 half
+// as slow again.
 #include "gla_block.hpp"
 
 namespace gla {
@@ -21,7 +27,39 @@ __global__ __launch_bounds__(256) void step_kernel(StepArgs a) {
   const bool col = j < a.dv;
   E* o = (E*)a.o + (long)bh * a.n * a.dv + j;
   const int slot = row_slot(a.slots, b, a.n_slots);
-  if (slot < 0) {
+  float* st = a.state + ((long)slot * a.H + h) * a.dk * a.dv + j;
+  const E* q = (const E*)a.q + b * a.qs.b + h * a.qs.h;
+  const E* k = (const E*)a.k + b * a.ks.b + h * a.ks.h;
+  const E* vp = (const E*)a.v + b * a.vs.b + h * a.vs.h + j;
+  const float* g = a.g + b * a.gs.b + h * a.gs.h;
+  // a token's inputs, loaded a token ahead; the first one's with the state, before the slot is checked
+  // against the earlier rows'
+  float vv[VEC], gt[RPT], kt[RPT], qt[RPT];
+  const auto load_token = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const int r = rg + 16 * i;
+      gt[i] = kt[i] = qt[i] = 0.f;  // rows past dk: a decay of 1 and no terms
+      if (r < a.dk) {
+        gt[i] = g[t * a.gs.t + r];
+        kt[i] = (float)k[t * a.ks.t + r];
+        qt[i] = (float)q[t * a.qs.t + r];
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) vv[v] = 0.f;
+    if (col) load_row<E, VEC>(vp + t * a.vs.t, vv);
+  };
+  load_token(0);
+  float S[RPT][VEC];
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const int r = rg + 16 * i;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) S[i][v] = 0.f;
+    if (slot >= 0 && col && r < a.dk) load_stream<float, VEC>(st + (long)r * a.dv, S[i]);
+  }
+  if (slot < 0 || slot_taken(a.slots, b, slot)) {
     float fill[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) fill[v] = slot == -1 ? 0.f : __builtin_nanf("");
@@ -29,53 +67,36 @@ __global__ __launch_bounds__(256) void step_kernel(StepArgs a) {
       for (int t = rg; t < a.n; t += 16) store_row<E, VEC>(o + (long)t * a.dv, fill);
     return;
   }
-  float* st = a.state + ((long)slot * a.H + h) * a.dk * a.dv + j;
-  float S[RPT][VEC];
-#pragma unroll
-  for (int i = 0; i < RPT; ++i) {
-    const int r = rg + 16 * i;
-    if (col && r < a.dk) load_row<float, VEC>(st + (long)r * a.dv, S[i]);
-    else
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) S[i][v] = 0.f;
-  }
-  __shared__ float red[4][TC];
-  const E* q = (const E*)a.q + b * a.qs.b + h * a.qs.h;
-  const E* k = (const E*)a.k + b * a.ks.b + h * a.ks.h;
-  const E* vp = (const E*)a.v + b * a.vs.b + h * a.vs.h + j;
-  const float* g = a.g + b * a.gs.b + h * a.gs.h;
+  __shared__ float red[2][4][TC];
   for (int t = 0; t < a.n; ++t) {
-    float vv[VEC], acc[VEC];
+    float acc[VEC];
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) vv[v] = acc[v] = 0.f;
-    if (col) load_row<E, VEC>(vp + t * a.vs.t, vv);
+    for (int v = 0; v < VEC; ++v) acc[v] = 0.f;
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
-      const int r = rg + 16 * i;
-      if (r < a.dk) {
-        const float at = decay(g[t * a.gs.t + r]), kt = (float)k[t * a.ks.t + r], qt = (float)q[t * a.qs.t + r];
+      const float at = decay(gt[i]);
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          S[i][v] = advance(at, S[i][v], kt * vv[v]);
-          acc[v] = fmaf(qt, S[i][v], acc[v]);
-        }
+      for (int v = 0; v < VEC; ++v) {
+        S[i][v] = advance(at, S[i][v], kt[i] * vv[v]);
+        acc[v] = fmaf(qt[i], S[i][v], acc[v]);
       }
     }
+    if (t + 1 < a.n) load_token(t + 1);
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
       acc[v] += __shfl_xor(acc[v], 16);
       acc[v] += __shfl_xor(acc[v], 32);
     }
-    if (t) __syncthreads();  // the last token's sums are read
+    float(&sums)[4][TC] = red[t & 1];  // in turn: the barrier of the token between is behind every read
     if ((threadIdx.x & 63) < 16)
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) red[wave][cl * VEC + v] = acc[v];
+      for (int v = 0; v < VEC; ++v) sums[wave][cl * VEC + v] = acc[v];
     __syncthreads();
     if (threadIdx.x < 16 && col) {
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
         const int e = cl * VEC + v;
-        acc[v] = (red[0][e] + red[1][e]) + (red[2][e] + red[3][e]);
+        acc[v] = (sums[0][e] + sums[1][e]) + (sums[2][e] + sums[3][e]);
       }
       store_row<E, VEC>(o + (long)t * a.dv, acc);
     }
@@ -84,7 +105,7 @@ __global__ __launch_bounds__(256) void step_kernel(StepArgs a) {
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       const int r = rg + 16 * i;
-      if (r < a.dk) store_row<float, VEC>(st + (long)r * a.dv, S[i]);
+      if (r < a.dk) store_stream<float, VEC>(st + (long)r * a.dv, S[i]);
     }
 }
 

@@ -45,6 +45,8 @@ class GLAError(RuntimeError):
 def load_library(path: str = LIB_PATH):
     """Open libgla.so and declare the C signatures.  Raises if the library is not built."""
     global _lib
+    if _lib is not None and path == LIB_PATH:
+        return _lib
     with _lock:
         if _lib is not None and path == LIB_PATH:
             return _lib
@@ -495,12 +497,8 @@ def _view(t, name, shape, dtype, device):
     checking it as _expect does; strides are None for a contiguous tensor."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if t.shape != shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if t.dtype != dtype:
-        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
-    if t.device != device:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        _expect(t, name, shape, dtype, device)
     if t.is_contiguous():
         return t.data_ptr(), None
     st = t.stride()
@@ -515,8 +513,18 @@ def _out(t, name, shape, dtype, device, optional=False):
     """Pointer of a contiguous tensor (None for an optional one that is not given), checked."""
     if t is None and optional:
         return None
-    _expect(t, name, shape, dtype, device)
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != dtype or t.device != device or \
+            not t.is_contiguous():
+        _expect(t, name, shape, dtype, device)  # says which
     return t.data_ptr()
+
+
+def _new(t, name, shape, dtype, device):
+    """(tensor, pointer) of an output: the caller's, checked, or a new one."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    return t, _out(t, name, shape, dtype, device)
 
 
 def _on_gpu(t, name):
@@ -532,10 +540,19 @@ def _code(table, key, name):
     return table[key]
 
 
+def _raw_stream(index):
+    """hipStream_t of torch's current stream on device ``index``."""
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):  # the same number without the Stream object around it
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _launch(fn, device, *args):
     """The C call on torch's current stream of ``device``, with that device current (a kernel is
     launched on the current one)."""
-    stream = torch.cuda.current_stream(device).cuda_stream
+    stream = _raw_stream(device.index)
     if torch.cuda.current_device() == device.index:
         status = fn(*args, stream)
     else:
@@ -597,19 +614,13 @@ def gla_recur_fwd(x, g, h0=None, lens=None, mode: str = "plain", h=None, chunk_i
     gp, gs = _view(g, "g", (B, T, D), f32, dev)
     h0p = _out(h0, "h0", (B, D), f32, dev, optional=True)
     lp = _out(lens, "lens", (B,), torch.int32, dev, optional=True)
-    if h is None:
-        h = torch.empty((B, T, D), dtype=x.dtype, device=dev)
-    if h_final is None:
-        h_final = torch.empty((B, D), dtype=f32, device=dev)
-    cs_shape = (B, (T + RECUR_CHUNK - 1) // RECUR_CHUNK, D)
-    if not keep_chunk_states:
-        if chunk_in is not None:
-            raise ValueError("chunk_in given with keep_chunk_states=False")
-    elif chunk_in is None:
-        chunk_in = torch.empty(cs_shape, dtype=f32, device=dev)
-    hp = _out(h, "h", (B, T, D), x.dtype, dev)
-    cp = _out(chunk_in, "chunk_in", cs_shape, f32, dev, optional=True)
-    fp = _out(h_final, "h_final", (B, D), f32, dev)
+    h, hp = _new(h, "h", (B, T, D), x.dtype, dev)
+    h_final, fp = _new(h_final, "h_final", (B, D), f32, dev)
+    cp = None
+    if keep_chunk_states:
+        chunk_in, cp = _new(chunk_in, "chunk_in", (B, (T + RECUR_CHUNK - 1) // RECUR_CHUNK, D), f32, dev)
+    elif chunk_in is not None:
+        raise ValueError("chunk_in given with keep_chunk_states=False")
     workspace, wp, wn = _scratch(workspace, recur_workspace_size(B, T, D), dev)
     _launch(load_library().gla_recur_fwd, dev, xp, xs, gp, gs, h0p, lp, hp, cp, fp, B, T, D, m, dt, wp, wn)
     return h, chunk_in, h_final
@@ -629,14 +640,9 @@ def gla_recur_bwd(x, g, dh, chunk_in, lens=None, dhT=None, mode: str = "plain", 
     cp = _out(chunk_in, "chunk_in", (B, (T + RECUR_CHUNK - 1) // RECUR_CHUNK, D), f32, dev)
     lp = _out(lens, "lens", (B,), torch.int32, dev, optional=True)
     tp = _out(dhT, "dhT", (B, D), f32, dev, optional=True)
-    if dx is None:
-        dx = torch.empty((B, T, D), dtype=x.dtype, device=dev)
-    if dg is None:
-        dg = torch.empty((B, T, D), dtype=f32, device=dev)
-    if dh0 is None:
-        dh0 = torch.empty((B, D), dtype=f32, device=dev)
-    dxp, dgp = _out(dx, "dx", (B, T, D), x.dtype, dev), _out(dg, "dg", (B, T, D), f32, dev)
-    d0p = _out(dh0, "dh0", (B, D), f32, dev)
+    dx, dxp = _new(dx, "dx", (B, T, D), x.dtype, dev)
+    dg, dgp = _new(dg, "dg", (B, T, D), f32, dev)
+    dh0, d0p = _new(dh0, "dh0", (B, D), f32, dev)
     workspace, wp, wn = _scratch(workspace, recur_workspace_size(B, T, D), dev)
     _launch(load_library().gla_recur_bwd, dev, xp, xs, gp, gs, dp, ds, cp, lp, tp, dxp, dgp, d0p, B, T, D, m, dt, wp, wn)
     return dx, dg, dh0
@@ -667,9 +673,7 @@ def gla_recur_step(x, g, state, slots=None, mode: str = "plain", h=None):
     xp, xs = _view(x, "x", (B, D), x.dtype, dev)
     gp, gs = _view(g, "g", (B, D), torch.float32, dev)
     sp, ip, n = _pool(state, slots, B, (D,), dev)
-    if h is None:
-        h = torch.empty((B, D), dtype=x.dtype, device=dev)
-    hp = _out(h, "h", (B, D), x.dtype, dev)
+    h, hp = _new(h, "h", (B, D), x.dtype, dev)
     _launch(load_library().gla_recur_step, dev, xp, xs, gp, gs, sp, ip, hp, B, D, n, m, dt)
     return h
 
@@ -690,9 +694,7 @@ def gla_step(q, k, v, g, state, slots=None, o=None):
     vp, vs = _view(v, "v", (B, H, n, dv), q.dtype, dev)
     gp, gs = _view(g, "g", (B, H, n, dk), torch.float32, dev)
     sp, ip, n_slots = _pool(state, slots, B, (H, dk, dv), dev)
-    if o is None:
-        o = torch.empty((B, H, n, dv), dtype=q.dtype, device=dev)
-    op = _out(o, "o", (B, H, n, dv), q.dtype, dev)
+    o, op = _new(o, "o", (B, H, n, dv), q.dtype, dev)
     _launch(load_library().gla_step, dev, qp, qs, kp, ks, vp, vs, gp, gs, sp, ip, op, B, H, n, dk, dv, n_slots, dt)
     return o
 
@@ -731,15 +733,12 @@ def gla_join_fwd(y, z=None, w_post=None, residual=None, scale=None, w_pre=None, 
     gla_join_bwd (None with keep_rstd=False)."""
     (B, H, T, d), st, dt, ptrs = _join_args(y, z, w_post, residual, scale, w_pre)
     dev, D, f32 = y.device, H * d, torch.float32
-    if out is None:
-        out = torch.empty((B, T, D), dtype=st, device=dev)
-    if w_pre is None:
-        if normed is not None:
-            raise ValueError("normed given without w_pre")
-    elif normed is None:
-        normed = torch.empty((B, T, D), dtype=y.dtype, device=dev)
-    op = _out(out, "out", (B, T, D), st, dev)
-    np_ = _out(normed, "normed", (B, T, D), y.dtype, dev, optional=True)
+    out, op = _new(out, "out", (B, T, D), st, dev)
+    np_ = None
+    if w_pre is not None:
+        normed, np_ = _new(normed, "normed", (B, T, D), y.dtype, dev)
+    elif normed is not None:
+        raise ValueError("normed given without w_pre")
     r_post = torch.empty((B, T, H), dtype=f32, device=dev) if keep_rstd and w_post is not None else None
     r_pre = torch.empty((B, T), dtype=f32, device=dev) if keep_rstd and w_pre is not None else None
     _launch(load_library().gla_join_fwd, dev, *ptrs, op, np_, None if r_post is None else r_post.data_ptr(),
