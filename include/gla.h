@@ -383,7 +383,8 @@ size_t gla_recur_workspace_size(int B, int T, int D);
  *   h_t = a_t h_{t-1} + beta(g_t) x_t,   a_t = exp(g_t),   h_{-1} = h0 (NULL = 0)
  * with beta by mode (GLA_RECUR_*).  x [B][T][D] (dtype), g [B][T][D] (float32, finite and <= 0, or
  * -inf: a reset, a token that starts from no state whatever the state held, e.g. the first token
- * of a packed document).  The state is float32.
+ * of a packed document).  The state is float32.  A stretch whose decay underflows to zero drops the
+ * state before it like a reset.
  * lens: int32 [B] or NULL: sequence b has lens[b] tokens (limited to 0..T).  x and g of the tokens
  * behind are ignored whatever they hold; h is zero there.
  * Outputs, fully overwritten: h [B][T][D] (dtype); h_final [B][D] (float32, the state after the

@@ -8,6 +8,7 @@
 namespace gla {
 
 constexpr int kRecurChunk = 128;  // tokens between the states gla_recur_fwd keeps (GLA_RECUR_CHUNK)
+constexpr int kRecurTile = 256;   // tokens of a scan's tile where there are several
 // Token strides and D of the recurrence stay below this, so that 32 tokens span less than 2^31 bytes.
 constexpr int kMaxStride = 1 << 24;
 constexpr int kStepMaxDk = 256;   // key rows a gla_step workgroup can hold

@@ -53,7 +53,7 @@ gla_status check_recur(const char* fn, int B, int T, int D, int mode, int dtype)
     return set_error(GLA_ERR_INVALID_ARG, "%s: unknown mode %d", fn, mode);
   GLA_TRY(check_dtype(fn, dtype));
   const long long tiles = (long long)B * ((D + 63) / 64);
-  if (B > 65535 || D >= gla::kMaxStride || tiles > kMaxGrid || tiles * ((T + gla::kRecurChunk - 1) / gla::kRecurChunk) > kMaxGrid)
+  if (B > 65535 || D >= gla::kMaxStride || tiles > kMaxGrid || tiles * (((long long)T + gla::kRecurTile - 1) / gla::kRecurTile) > kMaxGrid)
     return set_error(GLA_ERR_UNSUPPORTED, "%s: B=%d, T=%d, D=%d are too many for one call", fn, B, T, D);
   return GLA_OK;
 }
@@ -91,7 +91,7 @@ gla_status gla_recur_fwd(const void* x, const gla_strides* x_st, const float* g,
   gla::RecurArgs a{};
   if (!strides(x_st, (long long)T * D, 0, D, &a.xs) || !strides(g_st, (long long)T * D, 0, D, &a.gs))
     return set_error(GLA_ERR_INVALID_ARG, "%s: strides must not be negative", fn);
-  if (a.xs.t >= gla::kMaxStride || a.gs.t >= gla::kMaxStride)
+  if (T > 1 && (a.xs.t >= gla::kMaxStride || a.gs.t >= gla::kMaxStride))
     return set_error(GLA_ERR_UNSUPPORTED, "%s: token strides must be below %d elements", fn, gla::kMaxStride);
   if (aliased<4, 4>({h, chunk_in, h_final, workspace}, {x, g, h0, lens}))
     return set_error(GLA_ERR_INVALID_ARG, "%s: outputs and the workspace must not alias inputs or each other", fn);
@@ -124,7 +124,7 @@ gla_status gla_recur_bwd(const void* x, const gla_strides* x_st, const float* g,
   if (!strides(x_st, (long long)T * D, 0, D, &a.xs) || !strides(g_st, (long long)T * D, 0, D, &a.gs) ||
       !strides(dh_st, (long long)T * D, 0, D, &a.dhs))
     return set_error(GLA_ERR_INVALID_ARG, "%s: strides must not be negative", fn);
-  if (a.xs.t >= gla::kMaxStride || a.gs.t >= gla::kMaxStride || a.dhs.t >= gla::kMaxStride)
+  if (T > 1 && (a.xs.t >= gla::kMaxStride || a.gs.t >= gla::kMaxStride || a.dhs.t >= gla::kMaxStride))
     return set_error(GLA_ERR_UNSUPPORTED, "%s: token strides must be below %d elements", fn, gla::kMaxStride);
   if (aliased<4, 6>({dx, dg, dh0, workspace}, {x, g, dh, chunk_in, lens, dhT}))
     return set_error(GLA_ERR_INVALID_ARG, "%s: outputs and the workspace must not alias inputs or each other", fn);

@@ -417,7 +417,7 @@ static bool rows_aligned(const void* p, const Strides& s, int bytes) {
 // of one element otherwise.
 static bool join_wide(const JoinArgs& a) {
   const Strides none{0, 0, 0};
-  const void* own[] = {a.w_post, a.scale, a.w_pre, a.out, a.normed, a.dy, a.dz, a.d_residual};
+  const void* own[] = {a.w_post, a.scale, a.w_pre, a.out, a.normed, a.dy, a.dz, a.d_residual, a.partial};
   for (const void* q : own)
     if (q && !rows_aligned(q, none, 16)) return false;
   return a.d % 8 == 0 && rows_aligned(a.y, a.ys, 16) && rows_aligned(a.z, a.zs, 16) &&

@@ -49,26 +49,32 @@ __device__ __forceinline__ int seq_len(const RecurArgs& a, int b) {
 // enters tile 0, tiles 0 .. at - 1 have published or will.  It needs one known state among the
 // LOOK tiles before; where there is none yet it waits for the oldest of them, which comes first:
 // a state that becomes known so serves LOOK tiles at once.
+// Every wait ends: after kMaxPolls (seconds, where a wait takes microseconds) it gives up with NaN,
+// as happens where two calls that run at once are handed one workspace against the rules.
+constexpr int kMaxPolls = 1 << 20;
+
 template <int LOOK>
 __device__ __forceinline__ float look_back(const word* w, long stride, int at, float state0) {
   word win[LOOK];
 #pragma unroll
   for (int i = 0; i < LOOK; ++i) win[i] = at - 1 - i >= 0 ? peek(w + (at - 1 - i) * stride) : pack(-1.f, state0);
+  int polls = 0;
   for (;;) {
     bool known = false;
 #pragma unroll
     for (int i = 0; i < LOOK; ++i) known |= word_a(win[i]) < 0.f;
-    if (__all(known)) break;
+    if (__all(known) || ++polls > kMaxPolls) break;
     __builtin_amdgcn_s_sleep(1);
     if (at >= LOOK) win[LOOK - 1] = peek(w + (at - LOOK) * stride);
   }
-  float state = 0.f;  // replaced by the first known one
+  float state = __builtin_nanf("");  // replaced by the first known one
 #pragma unroll
   for (int i = LOOK - 1; i >= 0; --i) {
-    while (win[i] == kEmpty) {
+    while (win[i] == kEmpty && ++polls <= kMaxPolls) {
       __builtin_amdgcn_s_sleep(1);
       win[i] = peek(w + (at - 1 - i) * stride);
     }
+    if (win[i] == kEmpty) win[i] = pack(-1.f, __builtin_nanf(""));
     const float A = word_a(win[i]), B = word_b(win[i]);
     state = A < 0.f ? B : advance(A, state, B);
   }
@@ -218,6 +224,7 @@ __global__ __launch_bounds__(64 * NW) void recur_bwd_kernel(RecurArgs a) {
   const unsigned cl = live ? c : 0;
   E* dx = (E*)a.h + ((long)b * a.T + t0) * a.D;
   float* dg = a.dg + ((long)b * a.T + t0) * a.D;
+  if (n < 0) return;  // a ticket of another call's (a workspace shared against the rules)
   if (n * TILE >= len && n > 0) {
     if (live)
       for (int i = 0; i < TW && t0 + i < a.T; ++i) {
@@ -310,10 +317,9 @@ __global__ __launch_bounds__(256) void recur_clear_kernel(word* p, long n) {
 }
 
 constexpr size_t kTicketWords = 32;  // the counter's own 256 bytes
-constexpr int kTile = 256;           // tokens of a tile where there are several
 
 size_t recur_workspace_words(int B, int T, int D) {
-  const size_t tiles = ((size_t)T + kTile - 1) / kTile;
+  const size_t tiles = ((size_t)T + kRecurTile - 1) / kRecurTile;
   return tiles > 1 ? kTicketWords + tiles * B * D : 0;
 }
 
@@ -321,7 +327,7 @@ template <bool BWD, typename E, int MODE, int NW, int TW, int LOOK>
 static void recur_run(RecurArgs a, hipStream_t s) {
   const unsigned ncb = (a.D + 63) / 64, tiles = (a.T + NW * TW - 1) / (NW * TW);
   if (tiles > 1) {
-    static_assert(LOOK == 1 || NW * TW == kTile, "the workspace is laid out for tiles of kTile tokens");
+    static_assert(LOOK == 1 || NW * TW == kRecurTile, "the workspace is laid out for tiles of that many tokens");
     word* ws = a.words;
     const long n = (long)recur_workspace_words(a.B, a.T, a.D), blocks = (n + 255) / 256;
     recur_clear_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(ws, n);

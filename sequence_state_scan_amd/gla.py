@@ -16,6 +16,7 @@ every chunk).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 import threading
@@ -562,6 +563,7 @@ def _launch(fn, device, *args):
         _check(status)
 
 
+@functools.lru_cache(maxsize=4096)
 def recur_workspace_size(B: int, T: int, D: int) -> int:
     """Bytes of workspace gla_recur_fwd and gla_recur_bwd need (0: none)."""
     lib = load_library()
@@ -571,6 +573,7 @@ def recur_workspace_size(B: int, T: int, D: int) -> int:
     return int(n)
 
 
+@functools.lru_cache(maxsize=4096)
 def join_workspace_size(B: int, H: int, T: int, d: int) -> int:
     """Bytes of workspace gla_join_bwd needs for the weights' gradients."""
     lib = load_library()

@@ -57,7 +57,8 @@ JOIN_BWD = _table(["y", "y_st", "z", "z_st", "w_post", "residual", "r_st", "scal
     (dict(B=0), E), (dict(T=0), E), (dict(D=0), E), (dict(mode=3), E), (dict(mode=-1), E), (dict(dtype=2), E),
     (dict(x=None), E), (dict(g=None), E), (dict(h=None), E), (dict(h=p(0)), E), (dict(chunk_in=p(6)), E),
     (dict(h_final=p(4)), E), (dict(x_st=strides(-1, 0, 64)), E), (dict(g_st=strides(0, 0, -64)), E), (dict(B=70000), UN),
-    (dict(ws=p(0)), E)])
+    (dict(ws=p(0)), E), (dict(ws=None), E), (dict(wsb=16), E), (dict(ws=ctypes.c_void_p(0x300004)), E),
+    (dict(D=1 << 24), UN), (dict(x_st=strides(1 << 30, 0, 1 << 24)), UN), (dict(B=60000, T=1 << 20), UN)])
 def test_recur_fwd_refusals(lib, kw, want):
     assert call(lib.gla_recur_fwd, *RECUR_FWD, **kw) == want
     assert lib.gla_last_error().startswith(b"gla_recur_fwd: ")
@@ -66,7 +67,7 @@ def test_recur_fwd_refusals(lib, kw, want):
 @pytest.mark.parametrize("kw,want", [
     (dict(B=-1), E), (dict(T=0), E), (dict(mode=9), E), (dict(dtype=5), E), (dict(dh=None), E), (dict(chunk_in=None), E),
     (dict(dx=None), E), (dict(dg=None), E), (dict(dx=p(4)), E), (dict(dg=p(9)), E), (dict(dh0=p(8)), E),
-    (dict(dh_st=strides(0, 0, -1)), E)])
+    (dict(dh_st=strides(0, 0, -1)), E), (dict(dh_st=strides(0, 0, 1 << 24)), UN), (dict(ws=None), E), (dict(wsb=16), E)])
 def test_recur_bwd_refusals(lib, kw, want):
     assert call(lib.gla_recur_bwd, *RECUR_BWD, **kw) == want
     assert lib.gla_last_error().startswith(b"gla_recur_bwd: ")

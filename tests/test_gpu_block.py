@@ -480,7 +480,8 @@ def check_join(y, a, d_out, d_normed, act, label, wrap=lambda t: t.cuda()):
 
 JOIN_SIZES = [(1, 1, 1, 1), (2, 1, 3, 64), (1, 4, 5, 256), (2, 3, 33, 50), (1, 1, 7, 2048), (1, 16, 40, 128),
               (3, 2, 9, 7), (1, 2, 300, 129), (1, 1, 4, 8192), (2, 5, 6, 96), (1, 1, 3, 4099), (700, 1, 3, 16),
-              (1, 3, 8, 520), (2, 1, 2, 1000), (1, 8, 11, 1024)]
+              (1, 3, 8, 520), (2, 1, 2, 1000), (1, 8, 11, 1024), (1, 15, 3, 520), (1, 126, 2, 65), (9, 1, 1, 1),
+              (1, 1, 1100, 24)]
 
 
 @pytest.mark.parametrize("dt,st", [(F32, F32), (BF16, BF16), (BF16, F32)])
@@ -615,6 +616,50 @@ def test_a_recurrent_block_as_it_is_used():
     a2 = recur_reference(norm(out), g.double(), zero, lens, "norm")["h"][0]
     assert float((h2.cpu().double() - a2).abs().max()) <= 1e-4
     assert float((f1["out"].cpu().double() - out).abs().max()) <= 1e-4
+
+
+def test_a_served_block_prompt_then_tokens():
+    # a prompt through the chunked chain with its join, then token by token: gla_step on the prompt's final
+    # state, and the join in the residual's place, against float64 of the whole sequence
+    B, H, T, dk, dv, chunk, more = 2, 2, 128, 32, 64, 32, 5
+    d = inputs.generate(B, H, T + more, dk, dv, "bf16", 9)
+    _, a, _, _ = join_inputs(15, B, H, T + more, dv, BF16, F32)
+    x = {n: t.cuda() for n, t in d.items()}
+    rows = {n: t.cuda() for n, t in a.items() if n in ("z", "residual")}
+    w = {n: t.cuda() for n, t in a.items() if n not in rows}
+    part = lambda n, lo, hi: x[n][:, :, lo:hi].contiguous()  # noqa: E731
+    f = gla.states_first_forward(*(part(n, 0, T) for n in "qkvg"), chunk, 1, 1,
+                                 join=dict(w, z=rows["z"][:, :T], residual=rows["residual"][:, :T], eps=EPS))
+    state, outs = f["h_final"], [f["join"]]
+    for t in range(T, T + more):
+        o = gla.gla_step(*(x[n][:, :, t:t + 1] for n in "qkvg"), state)
+        r = rows["residual"][:, t:t + 1].contiguous()
+        outs.append(gla.gla_join_fwd(o, z=rows["z"][:, t:t + 1], residual=r, out=r, eps=EPS, keep_rstd=False, **w))
+    o, _ = oracle.gla_fwd(*(inputs.as_f64(d[n]) for n in "qkvg"))
+    ref = join_reference(torch.from_numpy(o), *(a[n].double() for n in ("z", "w_post", "residual", "scale", "w_pre")),
+                         "silu", None, None)
+    for n in ("out", "normed"):
+        got = torch.cat([j[n] for j in outs], 1).cpu().double()
+        assert float((got - ref[n][0]).norm() / ref[n][0].norm()) <= 4e-2, n
+        tail = got[:, T:] - ref[n][0][:, T:]
+        assert float(tail.norm() / ref[n][0][:, T:].norm()) <= 4e-2, n
+
+
+def test_two_calls_at_once():
+    # scans of several tiles on two streams, each with a workspace of its own
+    x, g, dh, h0, dhT = (t.cuda() for t in recur_inputs(41, 1, 30000, 320, BF16, "weak"))
+    want = gla.gla_recur_fwd(x, g, h0=h0, mode="norm")
+    wantb = gla.gla_recur_bwd(x, g, dh, want[1], dhT=dhT, mode="norm")
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(6):
+        with torch.cuda.stream(streams[i % 3]):
+            f = gla.gla_recur_fwd(x, g, h0=h0, mode="norm")
+            got.append(f + gla.gla_recur_bwd(x, g, dh, f[1], dhT=dhT, mode="norm"))
+    torch.cuda.synchronize()
+    for r in got:
+        assert all(torch.equal(s, t) for s, t in zip(r, want + wantb))
 
 
 def test_other_streams_and_replayed_graphs():
