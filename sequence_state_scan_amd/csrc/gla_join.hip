@@ -4,15 +4,19 @@
 //   m = yn w_post act(z)                     (the gate: silu or sigmoid)
 //   out = residual + scale m
 //   normed = out rsqrt(mean(out^2) + eps) w_pre
-// A row is spread over TPR lanes in slots of VEC elements.  A head takes LPH slots (its last ones
-// are empty where d / VEC is not LPH): a power of 2 up to 64, so that a head's sum is a lane
-// exchange inside an aligned group, or a multiple of 64, so that no wave's slots belong to two
-// heads and a head's sum is a wave sum and a sum of LPH / 64 of them from LDS.  Slot s of a row
+// A row is spread over TPR lanes in slots of 8 elements (16 bytes of bf16; the loads are whole
+// whatever the alignment, which the hardware takes, except a head's last slot where d is no
+// multiple of 8: EVEN kernels know there is none).  A head takes LPH slots (its last ones are empty
+// where d / 8 is not LPH): a power of 2 up to 64, so that a head's sum is a lane exchange inside an
+// aligned group, or a multiple of 64, so that no wave's slots belong to two heads and a head's sum
+// is a wave sum and a sum of LPH / 64 of them from LDS.  Slot s of a row
 // is lane s % TPR, register s / TPR.  All arithmetic is float32, rounded once at the store; the
 // backward recomputes out from y, z and the residual instead of reading its rounded value.
 #include "gla_block.hpp"
 
 namespace gla {
+
+constexpr int VEC = 8;  // elements of a slot
 
 struct JoinShape {
   int LPH, slots, TPR, NV, RPB;  // RPB rows per workgroup of TPR * RPB lanes
@@ -25,14 +29,14 @@ static int pow2_up(int n) {
   return p;
 }
 
-// threads: of a workgroup, where a row takes fewer.
-static JoinShape join_shape(int H, int d, int vec, int threads) {
+// threads: of a workgroup, where a row takes fewer; most: lanes of a row.
+static JoinShape join_shape(int H, int d, int threads, int most) {
   JoinShape s;
-  const int n = (d + vec - 1) / vec;
+  const int n = (d + VEC - 1) / VEC;
   s.LPH = n <= 64 ? pow2_up(n) : (n + 63) / 64 * 64;
   s.slots = H * s.LPH;
   s.TPR = pow2_up(s.slots);
-  if (s.TPR > 1024) s.TPR = 1024;
+  if (s.TPR > most) s.TPR = most;
   s.NV = pow2_up((s.slots + s.TPR - 1) / s.TPR);
   s.RPB = s.TPR >= threads ? 1 : threads / s.TPR;
   s.inv_d = 1.f / d;
@@ -110,12 +114,41 @@ __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896340736f));
 }
 
+// VEC elements at any alignment of the element.
+template <typename E>
+struct Pack {
+  typedef E raw __attribute__((ext_vector_type(VEC), aligned(sizeof(E))));
+};
+
+// The first `left` of a slot's elements (all of them where left >= VEC), the others zero.
+template <bool EVEN, typename E>
+__device__ __forceinline__ typename Pack<E>::raw load_slot(const E* p, int left) {
+  if (EVEN || left >= VEC) return *reinterpret_cast<const typename Pack<E>::raw*>(p);
+  typename Pack<E>::raw r;
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) r[v] = v < left ? p[v] : (E)0.f;
+  return r;
+}
+template <bool EVEN, typename E>
+__device__ __forceinline__ void store_slot(E* p, const float (&v)[VEC], int left) {
+  if (EVEN || left >= VEC) {
+    typename Pack<E>::raw r;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) r[i] = (E)v[i];
+    *reinterpret_cast<typename Pack<E>::raw*>(p) = r;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (i < left) p[i] = (E)v[i];
+  }
+}
+
 // A lane's slots of a row: the same for every row.
 template <int NV>
 struct Slots {
-  int at[NV], in[NV], head[NV];  // column in the row, column in the head (-1: an empty slot), head
+  int at[NV], in[NV], head[NV], left[NV];  // column in the row, in the head (-1: an empty slot), head, elements
 };
-template <int VEC, int NV>
+template <int NV>
 __device__ __forceinline__ Slots<NV> row_slots(const JoinArgs& a, const JoinShape& p, int lane) {
   Slots<NV> r;
 #pragma unroll
@@ -124,18 +157,20 @@ __device__ __forceinline__ Slots<NV> row_slots(const JoinArgs& a, const JoinShap
     r.in[j] = h < a.H && i < a.d ? i : -1;
     r.at[j] = h * a.d + i;
     r.head[j] = h;
+    r.left[j] = a.d - i;
   }
   return r;
 }
 
-// w's values at a lane's slots (`one` where there is no w).
-template <int VEC, int NV>
-__device__ __forceinline__ void load_weights(const float* w, const int (&at)[NV], const int (&in)[NV], float (&v)[NV][VEC]) {
+// w's values at a slot, ones where there is no w.
+template <bool EVEN>
+__device__ __forceinline__ void load_weights(const float* w, int at, int in, int left, float (&v)[VEC]) {
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
+  for (int i = 0; i < VEC; ++i) v[i] = 1.f;
+  if (w && in >= 0) {
+    const auto r = load_slot<EVEN, float>(w + at, left);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) v[j][i] = 1.f;
-    if (w && in[j] >= 0) load_row<float, VEC>(w + at[j], v[j]);
+    for (int i = 0; i < VEC; ++i) v[i] = r[i];
   }
 }
 
@@ -161,11 +196,11 @@ struct RowStep {
   }
 };
 
-// One row's inputs as they lie in memory (bf16 stays packed), loaded a row ahead of their use.
-template <typename E, typename R, int VEC, int NV, bool BWD>
+// One row's inputs as they lie in memory (bf16 stays packed).
+template <typename E, typename R, int NV, bool BWD, bool EVEN>
 struct RowIn {
-  typename Vec<E, VEC>::raw y[NV], z[NV], dn[BWD ? NV : 1];
-  typename Vec<R, VEC>::raw r[NV], dout[BWD ? NV : 1];
+  typename Pack<E>::raw y[NV], z[NV], dn[BWD ? NV : 1];
+  typename Pack<R>::raw r[NV], dout[BWD ? NV : 1];
   float ry[BWD ? NV : 1], rp;
   __device__ __forceinline__ void load(const JoinArgs& a, const Slots<NV>& s, const RowStep& at) {
     const long b = at.b, t = at.t;
@@ -173,41 +208,66 @@ struct RowIn {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (s.in[j] < 0) continue;
-      y[j] = *(const typename Vec<E, VEC>::raw*)((const E*)a.y + b * a.ys.b + s.head[j] * a.ys.h + t * a.ys.t + s.in[j]);
-      if (a.z) z[j] = *(const typename Vec<E, VEC>::raw*)((const E*)a.z + b * a.zs.b + t * a.zs.t + s.at[j]);
-      if (a.residual)
-        r[j] = *(const typename Vec<R, VEC>::raw*)((const R*)a.residual + b * a.rs.b + t * a.rs.t + s.at[j]);
+      const int c = s.at[j], left = s.left[j];
+      y[j] = load_slot<EVEN>((const E*)a.y + b * a.ys.b + s.head[j] * a.ys.h + t * a.ys.t + s.in[j], left);
+      if (a.z) z[j] = load_slot<EVEN>((const E*)a.z + b * a.zs.b + t * a.zs.t + c, left);
+      if (a.residual) r[j] = load_slot<EVEN>((const R*)a.residual + b * a.rs.b + t * a.rs.t + c, left);
       if constexpr (BWD) {
         ry[j] = a.w_post ? a.rstd_post[at.row * a.H + s.head[j]] : 1.f;
-        if (a.d_normed)
-          dn[j] = *(const typename Vec<E, VEC>::raw*)((const E*)a.d_normed + b * a.dns.b + t * a.dns.t + s.at[j]);
-        if (a.d_out)
-          dout[j] = *(const typename Vec<R, VEC>::raw*)((const R*)a.d_out + b * a.dos.b + t * a.dos.t + s.at[j]);
+        if (a.d_normed) dn[j] = load_slot<EVEN>((const E*)a.d_normed + b * a.dns.b + t * a.dns.t + c, left);
+        if (a.d_out) dout[j] = load_slot<EVEN>((const R*)a.d_out + b * a.dos.b + t * a.dos.t + c, left);
       }
     }
   }
 };
 
-template <typename E, typename R, int VEC, int NV, int NT>
+// The weights at a lane's slots and the next row's inputs are held in registers (a row ahead of
+// their use) where a lane has one slot; with more (LEAN) both are loaded when the row comes.
+template <bool LEAN, bool EVEN, int NV>
+struct Weights {
+  float post[LEAN ? 1 : NV][VEC], scale[LEAN ? 1 : NV][VEC], pre[LEAN ? 1 : NV][VEC];
+  __device__ __forceinline__ Weights(const JoinArgs& a, const Slots<NV>& s) {
+    if constexpr (!LEAN)
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        load_weights<EVEN>(a.w_post, s.in[j], s.in[j], s.left[j], post[j]);
+        load_weights<EVEN>(a.scale, s.at[j], s.in[j], s.left[j], scale[j]);
+        load_weights<EVEN>(a.w_pre, s.at[j], s.in[j], s.left[j], pre[j]);
+      }
+  }
+  __device__ __forceinline__ void get(const float* w, const float (&held)[LEAN ? 1 : NV][VEC], int at, int in, int left,
+                                      int j, float (&v)[VEC]) const {
+    if constexpr (LEAN) {
+      load_weights<EVEN>(w, at, in, left, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[i] = held[j][i];
+    }
+  }
+};
+
+template <typename E, typename R, int NV, int NT, bool EVEN>
 __global__ __launch_bounds__(NT) void join_fwd_kernel(JoinArgs a, JoinShape p) {
+  constexpr bool LEAN = NV > 1;
   __shared__ float red[2 * 16], hred[2 * 16 * NV];
   const int D = a.H * a.d;
   const int lane = threadIdx.x % p.TPR, sub = threadIdx.x / p.TPR;
   const long rows = (long)a.B * a.T, step = (long)gridDim.x * p.RPB;
-  const Slots<NV> s = row_slots<VEC, NV>(a, p, lane);
-  float wpost[NV][VEC], scale[NV][VEC], wpre[NV][VEC];
-  load_weights<VEC, NV>(a.w_post, s.in, s.in, wpost);
-  load_weights<VEC, NV>(a.scale, s.at, s.in, scale);
-  load_weights<VEC, NV>(a.w_pre, s.at, s.in, wpre);
+  const Slots<NV> s = row_slots<NV>(a, p, lane);
+  const Weights<LEAN, EVEN, NV> w(a, s);
   RowStep at((long)blockIdx.x * p.RPB + sub, a.T, step);
-  RowIn<E, R, VEC, NV, false> in, next;
-  if (at.row < rows) in.load(a, s, at);
+  RowIn<E, R, NV, false, EVEN> in, next;
+  if (!LEAN && at.row < rows) in.load(a, s, at);
   int turn = 0;
-  for (long row0 = (long)blockIdx.x * p.RPB; row0 < rows; row0 += step, turn ^= 1, in = next) {
+  for (long row0 = (long)blockIdx.x * p.RPB; row0 < rows; row0 += step, turn ^= 1) {
     const RowStep here = at;
     const bool live = here.row < rows;
     at.next(a.T, step);
-    if (at.row < rows) next.load(a, s, at);
+    if constexpr (LEAN) {
+      if (live) in.load(a, s, here);
+    } else {
+      if (at.row < rows) next.load(a, s, at);
+    }
     float y[NV][VEC], hs[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -225,24 +285,28 @@ __global__ __launch_bounds__(NT) void join_fwd_kernel(JoinArgs a, JoinShape p) {
       for (int j = 0; j < NV; ++j) {
         const float r = rsqrtf(hs[j] * p.inv_d + a.eps);
         if (a.rstd_post && live && s.in[j] == 0) a.rstd_post[here.row * a.H + s.head[j]] = r;
+        float wv[VEC];
+        w.get(a.w_post, w.post, s.in[j], s.in[j], s.left[j], j, wv);
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) y[j][v] *= r * wpost[j][v];
+        for (int v = 0; v < VEC; ++v) y[j][v] *= r * wv[v];
       }
     }
     float sq = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (!live || s.in[j] < 0) continue;
+      float sc[VEC];
+      w.get(a.scale, w.scale, s.at[j], s.in[j], s.left[j], j, sc);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
         if (a.z) {
           const float z = (float)in.z[j][v], g = sigmoid(z);
           y[j][v] *= a.act == GLA_ACT_SILU ? z * g : g;
         }
-        y[j][v] = fmaf(scale[j][v], y[j][v], a.residual ? (float)in.r[j][v] : 0.f);
+        y[j][v] = fmaf(sc[v], y[j][v], a.residual ? (float)in.r[j][v] : 0.f);
         sq = fmaf(y[j][v], y[j][v], sq);
       }
-      store_row<R, VEC>((R*)a.out + here.row * D + s.at[j], y[j]);
+      store_slot<EVEN>((R*)a.out + here.row * D + s.at[j], y[j], s.left[j]);
     }
     if (a.w_pre) {
       const float r = rsqrtf(row_sum(sq, p.TPR, red, turn) * p.inv_D + a.eps);
@@ -250,11 +314,14 @@ __global__ __launch_bounds__(NT) void join_fwd_kernel(JoinArgs a, JoinShape p) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         if (!live || s.in[j] < 0) continue;
+        float wv[VEC];
+        w.get(a.w_pre, w.pre, s.at[j], s.in[j], s.left[j], j, wv);
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) y[j][v] *= r * wpre[j][v];
-        store_row<E, VEC>((E*)a.normed + here.row * D + s.at[j], y[j]);
+        for (int v = 0; v < VEC; ++v) y[j][v] *= r * wv[v];
+        store_slot<EVEN>((E*)a.normed + here.row * D + s.at[j], y[j], s.left[j]);
       }
     }
+    if constexpr (!LEAN) in = next;
   }
 }
 
@@ -265,45 +332,53 @@ __global__ __launch_bounds__(NT) void join_fwd_kernel(JoinArgs a, JoinShape p) {
 // and adds up the weights' gradients dn n, dO m, du yn over its rows in registers, then over the
 // workgroup's RPB rows and for w_post the heads in LDS; partial: [workgroup][3][D], summed in
 // order by join_sum_kernel.
-template <typename E, typename R, int VEC, int NV, int NT>
+template <typename E, typename R, int NV, int NT, bool EVEN>
 __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinArgs a, JoinShape p) {
+  constexpr bool LEAN = NV > 1;
   extern __shared__ float lds[];
   float *red = lds, *hred = lds + 32;  // 2 x 16, 2 x 16 NV floats, then RPB rows for the last sums
   const int D = a.H * a.d;
   const int lane = threadIdx.x % p.TPR, sub = threadIdx.x / p.TPR;
   const long rows = (long)a.B * a.T, step = (long)gridDim.x * p.RPB;
-  const Slots<NV> s = row_slots<VEC, NV>(a, p, lane);
-  float wpost[NV][VEC], scale[NV][VEC], wpre[NV][VEC];
-  load_weights<VEC, NV>(a.w_post, s.in, s.in, wpost);
-  load_weights<VEC, NV>(a.scale, s.at, s.in, scale);
-  load_weights<VEC, NV>(a.w_pre, s.at, s.in, wpre);
+  const Slots<NV> s = row_slots<NV>(a, p, lane);
+  const Weights<LEAN, EVEN, NV> w(a, s);
   float spre[NV][VEC] = {}, sscale[NV][VEC] = {}, spost[NV][VEC] = {};
   RowStep at((long)blockIdx.x * p.RPB + sub, a.T, step);
-  RowIn<E, R, VEC, NV, true> in, next;
-  if (at.row < rows) in.load(a, s, at);
+  RowIn<E, R, NV, true, EVEN> in, next;
+  if (!LEAN && at.row < rows) in.load(a, s, at);
   int turn = 0;
-  for (long row0 = (long)blockIdx.x * p.RPB; row0 < rows; row0 += step, turn ^= 1, in = next) {
+  for (long row0 = (long)blockIdx.x * p.RPB; row0 < rows; row0 += step, turn ^= 1) {
     const RowStep here = at;
     const bool live = here.row < rows;
     at.next(a.T, step);
-    if (at.row < rows) next.load(a, s, at);
+    if constexpr (LEAN) {
+      if (live) in.load(a, s, here);
+    } else {
+      if (at.row < rows) next.load(a, s, at);
+    }
     float yn[NV][VEC], f[NV][VEC], n[NV][VEC], e[NV][VEC];  // f: sigmoid(z)
     float dot = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const bool have = live && s.in[j] >= 0;
+      float wpost[VEC], scale[VEC], wpre[VEC];
+      if (a.d_normed) {
+        w.get(a.w_post, w.post, s.in[j], s.in[j], s.left[j], j, wpost);
+        w.get(a.scale, w.scale, s.at[j], s.in[j], s.left[j], j, scale);
+        w.get(a.w_pre, w.pre, s.at[j], s.in[j], s.left[j], j, wpre);
+      }
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
         yn[j][v] = have ? (float)in.y[j][v] * in.ry[j] : 0.f;
         f[j][v] = a.z && have ? sigmoid((float)in.z[j][v]) : 1.f;
         n[j][v] = e[j][v] = 0.f;
         if (a.d_normed && have) {
-          float m = yn[j][v] * wpost[j][v] * f[j][v];
+          float m = yn[j][v] * wpost[v] * f[j][v];
           if (a.z && a.act == GLA_ACT_SILU) m *= (float)in.z[j][v];
-          n[j][v] = fmaf(scale[j][v], m, a.residual ? (float)in.r[j][v] : 0.f) * in.rp;
+          n[j][v] = fmaf(scale[v], m, a.residual ? (float)in.r[j][v] : 0.f) * in.rp;
           const float dn = (float)in.dn[j][v];
           spre[j][v] = fmaf(dn, n[j][v], spre[j][v]);
-          e[j][v] = dn * wpre[j][v];
+          e[j][v] = dn * wpre[v];
           dot = fmaf(e[j][v], n[j][v], dot);
         }
       }
@@ -320,10 +395,13 @@ __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinArgs a, JoinShape p) {
         dO[v] = a.d_out ? (float)in.dout[j][v] : 0.f;
         if (a.d_normed) dO[v] = fmaf(in.rp, fmaf(-n[j][v], dot, e[j][v]), dO[v]);
       }
-      if (a.d_residual) store_row<R, VEC>((R*)a.d_residual + here.row * D + s.at[j], dO);
+      if (a.d_residual) store_slot<EVEN>((R*)a.d_residual + here.row * D + s.at[j], dO, s.left[j]);
+      float wpost[VEC], scale[VEC];
+      w.get(a.w_post, w.post, s.in[j], s.in[j], s.left[j], j, wpost);
+      w.get(a.scale, w.scale, s.at[j], s.in[j], s.left[j], j, scale);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
-        const float u = yn[j][v] * wpost[j][v];
+        const float u = yn[j][v] * wpost[v];
         float act = 1.f, slope = 0.f;
         if (a.z) {
           const float z = (float)in.z[j][v], g = f[j][v];
@@ -331,14 +409,14 @@ __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinArgs a, JoinShape p) {
           slope = a.act == GLA_ACT_SILU ? g * fmaf(z, 1.f - g, 1.f) : g * (1.f - g);
         }
         sscale[j][v] = fmaf(dO[v], u * act, sscale[j][v]);
-        dO[v] *= scale[j][v];
+        dO[v] *= scale[v];
         dz[v] = dO[v] * u * slope;
         dO[v] *= act;  // du
         spost[j][v] = fmaf(dO[v], yn[j][v], spost[j][v]);
-        e[j][v] = dO[v] * wpost[j][v];
+        e[j][v] = dO[v] * wpost[v];
         hs[j] = fmaf(e[j][v], yn[j][v], hs[j]);
       }
-      if (a.z) store_row<E, VEC>((E*)a.dz + here.row * D + s.at[j], dz);
+      if (a.z) store_slot<EVEN>((E*)a.dz + here.row * D + s.at[j], dz, s.left[j]);
     }
     if (a.w_post) head_sums<NV>(hs, p, lane, hred, turn);
 #pragma unroll
@@ -349,8 +427,9 @@ __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinArgs a, JoinShape p) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) e[j][v] = in.ry[j] * fmaf(-yn[j][v], mean, e[j][v]);
       }
-      store_row<E, VEC>((E*)a.dy + (((long)here.b * a.H + s.head[j]) * a.T + here.t) * a.d + s.in[j], e[j]);
+      store_slot<EVEN>((E*)a.dy + (((long)here.b * a.H + s.head[j]) * a.T + here.t) * a.d + s.in[j], e[j], s.left[j]);
     }
+    if constexpr (!LEAN) in = next;
   }
   if (!a.partial) return;
   // the workgroup's sums, through LDS where several rows (and for w_post heads) add up
@@ -365,7 +444,13 @@ __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinArgs a, JoinShape p) {
     for (int j = 0; j < NV; ++j) {
       if (s.in[j] < 0) continue;
       const float(&acc)[VEC] = which == 0 ? spre[j] : which == 1 ? sscale[j] : spost[j];
-      store_row<float, VEC>((terms > 1 ? sums + sub * D : to) + s.at[j], acc);
+      if (terms > 1) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v)
+          if (EVEN || v < s.left[j]) sums[sub * D + s.at[j] + v] = acc[v];
+      } else {
+        store_slot<EVEN>(to + s.at[j], acc, s.left[j]);
+      }
     }
     if (terms == 1) continue;
     __syncthreads();
@@ -409,71 +494,56 @@ __global__ __launch_bounds__(1024) void join_sum_kernel(JoinArgs a, int G) {
   }
 }
 
-static bool rows_aligned(const void* p, const Strides& s, int bytes) {
-  return (uintptr_t)p % (bytes < 16 ? bytes : 16) == 0 && s.b % 8 == 0 && s.h % 8 == 0 && s.t % 8 == 0;
-}
-
-// Slots of 8 elements where the head width and every pointer and stride allow 16-byte accesses,
-// of one element otherwise.
-static bool join_wide(const JoinArgs& a) {
-  const Strides none{0, 0, 0};
-  const void* own[] = {a.w_post, a.scale, a.w_pre, a.out, a.normed, a.dy, a.dz, a.d_residual, a.partial};
-  for (const void* q : own)
-    if (q && !rows_aligned(q, none, 16)) return false;
-  return a.d % 8 == 0 && rows_aligned(a.y, a.ys, 16) && rows_aligned(a.z, a.zs, 16) &&
-         rows_aligned(a.residual, a.rs, 16) && rows_aligned(a.d_out, a.dos, 16) && rows_aligned(a.d_normed, a.dns, 16);
-}
-
-// Lanes of a workgroup (more where a row needs them) and the most workgroups.  Measured on
-// 16k rows of 2048, forward and backward together: backward 512 x 256 lanes 184 us, 256 x 256 238,
-// 384 202, 768 208, 1024 189, 512 x 512 198; on 32k rows of 1024 forward: 1024 x 256 38.2 us,
+// Lanes of a workgroup (more where a row needs them) and the most workgroups, each of which leaves
+// a row of partial sums backward; with more lanes fewer, as many as fit the chip at once.  Measured
+// on 16k rows of 2048, forward and backward together: backward 512 x 256 lanes 184 us, 256 x 256
+// 238, 384 202, 768 208, 1024 189, 512 x 512 198; on 32k rows of 1024 forward: 1024 x 256 38.2 us,
 // 2048 41.8, 4096 42.9.
-constexpr int kFwdThreads = 256, kBwdThreads = 256, kBwdGroups = 512, kFwdGroups = 1024;
+constexpr int kJoinThreads = 256, kBwdGroups = 512, kFwdGroups = 1024;
+// Lanes of a row at most: the backward's registers (one slot a lane 170, two 200) fit 8 waves on a CU.
+constexpr int kFwdLanes = 1024, kBwdLanes = 512;
 
-static int join_groups(long long rows, int RPB, int most) {
-  const long long n = (rows + RPB - 1) / RPB;
+static int join_groups(long long rows, const JoinShape& p, int most) {
+  const long long n = (rows + p.RPB - 1) / p.RPB;
+  most = most * kJoinThreads / (p.TPR * p.RPB);
   return (int)(n < most ? n : most);
 }
 
 size_t join_partial_floats(int B, int H, int T, int d) {
-  int G = 0;
-  for (int vec : {1, 8}) {
-    const int g = join_groups((long long)B * T, join_shape(H, d, vec, kBwdThreads).RPB, kBwdGroups);
-    if (g > G) G = g;
-  }
-  return (size_t)G * 3 * H * d;
+  return (size_t)join_groups((long long)B * T, join_shape(H, d, kJoinThreads, kBwdLanes), kBwdGroups) * 3 * H * d;
 }
 
-template <typename E, typename R, int VEC, int NV, int NT>
-static void join_run(const JoinArgs& a, const JoinShape& p, bool bwd, hipStream_t s) {
-  const long long rows = (long long)a.B * a.T;
-  const int threads = p.TPR * p.RPB;
-  if (!bwd) {
-    join_fwd_kernel<E, R, VEC, NV, NT><<<join_groups(rows, p.RPB, kFwdGroups), threads, 0, s>>>(a, p);
-  } else {
-    const int G = join_groups(rows, p.RPB, kBwdGroups);
-    const size_t lds = (32 + 32 * NV + (a.partial && (p.RPB > 1 || a.dw_post) ? p.RPB * a.H * a.d : 0)) * sizeof(float);
-    join_bwd_kernel<E, R, VEC, NV, NT><<<G, threads, lds, s>>>(a, p);
-    if (a.partial) join_sum_kernel<<<dim3((a.H * a.d + 63) / 64, 3), 1024, 0, s>>>(a, G);
-  }
+template <typename E, typename R, bool EVEN>
+static void join_fwd_run(const JoinArgs& a, hipStream_t s) {
+  const JoinShape p = join_shape(a.H, a.d, kJoinThreads, kFwdLanes);
+  const int G = join_groups((long long)a.B * a.T, p, kFwdGroups), threads = p.TPR * p.RPB;
+  if (threads == 256) join_fwd_kernel<E, R, 1, 256, EVEN><<<G, threads, 0, s>>>(a, p);
+  else if (p.NV == 1) join_fwd_kernel<E, R, 1, 1024, EVEN><<<G, threads, 0, s>>>(a, p);
+  else join_fwd_kernel<E, R, 2, 1024, EVEN><<<G, threads, 0, s>>>(a, p);
+}
+
+template <typename E, typename R, bool EVEN>
+static void join_bwd_run(const JoinArgs& a, hipStream_t s) {
+  const JoinShape p = join_shape(a.H, a.d, kJoinThreads, kBwdLanes);
+  const int G = join_groups((long long)a.B * a.T, p, kBwdGroups), threads = p.TPR * p.RPB;
+  const size_t lds = (32 + 32 * p.NV + (a.partial && (p.RPB > 1 || a.dw_post) ? p.RPB * a.H * a.d : 0)) * sizeof(float);
+  if (threads == 256) join_bwd_kernel<E, R, 1, 256, EVEN><<<G, threads, lds, s>>>(a, p);
+  else if (p.NV == 1) join_bwd_kernel<E, R, 1, 512, EVEN><<<G, threads, lds, s>>>(a, p);
+  else if (p.NV == 2) join_bwd_kernel<E, R, 2, 512, EVEN><<<G, threads, lds, s>>>(a, p);
+  else join_bwd_kernel<E, R, 4, 512, EVEN><<<G, threads, lds, s>>>(a, p);
+  if (a.partial) join_sum_kernel<<<dim3((a.H * a.d + 63) / 64, 3), 1024, 0, s>>>(a, G);
+}
+
+template <typename E, typename R, bool EVEN>
+static void join_rows(const JoinArgs& a, bool bwd, hipStream_t s) {
+  if (bwd) join_bwd_run<E, R, EVEN>(a, s);
+  else join_fwd_run<E, R, EVEN>(a, s);
 }
 
 template <typename E, typename R>
 static void join_vec(const JoinArgs& a, bool bwd, hipStream_t s) {
-  const int threads = bwd ? kBwdThreads : kFwdThreads;
-  if (join_wide(a)) {
-    const JoinShape p = join_shape(a.H, a.d, 8, threads);
-    if (p.TPR <= 512) join_run<E, R, 8, 1, 512>(a, p, bwd, s);
-    else if (p.NV == 1) join_run<E, R, 8, 1, 1024>(a, p, bwd, s);
-    else join_run<E, R, 8, 2, 1024>(a, p, bwd, s);
-  } else {
-    const JoinShape p = join_shape(a.H, a.d, 1, threads);
-    if (p.NV == 1) join_run<E, R, 1, 1, 1024>(a, p, bwd, s);
-    else if (p.NV == 2) join_run<E, R, 1, 2, 1024>(a, p, bwd, s);
-    else if (p.NV == 4) join_run<E, R, 1, 4, 1024>(a, p, bwd, s);
-    else if (p.NV == 8) join_run<E, R, 1, 8, 1024>(a, p, bwd, s);
-    else join_run<E, R, 1, 16, 1024>(a, p, bwd, s);
-  }
+  if (a.d % VEC == 0) join_rows<E, R, true>(a, bwd, s);
+  else join_rows<E, R, false>(a, bwd, s);
 }
 
 static hipError_t join_launch(const JoinArgs& a, bool bwd, hipStream_t s) {
