@@ -520,10 +520,14 @@ def _out(t, name, shape, dtype, device, optional=False):
     return t.data_ptr()
 
 
-def _new(t, name, shape, dtype, device):
-    """(tensor, pointer) of an output: the caller's, checked, or a new one."""
+def _new(t, name, shape, dtype, device, like=None):
+    """(tensor, pointer) of an output: the caller's, checked, or a new one (made like a tensor of its
+    shape where there is one: the quickest way to an empty tensor)."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
+        if like is None:
+            t = torch.empty(shape, dtype=dtype, device=device)
+        else:
+            t = torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
         return t, t.data_ptr()
     return t, _out(t, name, shape, dtype, device)
 
@@ -617,8 +621,8 @@ def gla_recur_fwd(x, g, h0=None, lens=None, mode: str = "plain", h=None, chunk_i
     gp, gs = _view(g, "g", (B, T, D), f32, dev)
     h0p = _out(h0, "h0", (B, D), f32, dev, optional=True)
     lp = _out(lens, "lens", (B,), torch.int32, dev, optional=True)
-    h, hp = _new(h, "h", (B, T, D), x.dtype, dev)
-    h_final, fp = _new(h_final, "h_final", (B, D), f32, dev)
+    h, hp = _new(h, "h", (B, T, D), x.dtype, dev, x)
+    h_final, fp = _new(h_final, "h_final", (B, D), f32, dev, h0)
     cp = None
     if keep_chunk_states:
         chunk_in, cp = _new(chunk_in, "chunk_in", (B, (T + RECUR_CHUNK - 1) // RECUR_CHUNK, D), f32, dev)
@@ -643,9 +647,9 @@ def gla_recur_bwd(x, g, dh, chunk_in, lens=None, dhT=None, mode: str = "plain", 
     cp = _out(chunk_in, "chunk_in", (B, (T + RECUR_CHUNK - 1) // RECUR_CHUNK, D), f32, dev)
     lp = _out(lens, "lens", (B,), torch.int32, dev, optional=True)
     tp = _out(dhT, "dhT", (B, D), f32, dev, optional=True)
-    dx, dxp = _new(dx, "dx", (B, T, D), x.dtype, dev)
-    dg, dgp = _new(dg, "dg", (B, T, D), f32, dev)
-    dh0, d0p = _new(dh0, "dh0", (B, D), f32, dev)
+    dx, dxp = _new(dx, "dx", (B, T, D), x.dtype, dev, x)
+    dg, dgp = _new(dg, "dg", (B, T, D), f32, dev, g)
+    dh0, d0p = _new(dh0, "dh0", (B, D), f32, dev, dhT)
     workspace, wp, wn = _scratch(workspace, recur_workspace_size(B, T, D), dev)
     _launch(load_library().gla_recur_bwd, dev, xp, xs, gp, gs, dp, ds, cp, lp, tp, dxp, dgp, d0p, B, T, D, m, dt, wp, wn)
     return dx, dg, dh0
@@ -676,7 +680,7 @@ def gla_recur_step(x, g, state, slots=None, mode: str = "plain", h=None):
     xp, xs = _view(x, "x", (B, D), x.dtype, dev)
     gp, gs = _view(g, "g", (B, D), torch.float32, dev)
     sp, ip, n = _pool(state, slots, B, (D,), dev)
-    h, hp = _new(h, "h", (B, D), x.dtype, dev)
+    h, hp = _new(h, "h", (B, D), x.dtype, dev, x)
     _launch(load_library().gla_recur_step, dev, xp, xs, gp, gs, sp, ip, hp, B, D, n, m, dt)
     return h
 
@@ -697,7 +701,7 @@ def gla_step(q, k, v, g, state, slots=None, o=None):
     vp, vs = _view(v, "v", (B, H, n, dv), q.dtype, dev)
     gp, gs = _view(g, "g", (B, H, n, dk), torch.float32, dev)
     sp, ip, n_slots = _pool(state, slots, B, (H, dk, dv), dev)
-    o, op = _new(o, "o", (B, H, n, dv), q.dtype, dev)
+    o, op = _new(o, "o", (B, H, n, dv), q.dtype, dev, v)
     _launch(load_library().gla_step, dev, qp, qs, kp, ks, vp, vs, gp, gs, sp, ip, op, B, H, n, dk, dv, n_slots, dt)
     return o
 
@@ -736,10 +740,10 @@ def gla_join_fwd(y, z=None, w_post=None, residual=None, scale=None, w_pre=None, 
     gla_join_bwd (None with keep_rstd=False)."""
     (B, H, T, d), st, dt, ptrs = _join_args(y, z, w_post, residual, scale, w_pre)
     dev, D, f32 = y.device, H * d, torch.float32
-    out, op = _new(out, "out", (B, T, D), st, dev)
+    out, op = _new(out, "out", (B, T, D), st, dev, z if residual is None else residual)
     np_ = None
     if w_pre is not None:
-        normed, np_ = _new(normed, "normed", (B, T, D), y.dtype, dev)
+        normed, np_ = _new(normed, "normed", (B, T, D), y.dtype, dev, out)
     elif normed is not None:
         raise ValueError("normed given without w_pre")
     r_post = torch.empty((B, T, H), dtype=f32, device=dev) if keep_rstd and w_post is not None else None
@@ -765,18 +769,14 @@ def gla_join_bwd(y, fwd: dict, d_out=None, d_normed=None, z=None, w_post=None, r
     rpre = None if d_normed is None else _out(fwd["rstd_pre"], "fwd['rstd_pre']", (B, T), f32, dev)
     dop, dos = (None, None) if d_out is None else _view(d_out, "d_out", (B, T, D), st, dev)
     dnp, dns = (None, None) if d_normed is None else _view(d_normed, "d_normed", (B, T, D), y.dtype, dev)
-    dy = torch.empty((B, H, T, d), dtype=y.dtype, device=dev)
-    dz = None if z is None else torch.empty((B, T, D), dtype=y.dtype, device=dev)
-    dr = None if residual is None else torch.empty((B, T, D), dtype=st, device=dev)
-    dwo = None if w_post is None else torch.empty(d, dtype=f32, device=dev)
-    dsc = None if scale is None else torch.empty(D, dtype=f32, device=dev)
-    dwp = None if w_pre is None else torch.empty(D, dtype=f32, device=dev)
+    grads = [None if t is None else torch.empty_like(t, memory_format=torch.contiguous_format)
+             for t in (y, z, residual, w_post, scale, w_pre)]
     sums = not (w_post is None and scale is None and w_pre is None)
     workspace, wp, wn = _scratch(workspace, join_workspace_size(B, H, T, d) if sums else 0, dev)
-    _launch(load_library().gla_join_bwd, dev, *ptrs, rpost, rpre, dop, dos, dnp, dns, dy.data_ptr(),
-            *(None if t is None else t.data_ptr() for t in (dz, dr, dwo, dsc, dwp)), B, H, T, d,
-            _code(ACTS, act, "act"), dt, _dtype_code(st), wp, wn)
-    return {"dy": dy, "dz": dz, "d_residual": dr, "dw_post": dwo, "dscale": dsc, "dw_pre": dwp}
+    _launch(load_library().gla_join_bwd, dev, *ptrs, rpost, rpre, dop, dos, dnp, dns,
+            *[None if t is None else t.data_ptr() for t in grads], B, H, T, d, _code(ACTS, act, "act"), dt,
+            _dtype_code(st), wp, wn)
+    return dict(zip(("dy", "dz", "d_residual", "dw_post", "dscale", "dw_pre"), grads))
 
 
 # ------------------------------------------------------------------------------ method chains
