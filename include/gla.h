@@ -1,7 +1,8 @@
 /*
  * gla.h -- C ABI of libgla.so: chunkwise gated linear attention with a per-key-channel
  * (diagonal) decay, forward and backward, and ZeCO's segment decomposition, on one
- * MI355X (gfx950).
+ * MI355X (gfx950); and the other operators of a recurrent block: the elementwise gated linear
+ * recurrence, the join with the residual stream, and the single-token steps (last section).
  *
  * The method (ZeCO, arXiv 2507.01004, as summarised on the atlas.scime.ai and
  * pith.science pages):

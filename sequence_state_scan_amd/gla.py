@@ -11,7 +11,11 @@ local pass -> segment scan -> correction, and the same for the backward.
 ``states_first_forward`` / ``states_first_backward`` chain the same decomposition with the
 segments' incoming states first: state pass -> segment scan -> local pass from the true incoming
 state, with no correction pass (cheaper where the decay is weak and the corrections would reach
-every chunk).
+every chunk).  All four take a join (gla_join_fwd / gla_join_bwd): the block's output norm, gate,
+residual and the next block's norm.
+
+The other operators of a recurrent block: gla_recur_fwd, gla_recur_bwd (elementwise gated linear
+recurrence), gla_step and gla_recur_step (single tokens on a pool of states).
 """
 from __future__ import annotations
 
@@ -765,6 +769,8 @@ def gla_join_bwd(y, fwd: dict, d_out=None, d_normed=None, z=None, w_post=None, r
         raise ValueError("one of d_out and d_normed is required")
     if d_normed is not None and w_pre is None:
         raise ValueError("d_normed given without w_pre")
+    if residual is not None and fwd["out"].data_ptr() == residual.data_ptr():
+        raise ValueError("the forward wrote out in the residual's place: its inputs are gone")
     rpost = None if w_post is None else _out(fwd["rstd_post"], "fwd['rstd_post']", (B, T, H), f32, dev)
     rpre = None if d_normed is None else _out(fwd["rstd_pre"], "fwd['rstd_pre']", (B, T), f32, dev)
     dop, dos = (None, None) if d_out is None else _view(d_out, "d_out", (B, T, D), st, dev)

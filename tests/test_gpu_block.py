@@ -364,10 +364,21 @@ def test_step_views_and_unaligned_rows():
         assert torch.equal(got, ref) and torch.equal(s2, s1)
 
 
+def test_step_with_shared_heads():
+    # one q, k and g for all heads, as expanded views
+    B, H, n, dk, dv = 3, 4, 2, 48, 64
+    q, k, v, g, pool = (t.cuda() for t in step_inputs(6, B, H, n, dk, dv, BF16))
+    one = lambda t: t[:, :1].expand(B, H, n, dk)  # noqa: E731
+    s1, s2 = pool.clone(), pool.clone()
+    o = gla.gla_step(one(q), one(k), v, one(g), s1)
+    assert torch.equal(o, gla.gla_step(*(one(t).contiguous() for t in (q, k)), v, one(g).contiguous(), s2))
+    assert torch.equal(s1, s2)
+
+
 def test_step_continues_a_chunked_forward():
     # a prompt of 2 chunks through the chunked forward, its ragged end and the answer through gla_step
     B, H, T, dk, dv, chunk = 2, 2, 139, 32, 64, 64
-    d = inputs.generate(B, H, T, dk, dv, "f32" if False else "bf16", 5)
+    d = inputs.generate(B, H, T, dk, dv, "bf16", 5)
     x = {n: t.cuda() for n, t in d.items()}
     cut = T // chunk * chunk
     head = {n: t[:, :, :cut].contiguous() for n, t in x.items()}
@@ -540,6 +551,8 @@ def test_join_in_the_residuals_place():
     g = gla.gla_join_fwd(y.cuda(), eps=EPS, out=r, keep_rstd=False, **dict(gpu, residual=r))
     assert g["out"] is r and torch.equal(r, f["out"]) and torch.equal(g["normed"], f["normed"])
     assert g["rstd_post"] is None and g["rstd_pre"] is None
+    with pytest.raises(ValueError, match="residual's place"):
+        gla.gla_join_bwd(y.cuda(), g, d_out=r, **dict(gpu, residual=r))
 
 
 def test_join_is_the_same_every_time():
