@@ -17,7 +17,7 @@
 // Which of the two a reader finds depends on the timing, the result does not: a state is the map
 // applied to the state before, whoever applies it.  Tiles are numbered by a ticket in the order
 // they start, and every tile publishes its pair before it waits, so each wait is for a tile that
-// runs already and waits for nothing before that.
+// runs already and itself waits only for tiles before it.
 #include "gla_block.hpp"
 
 namespace gla {
@@ -174,10 +174,13 @@ __global__ __launch_bounds__(64 * NW) void recur_fwd_kernel(RecurArgs a) {
       A *= wa;
       B = advance(wa, B, runB[w][lane]);
     }
-    const bool wanted = a.words && (n + 1) * TILE < len;  // a later tile of the sequence reads this one's word
-    if (a.words && n > 0) {
-      if (wanted) publish(a.words + n * stride + col, pack(A, B));
-      in = look_back<LOOK>(a.words + col, stride, n, in);
+    // a later tile of the sequence reads this one's word
+    const bool wanted = LOOK > 0 && a.words && (n + 1) * TILE < len;
+    if constexpr (LOOK > 0) {
+      if (a.words && n > 0) {
+        if (wanted) publish(a.words + n * stride + col, pack(A, B));
+        in = look_back<LOOK>(a.words + col, stride, n, in);
+      }
     }
     const float out = advance(A, in, B);
     if (wanted) publish(a.words + n * stride + col, pack(-1.f, out));
@@ -277,12 +280,14 @@ __global__ __launch_bounds__(64 * NW) void recur_bwd_kernel(RecurArgs a) {
       U = advance(wa, U, runU[w][lane]);
     }
     const int end = len > 0 ? (len - 1) / TILE : 0;  // the sequence's last tile; words count from it
-    if (a.words && n < end) {
-      if (n > 0) publish(a.words + (end - n) * stride + col, pack(A, U));
-      in = look_back<LOOK>(a.words + col, stride, end - n, in);
+    if constexpr (LOOK > 0) {
+      if (a.words && n < end) {
+        if (n > 0) publish(a.words + (end - n) * stride + col, pack(A, U));
+        in = look_back<LOOK>(a.words + col, stride, end - n, in);
+      }
     }
     const float out = advance(A, in, U);
-    if (a.words && n > 0) publish(a.words + (end - n) * stride + col, pack(-1.f, out));
+    if (LOOK > 0 && a.words && n > 0) publish(a.words + (end - n) * stride + col, pack(-1.f, out));
     enter[lane] = in;
     if (a.h_final && n == 0) a.h_final[col] = out;
   }
@@ -327,7 +332,7 @@ template <bool BWD, typename E, int MODE, int NW, int TW, int LOOK>
 static void recur_run(RecurArgs a, hipStream_t s) {
   const unsigned ncb = (a.D + 63) / 64, tiles = (a.T + NW * TW - 1) / (NW * TW);
   if (tiles > 1) {
-    static_assert(LOOK == 1 || NW * TW == kRecurTile, "the workspace is laid out for tiles of that many tokens");
+    static_assert(LOOK == 0 || NW * TW == kRecurTile, "the workspace is laid out for tiles of that many tokens");
     word* ws = a.words;
     const long n = (long)recur_workspace_words(a.B, a.T, a.D), blocks = (n + 255) / 256;
     recur_clear_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(ws, n);
@@ -342,7 +347,7 @@ static void recur_run(RecurArgs a, hipStream_t s) {
 }
 
 // The tile and the look back by size.  Up to 128 tokens one tile does, of as many waves as have
-// tokens.  Beyond, a tile is 256 tokens: forward 8 waves of 32, whose 64 loads a lane are in flight
+// tokens, with no look back.  Beyond, a tile is 256 tokens: forward 8 waves of 32, whose 64 loads a lane are in flight
 // at once (4 x 4096 x 2048 bf16 64 us; 128-token tiles of 64 channels 112, of 128 channels 82).
 // With few columns of 64 channels (cols) the tiles of one column wait for each other in a chain of
 // T / (256 LOOK) hops of about 1.5 us each, and a longer look pays; with many the words' reads do
@@ -354,11 +359,11 @@ template <bool BWD, typename E, int MODE>
 static void recur_shape(const RecurArgs& a, hipStream_t s) {
   const long long cols = (long long)a.B * ((a.D + 63) / 64);
   if (a.T <= 16) {
-    recur_run<BWD, E, MODE, 1, 16, 1>(a, s);
+    recur_run<BWD, E, MODE, 1, 16, 0>(a, s);
   } else if (a.T <= 64) {
-    recur_run<BWD, E, MODE, 4, 16, 1>(a, s);
+    recur_run<BWD, E, MODE, 4, 16, 0>(a, s);
   } else if (a.T <= 128) {
-    recur_run<BWD, E, MODE, 8, 16, 1>(a, s);
+    recur_run<BWD, E, MODE, 8, 16, 0>(a, s);
   } else if constexpr (!BWD) {
     if (cols >= 8) recur_run<BWD, E, MODE, 8, 32, 8>(a, s);
     else if (cols >= 3) recur_run<BWD, E, MODE, 16, 16, 16>(a, s);

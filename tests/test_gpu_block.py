@@ -301,6 +301,27 @@ def test_bad_slots_give_nan_and_touch_nothing():
     assert torch.equal(state[[1, 3]], pool[[1, 3]]) and not torch.equal(state[[0, 2]], pool[[0, 2]])
 
 
+def test_a_slot_named_twice_far_apart():
+    B, D = 300, 40
+    x, g, _, _, _ = recur_inputs(2, B, 1, D, F32)
+    x, g = x[:, 0].cuda(), g[:, 0].cuda()
+    slots = torch.randperm(400, generator=torch.Generator().manual_seed(3))[:B].to(torch.int32)
+    bad = {70: 3, 199: 64, 299: 0, 200: 199}  # 200 repeats 199's, which is 64's: both later ones are refused
+    for i, j in bad.items():
+        slots[i] = slots[j]
+    pool = torch.randn(400, D, device="cuda")
+    state = pool.clone()
+    h = gla.gla_recur_step(x, g, state, slots=slots.cuda())
+    good = [i for i in range(B) if i not in bad]
+    assert torch.isnan(h[list(bad)]).all() and torch.isfinite(h[good]).all()
+    want = pool.clone()
+    rows = slots[good].long().cuda()
+    sub = pool[rows].clone()
+    assert torch.equal(gla.gla_recur_step(x[good], g[good], sub), h[good])
+    want[rows] = sub
+    assert torch.equal(state, want)
+
+
 # ---------------------------------------------------------------------------------------- step
 
 def step_reference(q, k, v, g, S):
