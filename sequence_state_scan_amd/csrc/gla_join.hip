@@ -29,16 +29,20 @@ static int pow2_up(int n) {
   return p;
 }
 
-// threads: of a workgroup, where a row takes fewer; most: lanes of a row.
-static JoinShape join_shape(int H, int d, int threads, int most) {
+// Lanes of a workgroup, where a row takes fewer, and of a row at most.  Rows of more slots take two a
+// lane (padded heads four): 8192 rows of 8192 forward bf16 191 us, float32 258; with 1024 lanes of
+// one slot 198 and 293.  The backward's registers (one slot a lane 190, two 240) fit 8 waves on a CU.
+constexpr int kJoinThreads = 256, kJoinLanes = 512;
+
+static JoinShape join_shape(int H, int d) {
   JoinShape s;
   const int n = (d + VEC - 1) / VEC;
   s.LPH = n <= 64 ? pow2_up(n) : (n + 63) / 64 * 64;
   s.slots = H * s.LPH;
   s.TPR = pow2_up(s.slots);
-  if (s.TPR > most) s.TPR = most;
+  if (s.TPR > kJoinLanes) s.TPR = kJoinLanes;
   s.NV = pow2_up((s.slots + s.TPR - 1) / s.TPR);
-  s.RPB = s.TPR >= threads ? 1 : threads / s.TPR;
+  s.RPB = s.TPR >= kJoinThreads ? 1 : kJoinThreads / s.TPR;
   s.inv_d = 1.f / d;
   s.inv_D = 1.f / (H * d);
   return s;
@@ -196,12 +200,36 @@ struct RowStep {
   }
 };
 
+// Hides where a value comes from, so that what is formed from it before is formed again after
+// instead of being held in registers.
+template <typename T>
+__device__ __forceinline__ void forget(T& v) {
+  typedef unsigned words __attribute__((ext_vector_type(sizeof(T) / 4)));
+  words w = __builtin_bit_cast(words, v);
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 4; ++i) {
+    unsigned x = w[i];
+    asm volatile("" : "+v"(x));
+    w[i] = x;
+  }
+  v = __builtin_bit_cast(T, w);
+}
+
 // One row's inputs as they lie in memory (bf16 stays packed).
 template <typename E, typename R, int NV, bool BWD, bool EVEN>
 struct RowIn {
   typename Pack<E>::raw y[NV], z[NV], dn[BWD ? NV : 1];
   typename Pack<R>::raw r[NV], dout[BWD ? NV : 1];
   float ry[BWD ? NV : 1], rp;
+  __device__ __forceinline__ void forget_all() {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      forget(y[j]);
+      forget(z[j]);
+      forget(r[j]);
+      forget(dn[j]);
+    }
+  }
   __device__ __forceinline__ void load(const JoinArgs& a, const Slots<NV>& s, const RowStep& at) {
     const long b = at.b, t = at.t;
     if constexpr (BWD) rp = a.d_normed ? a.rstd_pre[at.row] : 0.f;
@@ -331,7 +359,10 @@ __global__ __launch_bounds__(NT) void join_fwd_kernel(JoinArgs a, JoinShape p) {
 //   dy = ry (e' - yn mean_d(e' yn))
 // and adds up the weights' gradients dn n, dO m, du yn over its rows in registers, then over the
 // workgroup's RPB rows and for w_post the heads in LDS; partial: [workgroup][3][D], summed in
-// order by join_sum_kernel.
+// order by join_sum_kernel.  With two slots a lane what the sum over the row stands between is formed
+// on both sides of it from the packed inputs, not held: 8192 rows of 8192 float32 578 us, 834 with it
+// held (and spilled); with one slot, where it fits, holding it is faster (32768 rows of 1024 bf16 121
+// us, 142 formed twice).
 template <typename E, typename R, int NV, int NT, bool EVEN>
 __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinArgs a, JoinShape p) {
   constexpr bool LEAN = NV > 1;
@@ -356,11 +387,8 @@ __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinArgs a, JoinShape p) {
     } else {
       if (at.row < rows) next.load(a, s, at);
     }
-    float yn[NV][VEC], f[NV][VEC], n[NV][VEC], e[NV][VEC];  // f: sigmoid(z)
-    float dot = 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const bool have = live && s.in[j] >= 0;
+    float yn[NV][VEC], f[NV][VEC], n[NV][VEC], e[NV][VEC], hs[NV];  // f: sigmoid(z), e: d_normed w_pre
+    const auto form = [&](int j) {
       float wpost[VEC], scale[VEC], wpre[VEC];
       if (a.d_normed) {
         w.get(a.w_post, w.post, s.in[j], s.in[j], s.left[j], j, wpost);
@@ -369,36 +397,45 @@ __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinArgs a, JoinShape p) {
       }
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
-        yn[j][v] = have ? (float)in.y[j][v] * in.ry[j] : 0.f;
-        f[j][v] = a.z && have ? sigmoid((float)in.z[j][v]) : 1.f;
+        yn[j][v] = (float)in.y[j][v] * in.ry[j];
+        f[j][v] = a.z ? sigmoid((float)in.z[j][v]) : 1.f;
         n[j][v] = e[j][v] = 0.f;
-        if (a.d_normed && have) {
+        if (a.d_normed) {
           float m = yn[j][v] * wpost[v] * f[j][v];
           if (a.z && a.act == GLA_ACT_SILU) m *= (float)in.z[j][v];
           n[j][v] = fmaf(scale[v], m, a.residual ? (float)in.r[j][v] : 0.f) * in.rp;
-          const float dn = (float)in.dn[j][v];
-          spre[j][v] = fmaf(dn, n[j][v], spre[j][v]);
-          e[j][v] = dn * wpre[v];
-          dot = fmaf(e[j][v], n[j][v], dot);
+          e[j][v] = (float)in.dn[j][v] * wpre[v];
         }
       }
+    };
+    float dot = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (!live || s.in[j] < 0) continue;
+      form(j);
+#pragma unroll
+      for (int v = 0; v < VEC; ++v)
+        if (a.d_normed) {
+          spre[j][v] = fmaf((float)in.dn[j][v], n[j][v], spre[j][v]);
+          dot = fmaf(e[j][v], n[j][v], dot);
+        }
     }
     if (a.d_normed) dot = row_sum(dot, p.TPR, red, turn) * p.inv_D;
-    float hs[NV];
+    if constexpr (LEAN) in.forget_all();
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       hs[j] = 0.f;
       if (!live || s.in[j] < 0) continue;
-      float dO[VEC], dz[VEC];
+      if constexpr (LEAN) form(j);
+      float wpost[VEC], scale[VEC], dO[VEC], dz[VEC];
+      w.get(a.w_post, w.post, s.in[j], s.in[j], s.left[j], j, wpost);
+      w.get(a.scale, w.scale, s.at[j], s.in[j], s.left[j], j, scale);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
         dO[v] = a.d_out ? (float)in.dout[j][v] : 0.f;
         if (a.d_normed) dO[v] = fmaf(in.rp, fmaf(-n[j][v], dot, e[j][v]), dO[v]);
       }
       if (a.d_residual) store_slot<EVEN>((R*)a.d_residual + here.row * D + s.at[j], dO, s.left[j]);
-      float wpost[VEC], scale[VEC];
-      w.get(a.w_post, w.post, s.in[j], s.in[j], s.left[j], j, wpost);
-      w.get(a.scale, w.scale, s.at[j], s.in[j], s.left[j], j, scale);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
         const float u = yn[j][v] * wpost[v];
@@ -425,7 +462,8 @@ __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinArgs a, JoinShape p) {
       if (a.w_post) {
         const float mean = hs[j] * p.inv_d;
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) e[j][v] = in.ry[j] * fmaf(-yn[j][v], mean, e[j][v]);
+        for (int v = 0; v < VEC; ++v)
+          e[j][v] = in.ry[j] * fmaf(LEAN ? -(float)in.y[j][v] * in.ry[j] : -yn[j][v], mean, e[j][v]);
       }
       store_slot<EVEN>((E*)a.dy + (((long)here.b * a.H + s.head[j]) * a.T + here.t) * a.d + s.in[j], e[j], s.left[j]);
     }
@@ -494,14 +532,11 @@ __global__ __launch_bounds__(1024) void join_sum_kernel(JoinArgs a, int G) {
   }
 }
 
-// Lanes of a workgroup (more where a row needs them) and the most workgroups, each of which leaves
-// a row of partial sums backward; with more lanes fewer, as many as fit the chip at once.  Measured
-// on 16k rows of 2048, forward and backward together: backward 512 x 256 lanes 184 us, 256 x 256
-// 238, 384 202, 768 208, 1024 189, 512 x 512 198; on 32k rows of 1024 forward: 1024 x 256 38.2 us,
-// 2048 41.8, 4096 42.9.
-constexpr int kJoinThreads = 256, kBwdGroups = 512, kFwdGroups = 1024;
-// Lanes of a row at most: the backward's registers (one slot a lane 170, two 200) fit 8 waves on a CU.
-constexpr int kFwdLanes = 1024, kBwdLanes = 512;
+// The most workgroups (of 256 lanes; half as many of 512), each of which leaves a row of partial sums
+// backward.  Measured on 16k rows of 2048, forward and backward together: backward 512 x 256 lanes
+// 184 us, 256 x 256 238, 384 202, 768 208, 1024 189, 512 x 512 198; on 32k rows of 1024 forward:
+// 1024 x 256 38.2 us, 2048 41.8, 4096 42.9.
+constexpr int kBwdGroups = 512, kFwdGroups = 1024;
 
 static int join_groups(long long rows, const JoinShape& p, int most) {
   const long long n = (rows + p.RPB - 1) / p.RPB;
@@ -510,21 +545,22 @@ static int join_groups(long long rows, const JoinShape& p, int most) {
 }
 
 size_t join_partial_floats(int B, int H, int T, int d) {
-  return (size_t)join_groups((long long)B * T, join_shape(H, d, kJoinThreads, kBwdLanes), kBwdGroups) * 3 * H * d;
+  return (size_t)join_groups((long long)B * T, join_shape(H, d), kBwdGroups) * 3 * H * d;
 }
 
 template <typename E, typename R, bool EVEN>
 static void join_fwd_run(const JoinArgs& a, hipStream_t s) {
-  const JoinShape p = join_shape(a.H, a.d, kJoinThreads, kFwdLanes);
+  const JoinShape p = join_shape(a.H, a.d);
   const int G = join_groups((long long)a.B * a.T, p, kFwdGroups), threads = p.TPR * p.RPB;
   if (threads == 256) join_fwd_kernel<E, R, 1, 256, EVEN><<<G, threads, 0, s>>>(a, p);
-  else if (p.NV == 1) join_fwd_kernel<E, R, 1, 1024, EVEN><<<G, threads, 0, s>>>(a, p);
-  else join_fwd_kernel<E, R, 2, 1024, EVEN><<<G, threads, 0, s>>>(a, p);
+  else if (p.NV == 1) join_fwd_kernel<E, R, 1, 512, EVEN><<<G, threads, 0, s>>>(a, p);
+  else if (p.NV == 2) join_fwd_kernel<E, R, 2, 512, EVEN><<<G, threads, 0, s>>>(a, p);
+  else join_fwd_kernel<E, R, 4, 512, EVEN><<<G, threads, 0, s>>>(a, p);
 }
 
 template <typename E, typename R, bool EVEN>
 static void join_bwd_run(const JoinArgs& a, hipStream_t s) {
-  const JoinShape p = join_shape(a.H, a.d, kJoinThreads, kBwdLanes);
+  const JoinShape p = join_shape(a.H, a.d);
   const int G = join_groups((long long)a.B * a.T, p, kBwdGroups), threads = p.TPR * p.RPB;
   const size_t lds = (32 + 32 * p.NV + (a.partial && (p.RPB > 1 || a.dw_post) ? p.RPB * a.H * a.d : 0)) * sizeof(float);
   if (threads == 256) join_bwd_kernel<E, R, 1, 256, EVEN><<<G, threads, lds, s>>>(a, p);
