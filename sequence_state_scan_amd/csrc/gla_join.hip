@@ -30,7 +30,7 @@ static int pow2_up(int n) {
 }
 
 // Lanes of a workgroup, where a row takes fewer, and of a row at most.  Rows of more slots take two a
-// lane (padded heads four): 8192 rows of 8192 forward bf16 191 us, float32 258; with 1024 lanes of
+// lane (padded heads four): 8192 rows of 8192 forward bf16 186 us, float32 275; with 1024 lanes of
 // one slot 198 and 293.  The backward's registers (one slot a lane 190, two 240) fit 8 waves on a CU.
 constexpr int kJoinThreads = 256, kJoinLanes = 512;
 
@@ -250,7 +250,8 @@ struct RowIn {
 };
 
 // The weights at a lane's slots and the next row's inputs are held in registers (a row ahead of
-// their use) where a lane has one slot; with more (LEAN) both are loaded when the row comes.
+// their use) where a lane has one slot.  With more (LEAN) the weights are loaded when they are used,
+// and the next row's inputs once this row's are used up, before its last reduction.
 template <bool LEAN, bool EVEN, int NV>
 struct Weights {
   float post[LEAN ? 1 : NV][VEC], scale[LEAN ? 1 : NV][VEC], pre[LEAN ? 1 : NV][VEC];
@@ -285,17 +286,13 @@ __global__ __launch_bounds__(NT) void join_fwd_kernel(JoinArgs a, JoinShape p) {
   const Weights<LEAN, EVEN, NV> w(a, s);
   RowStep at((long)blockIdx.x * p.RPB + sub, a.T, step);
   RowIn<E, R, NV, false, EVEN> in, next;
-  if (!LEAN && at.row < rows) in.load(a, s, at);
+  if (at.row < rows) in.load(a, s, at);
   int turn = 0;
   for (long row0 = (long)blockIdx.x * p.RPB; row0 < rows; row0 += step, turn ^= 1) {
     const RowStep here = at;
     const bool live = here.row < rows;
     at.next(a.T, step);
-    if constexpr (LEAN) {
-      if (live) in.load(a, s, here);
-    } else {
-      if (at.row < rows) next.load(a, s, at);
-    }
+    if (!LEAN && at.row < rows) next.load(a, s, at);
     float y[NV][VEC], hs[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -336,6 +333,7 @@ __global__ __launch_bounds__(NT) void join_fwd_kernel(JoinArgs a, JoinShape p) {
       }
       store_slot<EVEN>((R*)a.out + here.row * D + s.at[j], y[j], s.left[j]);
     }
+    if (LEAN && at.row < rows) in.load(a, s, at);
     if (a.w_pre) {
       const float r = rsqrtf(row_sum(sq, p.TPR, red, turn) * p.inv_D + a.eps);
       if (a.rstd_pre && live && lane == 0) a.rstd_pre[here.row] = r;
@@ -360,8 +358,8 @@ __global__ __launch_bounds__(NT) void join_fwd_kernel(JoinArgs a, JoinShape p) {
 // and adds up the weights' gradients dn n, dO m, du yn over its rows in registers, then over the
 // workgroup's RPB rows and for w_post the heads in LDS; partial: [workgroup][3][D], summed in
 // order by join_sum_kernel.  With two slots a lane what the sum over the row stands between is formed
-// on both sides of it from the packed inputs, not held: 8192 rows of 8192 float32 578 us, 834 with it
-// held (and spilled); with one slot, where it fits, holding it is faster (32768 rows of 1024 bf16 121
+// on both sides of it from the packed inputs, not held: 8192 rows of 8192 float32 537 us, 834 with it
+// held (and spilled) and no row loaded ahead; with one slot, where it fits, holding it is faster (32768 rows of 1024 bf16 121
 // us, 142 formed twice).
 template <typename E, typename R, int NV, int NT, bool EVEN>
 __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinArgs a, JoinShape p) {
@@ -376,17 +374,13 @@ __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinArgs a, JoinShape p) {
   float spre[NV][VEC] = {}, sscale[NV][VEC] = {}, spost[NV][VEC] = {};
   RowStep at((long)blockIdx.x * p.RPB + sub, a.T, step);
   RowIn<E, R, NV, true, EVEN> in, next;
-  if (!LEAN && at.row < rows) in.load(a, s, at);
+  if (at.row < rows) in.load(a, s, at);
   int turn = 0;
   for (long row0 = (long)blockIdx.x * p.RPB; row0 < rows; row0 += step, turn ^= 1) {
     const RowStep here = at;
     const bool live = here.row < rows;
     at.next(a.T, step);
-    if constexpr (LEAN) {
-      if (live) in.load(a, s, here);
-    } else {
-      if (at.row < rows) next.load(a, s, at);
-    }
+    if (!LEAN && at.row < rows) next.load(a, s, at);
     float yn[NV][VEC], f[NV][VEC], n[NV][VEC], e[NV][VEC], hs[NV];  // f: sigmoid(z), e: d_normed w_pre
     const auto form = [&](int j) {
       float wpost[VEC], scale[VEC], wpre[VEC];
@@ -455,6 +449,14 @@ __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinArgs a, JoinShape p) {
       }
       if (a.z) store_slot<EVEN>((E*)a.dz + here.row * D + s.at[j], dz, s.left[j]);
     }
+    typename Pack<E>::raw yk[NV];
+    float ryk[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      yk[j] = in.y[j];
+      ryk[j] = in.ry[j];
+    }
+    if (LEAN && at.row < rows) in.load(a, s, at);
     if (a.w_post) head_sums<NV>(hs, p, lane, hred, turn);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -463,7 +465,7 @@ __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinArgs a, JoinShape p) {
         const float mean = hs[j] * p.inv_d;
 #pragma unroll
         for (int v = 0; v < VEC; ++v)
-          e[j][v] = in.ry[j] * fmaf(LEAN ? -(float)in.y[j][v] * in.ry[j] : -yn[j][v], mean, e[j][v]);
+          e[j][v] = ryk[j] * fmaf(LEAN ? -(float)yk[j][v] * ryk[j] : -yn[j][v], mean, e[j][v]);
       }
       store_slot<EVEN>((E*)a.dy + (((long)here.b * a.H + s.head[j]) * a.T + here.t) * a.d + s.in[j], e[j], s.left[j]);
     }
