@@ -9,9 +9,12 @@
 // multiple of 8: EVEN kernels know there is none).  A head takes LPH slots (its last ones are empty
 // where d / 8 is not LPH): a power of 2 up to 64, so that a head's sum is a lane exchange inside an
 // aligned group, or a multiple of 64, so that no wave's slots belong to two heads and a head's sum
-// is a wave sum and a sum of LPH / 64 of them from LDS.  Slot s of a row
-// is lane s % TPR, register s / TPR.  All arithmetic is float32, rounded once at the store; the
-// backward recomputes out from y, z and the residual instead of reading its rounded value.
+// is a wave sum and a sum of LPH / 64 of them from LDS.  Slot s of a row is lane s % TPR, register
+// s / TPR.  All arithmetic is float32, rounded once at the store; the backward recomputes out from
+// y, z and the residual instead of reading its rounded value.
+//
+// Both are bound by HBM: forward 32768 rows of 4 heads of 256 bf16 (norm and gate) in 38.8 us, 5.2
+// TB/s; backward 16384 rows of 16 heads of 128 bf16, everything on, in 121 us, 4.5 TB/s.
 #include "gla_block.hpp"
 
 namespace gla {
@@ -359,8 +362,8 @@ __global__ __launch_bounds__(NT) void join_fwd_kernel(JoinArgs a, JoinShape p) {
 // workgroup's RPB rows and for w_post the heads in LDS; partial: [workgroup][3][D], summed in
 // order by join_sum_kernel.  With two slots a lane what the sum over the row stands between is formed
 // on both sides of it from the packed inputs, not held: 8192 rows of 8192 float32 537 us, 834 with it
-// held (and spilled) and no row loaded ahead; with one slot, where it fits, holding it is faster (32768 rows of 1024 bf16 121
-// us, 142 formed twice).
+// held (and spilled) and no row loaded ahead; with one slot, where it fits, holding it is faster
+// (32768 rows of 1024 bf16 121 us, 142 formed twice).
 template <typename E, typename R, int NV, int NT, bool EVEN>
 __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinArgs a, JoinShape p) {
   constexpr bool LEAN = NV > 1;

@@ -1,7 +1,8 @@
 // The elementwise gated linear recurrence, per sequence b and channel c:
 //   h_t = a_t h_{t-1} + beta(g_t) x_t,  a = exp(g),  beta = 1 | 1 - a | sqrt(1 - a^2)
 // and its backward, in one pass over the data each (2e + 4 and 3e + 8 bytes per element at e
-// bytes of dtype), bound by HBM.
+// bytes of dtype), bound by HBM: 256k x 1024 bf16 forward in 385 us, 5.6 TB/s; 4 x 4096 x 2048
+// backward in 106 us, 4.4 TB/s.
 //
 // A tile is NW waves of TW tokens each by 64 channels; a lane holds its wave's TW tokens of a
 // channel in registers.  The recurrence over a run of tokens is the map h -> A h + B with A the
