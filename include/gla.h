@@ -450,7 +450,7 @@ gla_status gla_step(const void* q, const gla_strides* q_st, const void* k, const
  * residual and out have stream_dtype (GLA_F32, or GLA_BF16 with a bf16 dtype); the weights are
  * float32.  All arithmetic is float32, and normed is formed from out before its rounding.
  * out may be the residual itself (contiguous; a forward-only call).  rstd_post [B][T][H] and
- * rstd_pre [B][T] (float32, for gla_join_bwd) may be NULL.  eps > 0.  H d <= 8192.
+ * rstd_pre [B][T] (float32, for gla_join_bwd) may be NULL.  eps > 0.  H d <= 8192 and H <= 2048.
  */
 gla_status gla_join_fwd(const void* y, const gla_strides* y_st, const void* z, const gla_strides* z_st,
                         const float* w_post, const void* residual, const gla_strides* r_st, const float* scale,

@@ -13,6 +13,7 @@ constexpr int kRecurTile = 256;   // tokens of a scan's tile where there are sev
 constexpr int kMaxStride = 1 << 24;
 constexpr int kStepMaxDk = 256;   // key rows a gla_step workgroup can hold
 constexpr int kJoinMaxRow = 8192; // H * d a gla_join row may have
+constexpr int kJoinMaxHeads = 2048;  // and heads: a head takes a slot of its own however narrow it is
 
 struct Strides {  // in elements; the last dimension is contiguous
   long long b, h, t;

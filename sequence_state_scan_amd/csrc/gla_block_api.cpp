@@ -226,6 +226,8 @@ gla_status check_join(const char* fn, int B, int H, int T, int d, int act, int d
     return set_error(GLA_ERR_UNSUPPORTED, "%s: a bf16 stream with float32 blocks", fn);
   if ((long long)H * d > gla::kJoinMaxRow)
     return set_error(GLA_ERR_UNSUPPORTED, "%s: rows of H*d=%lld are above %d", fn, (long long)H * d, gla::kJoinMaxRow);
+  if (H > gla::kJoinMaxHeads)
+    return set_error(GLA_ERR_UNSUPPORTED, "%s: rows of H=%d heads are above %d", fn, H, gla::kJoinMaxHeads);
   return GLA_OK;
 }
 

@@ -36,6 +36,10 @@ static int pow2_up(int n) {
 // lane (padded heads four): 8192 rows of 8192 forward bf16 186 us, float32 275; with 1024 lanes of
 // one slot 198 and 293.  The backward's registers (one slot a lane 190, two 240) fit 8 waves on a CU.
 constexpr int kJoinThreads = 256, kJoinLanes = 512;
+// A lane has at most four slots.  Heads of up to 8 values take one each, kJoinMaxHeads at most.  One of
+// n = ceil(d / 8) > 1 slots is padded to at most 2 (n - 1), fewer than 2 d / 8, so a row of such heads has
+// fewer than 2 kJoinMaxRow / 8.
+static_assert(kJoinMaxHeads <= 4 * kJoinLanes && 2 * kJoinMaxRow / VEC <= 4 * kJoinLanes, "a lane's slots");
 
 static JoinShape join_shape(int H, int d) {
   JoinShape s;

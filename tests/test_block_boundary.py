@@ -124,6 +124,17 @@ def test_sizes(lib):
         gla.join_workspace_size(1, 2, 1, 5000)
 
 
+@pytest.mark.parametrize("H,d", [(2049, 3), (4096, 2), (2049, 1), (8192, 1)])
+def test_join_refuses_more_heads_than_a_row_has_slots(lib, H, d):
+    # a head takes a slot of 8 values however narrow it is, and the kernels hold 2048 slots of a row
+    for fn, table in ((lib.gla_join_fwd, JOIN_FWD), (lib.gla_join_bwd, JOIN_BWD)):
+        assert call(fn, *table, H=H, d=d) == UN
+        assert b"heads are above 2048" in lib.gla_last_error()
+    assert lib.gla_join_workspace_size(1, H, 1, d) == 0 and b"heads are above 2048" in lib.gla_last_error()
+    for h in (2048, 2047):
+        assert lib.gla_join_workspace_size(1, h, 1, d) > 0
+
+
 def test_python_refuses_host_tensors_and_bad_arguments():
     x = torch.zeros(2, 3, 4)
     with pytest.raises(ValueError, match="device tensors only"):

@@ -755,3 +755,10 @@ def test_offsets_past_32_bits():
     diff = (h[:, -500:].double() - ref.double()).abs()
     assert (diff <= tol[:, None] + 2 * step * (ref.double().abs() + tol[:, None])).all()
     assert not h[:, :-500].any()
+
+
+@pytest.mark.parametrize("dt,st", [(F32, F32), (BF16, F32)])
+@pytest.mark.parametrize("B,H,T,d", [(1, 2048, 2, 4), (1, 2048, 3, 3), (2, 2047, 2, 1), (1, 1100, 2, 2)])
+def test_join_with_many_narrow_heads(B, H, T, d, dt, st):
+    y, a, d_out, d_normed = join_inputs(B + T + d, B, H, T, d, dt, st)
+    check_join(y, a, d_out, d_normed, "silu", "B%d H%d T%d d%d" % (B, H, T, d))
