@@ -762,3 +762,25 @@ def test_offsets_past_32_bits():
 def test_join_with_many_narrow_heads(B, H, T, d, dt, st):
     y, a, d_out, d_normed = join_inputs(B + T + d, B, H, T, d, dt, st)
     check_join(y, a, d_out, d_normed, "silu", "B%d H%d T%d d%d" % (B, H, T, d))
+
+
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("dk,dv", [(48, 32), (100, 17), (1, 5), (17, 64), (192, 8), (64, 32)])
+def test_step_with_a_value_that_is_not_finite(dk, dv, dt, bad):
+    # one column of v at token 0 is not finite; a reset at token 1 drops it.  k and q are positive, so
+    # that the sums over the rows are infinite, not NaN, where the formula says so
+    B, H, n = 2, 2, 4
+    q, k, v, g, pool = step_inputs(dk, B, H, n, dk, dv, dt)
+    q, k = q.abs() + 0.5, k.abs() + 0.5
+    v[:, :, 0, 0] = bad
+    g[:, :, 1] = -math.inf
+    state = pool.cuda()
+    o = gla.gla_step(q.cuda(), k.cuda(), v.cuda(), g.cuda(), state).cpu().double()
+    first = o[:, :, 0, 0]
+    assert (torch.isnan(first) if math.isnan(bad) else first == bad).all()
+    v[:, :, 0, 0] = 0
+    ref, tol, S, tolS = step_reference(q.double(), k.double(), v.double(), g.double(), pool[:B].double())
+    o[:, :, 0, 0] = ref[:, :, 0, 0]
+    inside("o", o, ref, (tol + half_step(dt) * ref.abs()) * (1 + half_step(dt)))
+    inside("state", state[:B], S, tolS + U * S.abs())
