@@ -358,6 +358,8 @@ gla_status gla_chunk_bwd_from(const void* q, const void* k, const void* v, const
  *     the strides of the dimensions before the last, in elements, none negative; NULL means
  *     contiguous.  A dimension the tensor does not have is ignored (h for [B][T][D], t and h for
  *     [B][D]).  Rows on 16 bytes are read fastest; any alignment of the element type is accepted.
+ *   - Outputs, states and workspaces must share no memory with inputs or each other (a view's gaps do not
+ *     count); such calls are refused.
  *   - Any size >= 1 up to the limits named at each call; no multiples are required.
  *   - The stream's device is the current one when a call is made (the Python calls see to that).
  *   - lens and slots are int arrays on the device.  Their values are checked there, by the kernels.

@@ -28,18 +28,67 @@ bool strides(const gla_strides* st, long long b, long long h, long long t, Strid
   return out->b >= 0 && out->h >= 0 && out->t >= 0;
 }
 
+typedef __int128 wide;  // bytes: a caller's strides may reach past 64 bits
+
+// The memory of a tensor: up to three strided dimensions over runs of `run` bytes.  No memory where it is null.
+struct Region {
+  wide base = 0, run = 0;
+  int dims = 0;
+  wide n[3], step[3];
+
+  // count contiguous elements of e bytes
+  Region(const void* p, wide count, int e) : base((unsigned long long)p), run(p ? count * e : 0) {}
+  Region(const float* p, wide count) : Region(p, count, 4) {}
+  // a [b][h][t] view of rows of `last` elements
+  Region(const void* p, int e, int b, int h, int t, int last, const Strides& st) : Region(p, last, e) {
+    const long long count[3] = {b, h, t}, by[3] = {st.b, st.h, st.t};
+    for (int i = 0; i < 3; ++i) {
+      if (count[i] == 1 || by[i] == 0) continue;  // one place
+      int at = dims++;
+      for (; at > 0 && step[at - 1] < (wide)by[i] * e; --at) {  // the largest step first
+        n[at] = n[at - 1];
+        step[at] = step[at - 1];
+      }
+      n[at] = count[i];
+      step[at] = (wide)by[i] * e;
+    }
+  }
+
+  wide extent(int from) const {
+    wide s = run;
+    for (int i = from; i < dims; ++i) s += (n[i] - 1) * step[i];
+    return s;
+  }
+  // Whether the part from dimension `at` on, placed at p, has a byte in [lo, hi).  What lies in a view's
+  // gaps does not count, unless its steps are shorter than what they step over.
+  bool meets(wide p, int at, wide lo, wide hi) const {
+    const wide e = extent(at + 1);
+    if (at == dims) return p < hi && p + run > lo;
+    wide first = p + e > lo ? 0 : (lo - e - p) / step[at] + 1, last = p >= hi ? -1 : (hi - 1 - p) / step[at];
+    if (last > n[at] - 1) last = n[at] - 1;
+    if (first > last) return false;
+    if (step[at] < e || last - first >= 2) return true;  // of three in a row the second lies inside
+    return meets(p + first * step[at], at + 1, lo, hi) || (last > first && meets(p + last * step[at], at + 1, lo, hi));
+  }
+};
+
+// Whether an output (all contiguous) shares memory with an input or another output.
 template <int N, int M>
-bool aliased(const void* const (&outs)[N], const void* const (&ins)[M]) {
-  for (const void* o : outs) {
-    if (!o) continue;
-    for (const void* i : ins)
-      if (o == i) return true;
-    int same = 0;
-    for (const void* p : outs) same += p == o;
-    if (same > 1) return true;
+bool overlaps(const Region (&outs)[N], const Region (&ins)[M]) {
+  wide ends[M];
+  for (int i = 0; i < M; ++i) ends[i] = ins[i].run ? ins[i].base + ins[i].extent(0) : 0;
+  for (int o = 0; o < N; ++o) {
+    const wide lo = outs[o].base, hi = lo + outs[o].run;
+    if (lo == hi) continue;
+    for (int i = 0; i < M; ++i)
+      if (ins[i].base < hi && ends[i] > lo && ins[i].meets(ins[i].base, 0, lo, hi)) return true;
+    for (int q = 0; q < o; ++q)
+      if (outs[q].run && outs[q].base < hi && outs[q].base + outs[q].run > lo) return true;
   }
   return false;
 }
+
+int size_of(int dtype) { return dtype == GLA_BF16 ? 2 : 4; }
 
 #define GLA_TRY(e)                     \
   do {                                 \
@@ -93,8 +142,12 @@ gla_status gla_recur_fwd(const void* x, const gla_strides* x_st, const float* g,
     return set_error(GLA_ERR_INVALID_ARG, "%s: strides must not be negative", fn);
   if (T > 1 && (a.xs.t >= gla::kMaxStride || a.gs.t >= gla::kMaxStride))
     return set_error(GLA_ERR_UNSUPPORTED, "%s: token strides must be below %d elements", fn, gla::kMaxStride);
-  if (aliased<4, 4>({h, chunk_in, h_final, workspace}, {x, g, h0, lens}))
-    return set_error(GLA_ERR_INVALID_ARG, "%s: outputs and the workspace must not alias inputs or each other", fn);
+  GLA_TRY(check_recur_workspace(fn, B, T, D, workspace, workspace_size));
+  const int e = size_of(dtype);
+  const wide n = (wide)B * T * D, row = (wide)B * D, states = (wide)B * ((T + gla::kRecurChunk - 1LL) / gla::kRecurChunk) * D;
+  if (overlaps<4, 4>({{h, n, e}, {chunk_in, states}, {h_final, row}, {workspace, (wide)recur_bytes(B, T, D), 1}},
+                     {{x, e, B, 1, T, D, a.xs}, {g, 4, B, 1, T, D, a.gs}, {h0, row}, {lens, B, 4}}))
+    return set_error(GLA_ERR_INVALID_ARG, "%s: outputs and the workspace must not overlap inputs or each other", fn);
   a.x = x;
   a.g = g;
   a.h0 = h0;
@@ -107,7 +160,6 @@ gla_status gla_recur_fwd(const void* x, const gla_strides* x_st, const float* g,
   a.D = D;
   a.mode = mode;
   a.dtype = dtype;
-  GLA_TRY(check_recur_workspace(fn, B, T, D, workspace, workspace_size));
   a.words = static_cast<unsigned long long*>(workspace);
   return launched(fn, gla::launch_recur_fwd(a, static_cast<hipStream_t>(stream)));
 }
@@ -126,8 +178,13 @@ gla_status gla_recur_bwd(const void* x, const gla_strides* x_st, const float* g,
     return set_error(GLA_ERR_INVALID_ARG, "%s: strides must not be negative", fn);
   if (T > 1 && (a.xs.t >= gla::kMaxStride || a.gs.t >= gla::kMaxStride || a.dhs.t >= gla::kMaxStride))
     return set_error(GLA_ERR_UNSUPPORTED, "%s: token strides must be below %d elements", fn, gla::kMaxStride);
-  if (aliased<4, 6>({dx, dg, dh0, workspace}, {x, g, dh, chunk_in, lens, dhT}))
-    return set_error(GLA_ERR_INVALID_ARG, "%s: outputs and the workspace must not alias inputs or each other", fn);
+  GLA_TRY(check_recur_workspace(fn, B, T, D, workspace, workspace_size));
+  const int e = size_of(dtype);
+  const wide n = (wide)B * T * D, row = (wide)B * D, states = (wide)B * ((T + gla::kRecurChunk - 1LL) / gla::kRecurChunk) * D;
+  if (overlaps<4, 6>({{dx, n, e}, {dg, n}, {dh0, row}, {workspace, (wide)recur_bytes(B, T, D), 1}},
+                     {{x, e, B, 1, T, D, a.xs}, {g, 4, B, 1, T, D, a.gs}, {dh, e, B, 1, T, D, a.dhs}, {chunk_in, states},
+                      {lens, B, 4}, {dhT, row}}))
+    return set_error(GLA_ERR_INVALID_ARG, "%s: outputs and the workspace must not overlap inputs or each other", fn);
   a.x = x;
   a.g = g;
   a.dh = dh;
@@ -142,7 +199,6 @@ gla_status gla_recur_bwd(const void* x, const gla_strides* x_st, const float* g,
   a.D = D;
   a.mode = mode;
   a.dtype = dtype;
-  GLA_TRY(check_recur_workspace(fn, B, T, D, workspace, workspace_size));
   a.words = static_cast<unsigned long long*>(workspace);
   return launched(fn, gla::launch_recur_bwd(a, static_cast<hipStream_t>(stream)));
 }
@@ -158,8 +214,10 @@ gla_status gla_recur_step(const void* x, const gla_strides* x_st, const float* g
   gla::RecurStepArgs a{};
   if (!strides(x_st, D, 0, 0, &a.xs) || !strides(g_st, D, 0, 0, &a.gs))
     return set_error(GLA_ERR_INVALID_ARG, "%s: strides must not be negative", fn);
-  if (aliased<2, 3>({state, h}, {x, g, slots}))
-    return set_error(GLA_ERR_INVALID_ARG, "%s: h and state must not alias inputs or each other", fn);
+  const int e = size_of(dtype);
+  if (overlaps<2, 3>({{state, (wide)n_slots * D}, {h, (wide)B * D, e}},
+                     {{x, e, B, 1, 1, D, a.xs}, {g, 4, B, 1, 1, D, a.gs}, {slots, B, 4}}))
+    return set_error(GLA_ERR_INVALID_ARG, "%s: h and state must not overlap inputs or each other", fn);
   a.x = x;
   a.g = g;
   a.state = state;
@@ -189,12 +247,15 @@ gla_status gla_step(const void* q, const gla_strides* q_st, const void* k, const
   if (!strides(q_st, HN * dk, N * dk, dk, &a.qs) || !strides(k_st, HN * dk, N * dk, dk, &a.ks) ||
       !strides(v_st, HN * dv, N * dv, dv, &a.vs) || !strides(g_st, HN * dk, N * dk, dk, &a.gs))
     return set_error(GLA_ERR_INVALID_ARG, "%s: strides must not be negative", fn);
-  if (aliased<2, 5>({state, o}, {q, k, v, g, slots}))
-    return set_error(GLA_ERR_INVALID_ARG, "%s: o and state must not alias inputs or each other", fn);
   if (dk > gla::kStepMaxDk) return set_error(GLA_ERR_UNSUPPORTED, "%s: dk=%d is above %d", fn, dk, gla::kStepMaxDk);
   if ((long long)B * H > kMaxGrid / ((dv + 15) / 16))
     return set_error(GLA_ERR_UNSUPPORTED, "%s: B*H=%lld heads of dv=%d are too many for one call", fn,
                      (long long)B * H, dv);
+  const int e = size_of(dtype);
+  if (overlaps<2, 5>({{state, (wide)n_slots * H * dk * dv}, {o, (wide)B * HN * dv, e}},
+                     {{q, e, B, H, n, dk, a.qs}, {k, e, B, H, n, dk, a.ks}, {v, e, B, H, n, dv, a.vs},
+                      {g, 4, B, H, n, dk, a.gs}, {slots, B, 4}}))
+    return set_error(GLA_ERR_INVALID_ARG, "%s: o and state must not overlap inputs or each other", fn);
   a.q = q;
   a.k = k;
   a.v = v;
@@ -263,8 +324,12 @@ gla_status gla_join_fwd(const void* y, const gla_strides* y_st, const void* z, c
   const bool in_place = out == residual;
   if (in_place && (a.rs.t != D || (B > 1 && a.rs.b != n * D)))
     return set_error(GLA_ERR_INVALID_ARG, "%s: an out in the residual's place needs a contiguous residual", fn);
-  if (aliased<4, 6>({out, normed, rstd_post, rstd_pre}, {y, z, w_post, in_place ? nullptr : residual, scale, w_pre}))
-    return set_error(GLA_ERR_INVALID_ARG, "%s: outputs must not alias inputs or each other", fn);
+  const int e = size_of(dtype), se = size_of(stream_dtype);
+  const wide rows = (wide)B * T;
+  if (overlaps<4, 6>({{out, rows * D, se}, {normed, rows * D, e}, {rstd_post, rows * H}, {rstd_pre, rows}},
+                     {{y, e, B, H, T, d, a.ys}, {z, e, B, 1, T, (int)D, a.zs}, {w_post, d},
+                      {in_place ? nullptr : residual, se, B, 1, T, (int)D, a.rs}, {scale, D}, {w_pre, D}}))
+    return set_error(GLA_ERR_INVALID_ARG, "%s: outputs must not overlap inputs or each other", fn);
   a.y = y;
   a.z = z;
   a.residual = residual;
@@ -314,9 +379,14 @@ gla_status gla_join_bwd(const void* y, const gla_strides* y_st, const void* z, c
       !strides(residual ? r_st : nullptr, n * D, 0, D, &a.rs) || !strides(d_out ? do_st : nullptr, n * D, 0, D, &a.dos) ||
       !strides(d_normed ? dn_st : nullptr, n * D, 0, D, &a.dns))
     return set_error(GLA_ERR_INVALID_ARG, "%s: strides must not be negative", fn);
-  if (aliased<7, 10>({dy, dz, d_residual, dw_post, dscale, dw_pre, workspace},
-                     {y, z, w_post, residual, scale, w_pre, rstd_post, rstd_pre, d_out, d_normed}))
-    return set_error(GLA_ERR_INVALID_ARG, "%s: outputs and the workspace must not alias inputs or each other", fn);
+  const int e = size_of(dtype), se = size_of(stream_dtype), W = (int)D;
+  const wide rows = (wide)B * T;
+  if (overlaps<7, 10>({{dy, rows * D, e}, {dz, rows * D, e}, {d_residual, rows * D, se}, {dw_post, d}, {dscale, D},
+                       {dw_pre, D}, {workspace, (wide)need, 1}},
+                      {{y, e, B, H, T, d, a.ys}, {z, e, B, 1, T, W, a.zs}, {w_post, d}, {residual, se, B, 1, T, W, a.rs},
+                       {scale, D}, {w_pre, D}, {rstd_post, rows * H}, {rstd_pre, rows}, {d_out, se, B, 1, T, W, a.dos},
+                       {d_normed, e, B, 1, T, W, a.dns}}))
+    return set_error(GLA_ERR_INVALID_ARG, "%s: outputs and the workspace must not overlap inputs or each other", fn);
   a.y = y;
   a.z = z;
   a.residual = residual;

@@ -135,6 +135,59 @@ def test_join_refuses_more_heads_than_a_row_has_slots(lib, H, d):
         assert lib.gla_join_workspace_size(1, h, 1, d) > 0
 
 
+def _apart(table):
+    """The table with its pointers so far apart that no tensor of the defaults reaches another."""
+    names, d = table
+    far = dict(d)
+    for i, n in enumerate(names):
+        if isinstance(d[n], ctypes.c_void_p):
+            far[n] = ctypes.c_void_p((i + 1) << 32)
+    return names, far
+
+
+# (call, table, the tensor that is moved, the one it is moved into, bytes from that one's start): the moved
+# one's first byte on another's last, or its last byte on another's first
+OVERLAPS = [
+    ("gla_recur_fwd", RECUR_FWD, "h", "x", 64), ("gla_recur_fwd", RECUR_FWD, "h", "x", 2 * 300 * 64 * 2 - 2),
+    ("gla_recur_fwd", RECUR_FWD, "h", "x", -2 * 300 * 64 * 2 + 2), ("gla_recur_fwd", RECUR_FWD, "h", "h0", 508),
+    ("gla_recur_fwd", RECUR_FWD, "chunk_in", "h", -2 * 3 * 64 * 4 + 2), ("gla_recur_fwd", RECUR_FWD, "h_final", "g", 4),
+    ("gla_recur_fwd", RECUR_FWD, "ws", "g", 2 * 300 * 64 * 4 - 8), ("gla_recur_fwd", RECUR_FWD, "lens", "h_final", 508),
+    ("gla_recur_bwd", RECUR_BWD, "dx", "dh", 128), ("gla_recur_bwd", RECUR_BWD, "dg", "chunk_in", 2 * 3 * 64 * 4 - 4),
+    ("gla_recur_bwd", RECUR_BWD, "dh0", "dg", 2 * 300 * 64 * 4 - 4), ("gla_recur_bwd", RECUR_BWD, "dhT", "dh0", 508),
+    ("gla_recur_bwd", RECUR_BWD, "ws", "lens", -8),
+    ("gla_recur_step", RECUR_STEP, "state", "g", -4 * 64 * 4 + 4), ("gla_recur_step", RECUR_STEP, "h", "state", 1020),
+    ("gla_recur_step", RECUR_STEP, "slots", "h", 252),
+    ("gla_step", STEP, "o", "q", 510), ("gla_step", STEP, "state", "v", -4 * 2 * 64 * 64 * 4 + 4),
+    ("gla_step", STEP, "o", "state", 4 * 2 * 64 * 64 * 4 - 2), ("gla_step", STEP, "slots", "state", 8),
+    ("gla_join_fwd", JOIN_FWD, "out", "y", 2), ("gla_join_fwd", JOIN_FWD, "out", "residual", 256),
+    ("gla_join_fwd", JOIN_FWD, "normed", "out", 2 * 10 * 128 * 2 - 2), ("gla_join_fwd", JOIN_FWD, "w_post", "normed", 16),
+    ("gla_join_fwd", JOIN_FWD, "rstd_post", "z", -2 * 10 * 2 * 4 + 4), ("gla_join_fwd", JOIN_FWD, "rstd_pre", "scale", 508),
+    ("gla_join_bwd", JOIN_BWD, "dy", "y", 2 * 10 * 128 * 2 - 2), ("gla_join_bwd", JOIN_BWD, "dz", "d_out", 2),
+    ("gla_join_bwd", JOIN_BWD, "d_residual", "d_normed", -2), ("gla_join_bwd", JOIN_BWD, "dw_post", "w_post", 252),
+    ("gla_join_bwd", JOIN_BWD, "dscale", "w_pre", 508), ("gla_join_bwd", JOIN_BWD, "dw_pre", "dscale", 508),
+    ("gla_join_bwd", JOIN_BWD, "ws", "rstd_pre", 76), ("gla_join_bwd", JOIN_BWD, "dy", "ws", 3 * 128 * 4 - 4)]
+
+
+@pytest.mark.parametrize("name,table,moved,into,by", OVERLAPS, ids=lambda v: str(v) if not isinstance(v, tuple) else "")
+def test_an_output_inside_another_tensor_is_refused(lib, name, table, moved, into, by):
+    table = _apart(table)
+    at = ctypes.c_void_p(table[1][into].value + by)
+    assert call(getattr(lib, name), *table, **{moved: at}) == E
+    assert b"must not overlap inputs or each other" in lib.gla_last_error()
+
+
+@pytest.mark.parametrize("st,by", [
+    (strides(1 << 20, 0, 64), (1 << 21) + 100),       # inside the second sequence's rows
+    (strides(1 << 20, 0, 640), 1280 * 299 + 126),     # on the last element of the first one's last row
+    (strides(64, 0, 1 << 20), (299 << 21) + 128),     # token-major: the last token's second sequence
+    (strides(1 << 20, 0, 0), 0), (strides(0, 0, 64), 300 * 128 - 2)])
+def test_an_output_inside_a_views_rows_is_refused(lib, st, by):
+    table = _apart(RECUR_FWD)
+    at = ctypes.c_void_p(table[1]["x"].value + by)
+    assert call(lib.gla_recur_fwd, *table, x_st=st, h=at) == E
+    assert b"must not overlap inputs or each other" in lib.gla_last_error()
+
+
 def test_python_refuses_host_tensors_and_bad_arguments():
     x = torch.zeros(2, 3, 4)
     with pytest.raises(ValueError, match="device tensors only"):

@@ -784,3 +784,46 @@ def test_step_with_a_value_that_is_not_finite(dk, dv, dt, bad):
     o[:, :, 0, 0] = ref[:, :, 0, 0]
     inside("o", o, ref, (tol + half_step(dt) * ref.abs()) * (1 + half_step(dt)))
     inside("state", state[:B], S, tolS + U * S.abs())
+
+
+def test_outputs_in_a_views_gaps_and_next_to_inputs():
+    # out between two of y's sequences; x, g and h side by side.  Nothing overlaps, and the results are those of
+    # separate tensors; one element further it does
+    B, H, T, d = 3, 2, 20, 32
+    y, a, _, _ = join_inputs(3, B, H, T, d, BF16, BF16)
+    gpu = {n: t.cuda() for n, t in a.items()}
+    want = gla.gla_join_fwd(y.cuda(), eps=EPS, **gpu)
+    n = B * H * T * d
+    flat = torch.zeros(4 * n, dtype=BF16, device="cuda")
+    view = flat[:3 * n].view(B, n)[:, :n // B].view(B, H, T, d)
+    view.copy_(y)
+    one = gla.gla_join_fwd(view[::2], eps=EPS, out=flat[n:n + 2 * n // 3].view(2, T, H * d),
+                           **{k: t if t.dim() == 1 else t[::2] for k, t in gpu.items()})
+    assert torch.equal(one["out"], want["out"][::2]) and torch.equal(one["normed"], want["normed"][::2])
+    x, g, _, _, _ = recur_inputs(4, 2, 70, 64, F32)
+    want, _, last = gla.gla_recur_fwd(x.cuda(), g.cuda())
+    m = x.numel()
+    both = torch.zeros(3 * m, device="cuda")
+    both[:m], both[m:2 * m] = x.cuda().flatten(), g.cuda().flatten()
+    h, _, f = gla.gla_recur_fwd(both[:m].view(2, 70, 64), both[m:2 * m].view(2, 70, 64), h=both[2 * m:].view(2, 70, 64))
+    assert torch.equal(h, want) and torch.equal(f, last)
+    for lo in (2 * m - 1, m - 4):
+        with pytest.raises(gla.GLAError, match="must not overlap"):
+            gla.gla_recur_fwd(both[:m].view(2, 70, 64), both[m:2 * m].view(2, 70, 64), h=both[lo:lo + m].view(2, 70, 64))
+
+
+@pytest.mark.parametrize("B", [1, 2])
+def test_an_output_between_a_views_rows(B):
+    # x is every other block of `wide`; h takes a whole block between
+    T, D = 3, 16
+    wide = torch.zeros(2 * B, B * T, D, device="cuda")
+    x = wide[::2][:, :T]
+    x.copy_(torch.randn(B, T, D))
+    g = -torch.rand(B, T, D, device="cuda")
+    want = gla.gla_recur_fwd(x.clone(), g)[0]
+    h = wide[1].view(B, T, D)
+    assert torch.equal(gla.gla_recur_fwd(x, g, h=h)[0], want) and torch.equal(wide[1].view(B, T, D), want)
+    if B > 1:
+        over = wide.view(-1)[B * T * D + D:][:B * T * D].view(B, T, D)  # ends in the next block's first row
+        with pytest.raises(gla.GLAError, match="must not overlap"):
+            gla.gla_recur_fwd(x, g, h=over)
