@@ -185,18 +185,19 @@ __device__ __forceinline__ void load_weights(const float* w, int at, int in, int
   }
 }
 
-// The row a workgroup's lane group is at: (b, t) stepped without a division.
+// The row a workgroup's lane group is at: (b, t) stepped without a division.  Unsigned: t + dt stays below
+// 2^32 for every T, and passes 2^31 for the longest ones.
 struct RowStep {
   long row;
-  int b, t, db, dt;
-  __device__ RowStep(long first, int T, long step) {
+  unsigned b, t, db, dt;
+  __device__ RowStep(long first, unsigned T, long step) {
     row = first;
-    b = (int)(first / T);
-    t = (int)(first - (long)b * T);
-    db = (int)(step / T);
-    dt = (int)(step - (long)db * T);
+    b = (unsigned)(first / T);
+    t = (unsigned)(first - (long)b * T);
+    db = (unsigned)(step / T);
+    dt = (unsigned)(step - (long)db * T);
   }
-  __device__ void next(int T, long step) {
+  __device__ void next(unsigned T, long step) {
     row += step;
     b += db;
     t += dt;

@@ -827,3 +827,21 @@ def test_an_output_between_a_views_rows(B):
         over = wide.view(-1)[B * T * D + D:][:B * T * D].view(B, T, D)  # ends in the next block's first row
         with pytest.raises(gla.GLAError, match="must not overlap"):
             gla.gla_recur_fwd(x, g, h=over)
+
+
+def test_join_with_the_longest_sequences():
+    # T = 2^31 - 1: a row's step passes 2^31 at the first sequence's end.  With every part left out out is y
+    # and dy is d_out
+    B, T = 2, 2 ** 31 - 1
+    y = torch.empty(B, 1, T, 1, dtype=BF16, device="cuda")
+    y.view(torch.int16).view(-1)[:] = 0
+    ends = torch.randn(2, 1 << 20, device="cuda").to(BF16)  # around the sequences' border and at the far end
+    flat = y.view(-1)
+    flat[T - (1 << 19):T + (1 << 19)] = ends[0]
+    flat[-(1 << 20):] = ends[1]
+    f = gla.gla_join_fwd(y)
+    out = f["out"].view(-1)
+    step = 1 << 28
+    assert all(torch.equal(out[i:i + step], flat[i:i + step]) for i in range(0, flat.numel(), step))
+    dy = gla.gla_join_bwd(y, f, d_out=y.view(B, T, 1))["dy"].view(-1)
+    assert all(torch.equal(dy[i:i + step], flat[i:i + step]) for i in range(0, flat.numel(), step))
