@@ -101,7 +101,7 @@ gla_status check_recur(const char* fn, int B, int T, int D, int mode, int dtype)
   if (mode < GLA_RECUR_PLAIN || mode > GLA_RECUR_NORM)
     return set_error(GLA_ERR_INVALID_ARG, "%s: unknown mode %d", fn, mode);
   GLA_TRY(check_dtype(fn, dtype));
-  const long long tiles = (long long)B * ((D + 63) / 64);
+  const long long tiles = B * ((D + 63LL) / 64);
   if (B > 65535 || D >= gla::kMaxStride || tiles > kMaxGrid || tiles * (((long long)T + gla::kRecurTile - 1) / gla::kRecurTile) > kMaxGrid)
     return set_error(GLA_ERR_UNSUPPORTED, "%s: B=%d, T=%d, D=%d are too many for one call", fn, B, T, D);
   return GLA_OK;
@@ -248,7 +248,7 @@ gla_status gla_step(const void* q, const gla_strides* q_st, const void* k, const
       !strides(v_st, HN * dv, N * dv, dv, &a.vs) || !strides(g_st, HN * dk, N * dk, dk, &a.gs))
     return set_error(GLA_ERR_INVALID_ARG, "%s: strides must not be negative", fn);
   if (dk > gla::kStepMaxDk) return set_error(GLA_ERR_UNSUPPORTED, "%s: dk=%d is above %d", fn, dk, gla::kStepMaxDk);
-  if ((long long)B * H > kMaxGrid / ((dv + 15) / 16))
+  if ((long long)B * H > kMaxGrid / ((dv + 15LL) / 16))
     return set_error(GLA_ERR_UNSUPPORTED, "%s: B*H=%lld heads of dv=%d are too many for one call", fn,
                      (long long)B * H, dv);
   const int e = size_of(dtype);

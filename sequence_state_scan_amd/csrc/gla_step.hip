@@ -66,7 +66,7 @@ __global__ __launch_bounds__(256) void step_kernel(StepArgs a) {
 #pragma unroll
     for (int v = 0; v < VEC; ++v) fill[v] = slot == -1 ? 0.f : __builtin_nanf("");
     if (col)
-      for (int t = rg; t < a.n; t += 16) store_row<E, VEC>(o + (long)t * a.dv, fill);
+      for (long t = rg; t < a.n; t += 16) store_row<E, VEC>(o + t * a.dv, fill);  // t + 16 may pass 2^31
     return;
   }
   __shared__ float red[2][4][TC];

@@ -845,3 +845,17 @@ def test_join_with_the_longest_sequences():
     assert all(torch.equal(out[i:i + step], flat[i:i + step]) for i in range(0, flat.numel(), step))
     dy = gla.gla_join_bwd(y, f, d_out=y.view(B, T, 1))["dy"].view(-1)
     assert all(torch.equal(dy[i:i + step], flat[i:i + step]) for i in range(0, flat.numel(), step))
+
+
+def test_step_fills_the_longest_call():
+    # a row that is left out, n = 2^31 - 1 tokens of one value: zeros up to the last, nothing behind
+    n = 2 ** 31 - 1
+    one = torch.ones(1, 1, 1, 1, dtype=BF16, device="cuda").expand(1, 1, n, 1)
+    g = torch.zeros(1, 1, 1, 1, device="cuda").expand(1, 1, n, 1)
+    whole = torch.ones(n + 1025, dtype=BF16, device="cuda")
+    o = whole[1024:-1].view(1, 1, n, 1)
+    gla.gla_step(one, one, one, g, torch.zeros(1, 1, 1, 1, device="cuda"),
+                 slots=torch.tensor([-1], dtype=torch.int32, device="cuda"), o=o)
+    step = 1 << 28
+    assert not any(whole[i:min(i + step, 1024 + n)].any() for i in range(1024, 1024 + n, step))
+    assert (whole[:1024] == 1).all() and whole[-1] == 1
