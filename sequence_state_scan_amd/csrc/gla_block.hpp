@@ -157,10 +157,9 @@ __device__ __forceinline__ float input_factor(float g, float a) {
   if constexpr (MODE == GLA_RECUR_LERP) return one_minus_decay(g, a);
   return __builtin_amdgcn_sqrtf(one_minus_decay(2.f * g, a * a));  // the instruction's: one step off at most
 }
-// Its derivative by g (zero where the norm's factor is zero, at g = 0).
+// Its derivative by g (zero where the norm's factor is zero, at g = 0).  The plain factor has none.
 template <int MODE>
 __device__ __forceinline__ float input_factor_slope(float a, float beta) {
-  if constexpr (MODE == GLA_RECUR_PLAIN) return 0.f;
   if constexpr (MODE == GLA_RECUR_LERP) return -a;
   return beta > 0.f ? -a * a * __builtin_amdgcn_rcpf(beta) : 0.f;
 }

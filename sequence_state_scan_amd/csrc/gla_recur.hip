@@ -309,7 +309,9 @@ __global__ __launch_bounds__(64 * NW) void recur_bwd_kernel(RecurArgs a) {
     const float at = decay(gr[i]), be = input_factor<MODE>(gr[i], at), G = (float)dr[i] + u;
     u = pass(at, G);
     const float vx = be * G;
-    const float vg = fmaf(input_factor_slope<MODE>(at, be) * (float)xr[i], G, at == 0.f ? 0.f : u * before[i]);
+    float vg = at == 0.f ? 0.f : u * before[i];
+    // a constant factor has no term, not zero times an x or G that may be infinite
+    if constexpr (MODE != GLA_RECUR_PLAIN) vg = fmaf(input_factor_slope<MODE>(at, be) * (float)xr[i], G, vg);
     if (full || t0 + i < a.T) {
       element(dx, a.D, i, cl) = (E)(full || i < left ? vx : 0.f);
       element(dg, a.D, i, cl) = full || i < left ? vg : 0.f;

@@ -859,3 +859,23 @@ def test_step_fills_the_longest_call():
     step = 1 << 28
     assert not any(whole[i:min(i + step, 1024 + n)].any() for i in range(1024, 1024 + n, step))
     assert (whole[:1024] == 1).all() and whole[-1] == 1
+
+
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("T", [10, 120, 700])
+def test_recur_plain_gate_gradient_does_not_read_the_input(T, dt, bad):
+    # beta = 1: dg_t = a_t h_{t-1} G_t whatever x_t is.  The token after is a reset, so nothing else has it
+    x, g, dh, h0, dhT = (t.cuda() for t in recur_inputs(T, 2, T, 40, dt))
+    at = [1, T // 2, T - 3]
+    g[:, [i + 1 for i in at]] = -math.inf
+    x[:, at] = 0
+    h, c, last = gla.gla_recur_fwd(x, g, h0=h0)
+    want = gla.gla_recur_bwd(x, g, dh, c, dhT=dhT)
+    y = x.clone()
+    y[:, at] = bad
+    h1, c1, last1 = gla.gla_recur_fwd(y, g, h0=h0)
+    assert torch.equal(c1, c) and torch.equal(last1, last)
+    assert (torch.isnan(h1[:, at]) if math.isnan(bad) else h1[:, at] == bad).all()
+    for s, t in zip(gla.gla_recur_bwd(y, g, dh, c1, dhT=dhT), want):
+        assert torch.isfinite(t).all() and torch.equal(s, t)
