@@ -22,9 +22,10 @@ gla_status check_dtype(const char* fn, int dtype) {
   return GLA_OK;
 }
 
-// The strides of a [b][h][t][last] tensor: the caller's, or the contiguous ones.  False if negative.
+// The strides of a [b][h][t][last] tensor: the caller's, or the contiguous ones b, h and t, which are 0 for
+// a dimension that the tensor does not have.  False if negative.
 bool strides(const gla_strides* st, long long b, long long h, long long t, Strides* out) {
-  *out = st ? Strides{st->b, st->h, st->t} : Strides{b, h, t};
+  *out = st ? Strides{st->b, h ? st->h : 0, t ? st->t : 0} : Strides{b, h, t};
   return out->b >= 0 && out->h >= 0 && out->t >= 0;
 }
 
@@ -322,7 +323,7 @@ gla_status gla_join_fwd(const void* y, const gla_strides* y_st, const void* z, c
   // out may be the residual itself (each lane reads its elements before it writes them), in the
   // same place: contiguous
   const bool in_place = out == residual;
-  if (in_place && (a.rs.t != D || (B > 1 && a.rs.b != n * D)))
+  if (in_place && ((T > 1 && a.rs.t != D) || (B > 1 && a.rs.b != n * D)))
     return set_error(GLA_ERR_INVALID_ARG, "%s: an out in the residual's place needs a contiguous residual", fn);
   const int e = size_of(dtype), se = size_of(stream_dtype);
   const wide rows = (wide)B * T;

@@ -879,3 +879,29 @@ def test_recur_plain_gate_gradient_does_not_read_the_input(T, dt, bad):
     assert (torch.isnan(h1[:, at]) if math.isnan(bad) else h1[:, at] == bad).all()
     for s, t in zip(gla.gla_recur_bwd(y, g, dh, c1, dhT=dhT), want):
         assert torch.isfinite(t).all() and torch.equal(s, t)
+
+
+def test_strides_of_dimensions_that_are_not_there():
+    # through the C calls: h of a [B][T][D] tensor, h and t of a [B][D] one may hold anything, and the token
+    # stride of a single token in the residual's place is not looked at
+    import ctypes
+    lib = gla.load_library()
+    st = lambda b, h, t: (ctypes.c_longlong * 3)(b, h, t)  # noqa: E731
+    stream = torch.cuda.current_stream().cuda_stream
+    B, T, D = 2, 5, 16
+    x, g, _, _, _ = (t.cuda() for t in recur_inputs(1, B, T, D, F32))
+    want, h = gla.gla_recur_fwd(x, g)[0], torch.empty_like(x)
+    s = st(T * D, -7, D)
+    assert lib.gla_recur_fwd(x.data_ptr(), s, g.data_ptr(), s, None, None, h.data_ptr(), None, None, B, T, D, 0, 0, None,
+                             0, stream) == 0
+    assert torch.equal(h, want)
+    one, s = torch.empty(B, D, device="cuda"), st(T * D, -1, -(1 << 40))
+    states = [torch.zeros(B, D, device="cuda") for _ in range(2)]
+    assert lib.gla_recur_step(x.data_ptr(), s, g.data_ptr(), s, states[0].data_ptr(), None, one.data_ptr(), B, D, B, 0, 0,
+                              stream) == 0
+    assert torch.equal(one, gla.gla_recur_step(x[:, 0], g[:, 0], states[1])) and torch.equal(*states)
+    y, r = torch.randn(B, 1, 1, D, device="cuda"), torch.randn(B, 1, D, device="cuda")
+    want = gla.gla_join_fwd(y, residual=r)["out"]
+    assert lib.gla_join_fwd(y.data_ptr(), None, None, None, None, r.data_ptr(), st(D, -1, 999), None, None, r.data_ptr(),
+                            None, None, None, B, 1, 1, D, 0, 1e-6, 0, 0, stream) == 0
+    assert torch.equal(r, want)
