@@ -905,3 +905,27 @@ def test_strides_of_dimensions_that_are_not_there():
     assert lib.gla_join_fwd(y.data_ptr(), None, None, None, None, r.data_ptr(), st(D, -1, 999), None, None, r.data_ptr(),
                             None, None, None, B, 1, 1, D, 0, 1e-6, 0, 0, stream) == 0
     assert torch.equal(r, want)
+
+
+@pytest.mark.parametrize("d", [64, 51])
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("off", [1, 3, 4, 8])
+def test_join_views_bit_for_bit(off, dt, d):
+    # a row's slots and sums do not depend on where it lies, so views give the contiguous tensors' bits
+    B, H, T = 2, 3, 21
+    y, a, d_out, d_normed = join_inputs(8, B, H, T, d, dt, dt)
+
+    def cut(t):
+        rows = t.transpose(1, 2).reshape(B, T, H * d) if t.dim() == 4 else t
+        wide = torch.full((B, T + 1, H * d + 2 * off + 8), math.nan, dtype=t.dtype, device="cuda")
+        view = wide[:, 1:, off:off + H * d]
+        view.copy_(rows)
+        return view.unflatten(2, (H, d)).transpose(1, 2) if t.dim() == 4 else view
+
+    res = []
+    for wrap in (cut, lambda t: t.cuda()):
+        gpu = {n: wrap(t) if t.dim() == 3 else t.cuda() for n, t in a.items()}
+        f = gla.gla_join_fwd(wrap(y), **gpu)
+        b = gla.gla_join_bwd(wrap(y), f, d_out=wrap(d_out), d_normed=wrap(d_normed), **gpu)
+        res.append({**f, **b})
+    assert all(torch.equal(t, res[1][n]) for n, t in res[0].items())
