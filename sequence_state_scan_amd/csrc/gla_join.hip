@@ -185,25 +185,25 @@ __device__ __forceinline__ void load_weights(const float* w, int at, int in, int
   }
 }
 
-// The row a workgroup's lane group is at: (b, t) stepped without a division.  Unsigned: t + dt stays below
-// 2^32 for every T, and passes 2^31 for the longest ones.
+// The row a workgroup's lane group is at: (b, t) stepped without a division.  The sums are unsigned: t + dt
+// passes 2^31 for the longest T, and b + db behind the last row.
 struct RowStep {
   long row;
-  unsigned b, t, db, dt;
-  __device__ RowStep(long first, unsigned T, long step) {
+  int b, t, db, dt;
+  __device__ RowStep(long first, int T, long step) {
     row = first;
-    b = (unsigned)(first / T);
-    t = (unsigned)(first - (long)b * T);
-    db = (unsigned)(step / T);
-    dt = (unsigned)(step - (long)db * T);
+    b = (int)(first / T);
+    t = (int)(first - (long)b * T);
+    db = (int)(step / T);
+    dt = (int)(step - (long)db * T);
   }
-  __device__ void next(unsigned T, long step) {
+  __device__ void next(int T, long step) {
     row += step;
-    b += db;
-    t += dt;
-    if (t >= T) {
-      t -= T;
-      ++b;
+    b = (int)((unsigned)b + (unsigned)db);
+    t = (int)((unsigned)t + (unsigned)dt);
+    if ((unsigned)t >= (unsigned)T) {
+      t = (int)((unsigned)t - (unsigned)T);
+      b = (int)((unsigned)b + 1u);
     }
   }
 };
