@@ -175,7 +175,9 @@ __device__ __forceinline__ int row_slot(const int* slots, int b, int n_slots) {
   return s < 0 ? -1 : s >= n_slots ? -2 : s;
 }
 // Whether an earlier row of the call names row b's slot.  Every lane of the wave calls it; apart from
-// row_slot, so that the row's loads are on their way meanwhile.
+// row_slot, so that the row's loads are on their way meanwhile.  Every wave reads b slots, which needs no
+// workspace and no order of the rows: 0.8 us of 5.7 at 256 rows of 4096, but quadratic (16384 rows of 256:
+// 50 of 63 us).
 __device__ __forceinline__ bool slot_taken(const int* slots, int b, int slot) {
   if (!slots || slot < 0) return false;
   bool dup = false;

@@ -13,8 +13,8 @@
 // s / TPR.  All arithmetic is float32, rounded once at the store; the backward recomputes out from
 // y, z and the residual instead of reading its rounded value.
 //
-// Both are bound by HBM: forward 32768 rows of 4 heads of 256 bf16 (norm and gate) in 38.8 us, 5.2
-// TB/s; backward 16384 rows of 16 heads of 128 bf16, everything on, in 121 us, 4.5 TB/s.
+// Both are bound by HBM: forward 32768 rows of 4 heads of 256 bf16 (norm and gate) in 39.6 us, 5.1
+// TB/s; backward 16384 rows of 16 heads of 128 bf16, everything on, in 117 us, 4.6 TB/s.
 #include "gla_block.hpp"
 
 namespace gla {
@@ -33,8 +33,11 @@ static int pow2_up(int n) {
 }
 
 // Lanes of a workgroup, where a row takes fewer, and of a row at most.  Rows of more slots take two a
-// lane (padded heads four): 8192 rows of 8192 forward bf16 186 us, float32 275; with 1024 lanes of
-// one slot 198 and 293.  The backward's registers (one slot a lane 190, two 240) fit 8 waves on a CU.
+// lane (padded heads four): 8192 rows of 8192 forward bf16 190 us, float32 274; with 1024 lanes of
+// one slot 198 and 293.  The backward's registers (one slot a lane 178 in bf16, 204 in float32; two 225
+// and 256, where float32 spills 6 to 10) fit 8 waves on a CU.  Four slots a lane, which only padded heads
+// reach, are far past them: the backward spills 293 to 812 and takes 1.0 ms for 8192 rows of 20 heads of
+// 320 bf16, whose bytes need 0.18; the forward (190 to 242, no spill) 157 us.
 constexpr int kJoinThreads = 256, kJoinLanes = 512;
 // A lane has at most four slots.  Heads of up to 8 values take one each, kJoinMaxHeads at most.  One of
 // n = ceil(d / 8) > 1 slots is padded to at most 2 (n - 1), fewer than 2 d / 8, so a row of such heads has
@@ -259,7 +262,9 @@ struct RowIn {
 
 // The weights at a lane's slots and the next row's inputs are held in registers (a row ahead of
 // their use) where a lane has one slot.  With more (LEAN) the weights are loaded when they are used,
-// and the next row's inputs once this row's are used up, before its last reduction.
+// and the next row's inputs once this row's are used up, before its last reduction.  In the forward that
+// is a trade: 8192 rows of 8192 bf16 192 us, 196 with the loads at the row's end; of 20 heads of 320 159
+// and 166; but one head of float32 loses (8192 wide 275 and 258, 5120 wide 172 and 162).
 template <bool LEAN, bool EVEN, int NV>
 struct Weights {
   float post[LEAN ? 1 : NV][VEC], scale[LEAN ? 1 : NV][VEC], pre[LEAN ? 1 : NV][VEC];
@@ -366,8 +371,8 @@ __global__ __launch_bounds__(NT) void join_fwd_kernel(JoinArgs a, JoinShape p) {
 // and adds up the weights' gradients dn n, dO m, du yn over its rows in registers, then over the
 // workgroup's RPB rows and for w_post the heads in LDS; partial: [workgroup][3][D], summed in
 // order by join_sum_kernel.  With two slots a lane what the sum over the row stands between is formed
-// on both sides of it from the packed inputs, not held: 8192 rows of 8192 float32 537 us, 834 with it
-// held (and spilled) and no row loaded ahead; with one slot, where it fits, holding it is faster
+// on both sides of it from the packed inputs, not held: 8192 rows of 8192 float32 533 us, 834 with it
+// held (and spilled by the hundred) and no row loaded ahead; with one slot, where it fits, holding it is faster
 // (32768 rows of 1024 bf16 121 us, 142 formed twice).
 template <typename E, typename R, int NV, int NT, bool EVEN>
 __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinArgs a, JoinShape p) {

@@ -1,8 +1,9 @@
 // The elementwise gated linear recurrence, per sequence b and channel c:
 //   h_t = a_t h_{t-1} + beta(g_t) x_t,  a = exp(g),  beta = 1 | 1 - a | sqrt(1 - a^2)
 // and its backward, in one pass over the data each (2e + 4 and 3e + 8 bytes per element at e
-// bytes of dtype), bound by HBM: 256k x 1024 bf16 forward in 385 us, 5.6 TB/s; 4 x 4096 x 2048
-// backward in 106 us, 4.4 TB/s.
+// bytes of dtype), bound by HBM: 256k x 1024 bf16 forward in 382 us in calls one after the other (5.6
+// TB/s; the memory-side cache still holds part of the inputs), the kernel alone 407 us under a trace;
+// 4 x 4096 x 2048 backward alone 105 us, 4.5 TB/s.
 //
 // A tile is NW waves of TW tokens each by 64 channels; a lane holds its wave's TW tokens of a
 // channel in registers.  The recurrence over a run of tokens is the map h -> A h + B with A the
@@ -356,8 +357,12 @@ static void recur_run(RecurArgs a, hipStream_t s) {
 // T / (256 LOOK) hops of about 1.5 us each, and a longer look pays; with many the words' reads do
 // not: 65536 x 256 bf16 44 us with 16 waves of 16 and 16 tiles back, 83 with 8 of 32 and 4; 131072
 // x 64 45 with 32 back, 56 with 16; 65536 x 1024 112 with 8 back, 118 with 16 waves and 16, 165 with
-// 32.  Backward 16 waves of 16 everywhere, which leaves a lane's three inputs in its registers: 4 x
-// 4096 x 2048 107 us, 65536 x 256 62 (8 waves of 8 pairs of channels: 119 and 171).
+// 32.  At the borders, 65536 tokens: 8 columns 73 us with 8 waves and 8 back, 79 with 16 and 16; 7 columns
+// 71 and 69; 3 columns 41 with 16 back and 42 with 32; 2 columns 39 and 35.  (Of shorter sequences the
+// border would lie higher: 8 x 16384 x 64 takes 37 us with 8 back, 28 with 16.)  Backward 16 waves of 16
+// everywhere, which leaves a lane's three inputs in its registers: 4 x 4096 x 2048 105 us, 65536 x 256 58
+// (8 waves of 8 pairs of channels: 119 and 171); with 8 back and 16, 65536 tokens: 6 columns 83 and 88, 4
+// columns 64 and 64, 3 columns 56 and 53, 2 columns 56 and 46.
 template <bool BWD, typename E, int MODE>
 static void recur_shape(const RecurArgs& a, hipStream_t s) {
   const long long cols = (long long)a.B * ((a.D + 63) / 64);
@@ -422,7 +427,7 @@ __global__ __launch_bounds__(64) void recur_step_kernel(RecurStepArgs a) {
 template <typename E, int MODE>
 static void recur_step_run(const RecurStepArgs& a, hipStream_t s) {
   const int e = sizeof(E);
-  // four channels a lane where the rows allow it: 256 x 4096 bf16 in 5.2 us, 7.6 with one
+  // four channels a lane where the rows allow it: 256 x 4096 bf16 in 4.8 us, 7.6 with one
   const bool four = a.D % 4 == 0 && a.xs.b % 4 == 0 && a.gs.b % 4 == 0 && (uintptr_t)a.x % (4 * e) == 0 &&
                     (uintptr_t)a.h % (4 * e) == 0 && (uintptr_t)a.g % 16 == 0 && (uintptr_t)a.state % 16 == 0;
   if (four) recur_step_kernel<E, MODE, 4><<<dim3((a.D + 255) / 256, a.B), 64, 0, s>>>(a);

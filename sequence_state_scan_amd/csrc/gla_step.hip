@@ -1,7 +1,9 @@
 // A few tokens of gated linear attention for each row of a batch, the rows' states in a pool:
 //   S <- diag(exp(g_t)) S + k_t v_t^T,   o_t = S^T q_t,   t = 0 .. n-1
 // The state is read and written once (8 dk dv bytes per row and head); everything else is small
-// beside it, so the kernel is bound by HBM for many rows and by one memory round trip for few.
+// beside it, so the kernel is bound by HBM for many rows and by one memory round trip for few.  Of several
+// tokens each adds its row sums and a barrier: 128 rows of 16 heads of 128 x 128 bf16 take 55 us for one
+// token, 81 for 4, 127 for 8.
 // A workgroup holds a tile of 16 VEC columns of one head's state in registers: lane (rg, cl) of
 // the 16 x 16 lanes has rows rg + 16 i and VEC adjacent columns, so that a row of the tile is one
 // 256-byte access of 16 lanes.  o sums over the rows: within a lane, over the 4 row groups of a
