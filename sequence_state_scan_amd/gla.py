@@ -694,7 +694,7 @@ def gla_step(q, k, v, g, state, slots=None, o=None):
     place on the pool ``state`` [n_slots, H, dk, dv] (float32; a forward chain's h_final is B such
     states): q, k [B, H, n, dk], v [B, H, n, dv] (bf16 or float32), g [B, H, n, dk] (float32).
     Row b's state is state[slots[b]], with the rules of gla_recur_step.  q, k, v and g may be views
-    whose last dimension is contiguous.  Returns o [B, H, n, dv]."""
+    whose last dimension is contiguous.  dk <= 256.  Returns o [B, H, n, dv]."""
     _on_gpu(q, "q")
     if q.dim() != 4 or not isinstance(v, torch.Tensor) or v.dim() != 4:
         raise ValueError("q and v must be [B, H, n, d] tensors")
@@ -740,6 +740,7 @@ def gla_join_fwd(y, z=None, w_post=None, residual=None, scale=None, w_pre=None, 
     normed = RMS norm of out with w_pre [H d].  Each of z, w_post, residual, scale and w_pre may be
     None (that step is then left out).  The weights are float32; residual and out have one dtype
     (float32 or y's), without a residual out has y's.  out may be the residual tensor itself.
+    H d <= 8192 and H <= 2048.
     Returns a dict: out, normed (None without w_pre), and rstd_post [B, T, H], rstd_pre [B, T] for
     gla_join_bwd (None with keep_rstd=False)."""
     (B, H, T, d), st, dt, ptrs = _join_args(y, z, w_post, residual, scale, w_pre)
