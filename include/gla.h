@@ -2,7 +2,8 @@
  * gla.h -- C ABI of libgla.so: chunkwise gated linear attention with a per-key-channel
  * (diagonal) decay, forward and backward, and ZeCO's segment decomposition, on one
  * MI355X (gfx950); and the other operators of a recurrent block: the elementwise gated linear
- * recurrence, the join with the residual stream, and the single-token steps (last section).
+ * recurrence, the join with the residual stream, the single-token steps, the gated delta rule
+ * and layer norm (last two sections).
  *
  * The method (ZeCO, arXiv 2507.01004, as summarised on the atlas.scime.ai and
  * pith.science pages):
@@ -481,6 +482,96 @@ gla_status gla_join_bwd(const void* y, const gla_strides* y_st, const void* z, c
                         const gla_strides* do_st, const void* d_normed, const gla_strides* dn_st, void* dy, void* dz,
                         void* d_residual, float* dw_post, float* dscale, float* dw_pre, int B, int H, int T, int d,
                         int act, int dtype, int stream_dtype, void* workspace, size_t workspace_size, void* stream);
+
+/*
+ * ---- The gated delta rule ----
+ *
+ * A state that corrects its own prediction, per value head h of key head h / (H / Hk):
+ *   A = exp(g_t) S_{t-1},   e_t = v_t - A^T k_t,   S_t = A + beta_t k_t e_t^T,   o_t = S_t^T q_t
+ * (arXiv 2412.06464, with the state as [dk][dv] as everywhere in this library).  One decay and one beta a token and
+ * head.  q and k [B][Hk][T][dk], v and o [B][H][T][dv] (dtype), g and beta [B][H][T] (float32), states [B][H][dk][dv]
+ * (float32).  The conventions of the section above hold; a stride of g and beta's last dimension is given too (their
+ * gla_strides name all three), so that a [B][T][H] projection can be passed as it stands.
+ *   - g is finite and <= 0, or -inf (a reset: the token starts from no state).  beta, and everything else, is finite.
+ *     A rule that is to stay bounded wants |k| <= 1 and 0 <= beta <= 2; nothing here relies on it.
+ *   - lens: int32 [B] or NULL: sequence b has lens[b] tokens (limited to 0..T).  What stands behind is ignored whatever
+ *     it holds; outputs there are zero.
+ *   - States, errors and the float32 results are computed to float32's accuracy also beside bf16 inputs (split operands
+ *     on the bf16 matrix instructions, 2^-17 a factor).
+ *   - Limits: dk <= 128 and dv <= 1024 in the chunked calls, dk <= 256 in the step; H a multiple of Hk; B H ceil(T/64)
+ *     below 2^22.
+ */
+
+/*
+ * gla_delta_workspace_size -- bytes of device workspace gla_delta_fwd (which == GLA_FWD) or gla_delta_bwd (GLA_BWD)
+ * needs; gla_delta_saved_size -- bytes of the buffer a training forward fills for its backward (about 8 (dk + 2 dv)
+ * bytes a token and head in bf16).  0, with gla_last_error() set, if the sizes are rejected.  Both buffers lie on 16
+ * bytes.  The workspace is written before it is read and must not be shared by calls that may run at the same time.
+ */
+size_t gla_delta_workspace_size(int which, int B, int H, int Hk, int T, int dk, int dv, int dtype);
+size_t gla_delta_saved_size(int B, int H, int Hk, int T, int dk, int dv, int dtype);
+
+/*
+ * gla_delta_fwd -- o, and h_final (the state after the last token, h0 for an empty sequence; may be NULL), from h0
+ * (NULL = 0).  saved: NULL in a forward-only call, else gla_delta_saved_size bytes for gla_delta_bwd (a private layout;
+ * a forward-only call rounds o's operands to bf16, so its o may differ from a training one's in the last place).
+ * Results do not depend on the timing of the run, bit for bit.
+ */
+gla_status gla_delta_fwd(const void* q, const gla_strides* q_st, const void* k, const gla_strides* k_st, const void* v,
+                         const gla_strides* v_st, const float* g, const gla_strides* g_st, const float* beta,
+                         const gla_strides* b_st, const float* h0, const int* lens, void* o, float* h_final, void* saved,
+                         size_t saved_size, int B, int H, int Hk, int T, int dk, int dv, int dtype, void* workspace,
+                         size_t workspace_size, void* stream);
+
+/*
+ * gla_delta_bwd -- the gradients of q, k (summed over a key head's value heads), v, g, beta and h0 (dh0 may be NULL),
+ * for do [B][H][T][dv] (dtype) and dhT (float32, the gradient of h_final; NULL = 0), over the forward's inputs, its o and
+ * the buffer it saved (same sizes and lens; read, not changed).  dg and dbeta [B][H][T] are contiguous.  dg is zero where
+ * exp(g) is.
+ */
+gla_status gla_delta_bwd(const void* q, const gla_strides* q_st, const void* k, const gla_strides* k_st, const void* v,
+                         const gla_strides* v_st, const float* g, const gla_strides* g_st, const float* beta,
+                         const gla_strides* b_st, const void* o, const void* do_, const gla_strides* do_st, void* saved,
+                         size_t saved_size, const int* lens, const float* dhT, void* dq, void* dk_, void* dv_, float* dg,
+                         float* dbeta, float* dh0, int B, int H, int Hk, int T, int dk, int dv, int dtype,
+                         void* workspace, size_t workspace_size, void* stream);
+
+/*
+ * gla_delta_step -- the next n tokens for every row of a batch, in place on a pool of states [n_slots][H][dk][dv], one or
+ * a few at a time: q, k [B][Hk][n][dk], v, o [B][H][n][dv], g, beta [B][H][n]; slots and their rules as in gla_step.
+ * gla_delta_fwd's h_final is B such states.
+ */
+gla_status gla_delta_step(const void* q, const gla_strides* q_st, const void* k, const gla_strides* k_st, const void* v,
+                          const gla_strides* v_st, const float* g, const gla_strides* g_st, const float* beta,
+                          const gla_strides* b_st, float* state, const int* slots, void* o, int B, int H, int Hk, int n,
+                          int dk, int dv, int n_slots, int dtype, void* stream);
+
+/*
+ * gla_layernorm_fwd -- the residual add and layer norm before a block, in one pass over rows of D values:
+ *   out = residual + x,   normed = (out - mean) rsqrt(mean((out - mean)^2) + eps) w + b
+ * x [B][T][D] and normed have dtype; residual [B][T][D] and out have stream_dtype (GLA_F32, or GLA_BF16 with a bf16
+ * dtype).  residual NULL (then out is NULL too): the norm of x.  w, b [D] (float32): NULL = 1, 0.  All arithmetic is
+ * float32, the variance taken about the mean; normed is formed from out before its rounding.  out may be NULL, or the
+ * residual itself (contiguous; a forward-only call).  mean, rstd [B][T] (float32, for gla_layernorm_bwd) may both be NULL.
+ * eps > 0.  D <= 16384.
+ */
+gla_status gla_layernorm_fwd(const void* x, const gla_strides* x_st, const void* residual, const gla_strides* r_st,
+                             const float* w, const float* b, void* out, void* normed, float* mean, float* rstd, int B,
+                             int T, int D, float eps, int dtype, int stream_dtype, void* stream);
+
+/* Bytes of device workspace gla_layernorm_bwd needs when it returns dw or db. */
+size_t gla_layernorm_workspace_size(int B, int T, int D);
+
+/*
+ * gla_layernorm_bwd -- its gradients, for d_normed (dtype) and d_out (stream_dtype; NULL = 0), over the forward's inputs
+ * and the mean and rstd it kept.  dx (dtype); d_residual (stream_dtype, the same values; may be NULL); dw, db [D] (float32,
+ * each may be NULL), summed in float32 in an order that does not depend on the timing.
+ */
+gla_status gla_layernorm_bwd(const void* x, const gla_strides* x_st, const void* residual, const gla_strides* r_st,
+                             const float* w, const float* mean, const float* rstd, const void* d_out,
+                             const gla_strides* do_st, const void* d_normed, const gla_strides* dn_st, void* dx,
+                             void* d_residual, float* dw, float* db, int B, int T, int D, int dtype, int stream_dtype,
+                             void* workspace, size_t workspace_size, void* stream);
 
 #ifdef __cplusplus
 }

@@ -21,7 +21,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgla.so")
 SOURCES = ["gla_fwd.hip", "gla_bwd.hip", "gla_correct_bwd.hip", "gla_exact.hip", "gla_scan.hip", "gla_resplit.hip", "gla_noalloc.hip", "gla_api.cpp",
-           "gla_recur.hip", "gla_step.hip", "gla_join.hip", "gla_block_api.cpp"]
+           "gla_recur.hip", "gla_step.hip", "gla_join.hip", "gla_block_api.cpp",
+           "gla_delta_fwd.hip", "gla_delta_bwd.hip", "gla_delta_step.hip", "gla_layernorm.hip", "gla_delta_api.cpp"]
 ARCH = "gfx950"
 
 CFLAGS = [

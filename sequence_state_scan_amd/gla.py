@@ -15,7 +15,8 @@ every chunk).  All four take a join (gla_join_fwd / gla_join_bwd): the block's o
 residual and the next block's norm.
 
 The other operators of a recurrent block: gla_recur_fwd, gla_recur_bwd (elementwise gated linear
-recurrence), gla_step and gla_recur_step (single tokens on a pool of states).
+recurrence), gla_step and gla_recur_step (single tokens on a pool of states), gla_delta_fwd,
+gla_delta_bwd and gla_delta_step (gated delta rule), gla_layernorm_fwd and gla_layernorm_bwd.
 """
 from __future__ import annotations
 
@@ -105,6 +106,22 @@ def load_library(path: str = LIB_PATH):
         lib.gla_join_fwd.restype = i
         lib.gla_join_bwd.argtypes = [vp] * 21 + [i] * 7 + [vp, sz, vp]
         lib.gla_join_bwd.restype = i
+        lib.gla_delta_workspace_size.argtypes = [i] * 8
+        lib.gla_delta_workspace_size.restype = sz
+        lib.gla_delta_saved_size.argtypes = [i] * 7
+        lib.gla_delta_saved_size.restype = sz
+        lib.gla_delta_fwd.argtypes = [vp] * 15 + [sz] + [i] * 7 + [vp, sz, vp]
+        lib.gla_delta_fwd.restype = i
+        lib.gla_delta_bwd.argtypes = [vp] * 14 + [sz] + [vp] * 8 + [i] * 7 + [vp, sz, vp]
+        lib.gla_delta_bwd.restype = i
+        lib.gla_delta_step.argtypes = [vp] * 13 + [i] * 8 + [vp]
+        lib.gla_delta_step.restype = i
+        lib.gla_layernorm_workspace_size.argtypes = [i] * 3
+        lib.gla_layernorm_workspace_size.restype = sz
+        lib.gla_layernorm_fwd.argtypes = [vp] * 10 + [i] * 3 + [fl, i, i, vp]
+        lib.gla_layernorm_fwd.restype = i
+        lib.gla_layernorm_bwd.argtypes = [vp] * 15 + [i] * 5 + [vp, sz, vp]
+        lib.gla_layernorm_bwd.restype = i
         if path == LIB_PATH:
             _lib = lib
         return lib
@@ -784,6 +801,194 @@ def gla_join_bwd(y, fwd: dict, d_out=None, d_normed=None, z=None, w_post=None, r
             *[None if t is None else t.data_ptr() for t in grads], B, H, T, d, _code(ACTS, act, "act"), dt,
             _dtype_code(st), wp, wn)
     return dict(zip(("dy", "dz", "d_residual", "dw_post", "dscale", "dw_pre"), grads))
+
+
+# -------------------------------------------------------------------------------- gated delta rule
+
+@functools.lru_cache(maxsize=4096)
+def delta_workspace_size(which: int, B: int, H: int, Hk: int, T: int, dk: int, dv: int, dtype) -> int:
+    """Bytes of workspace gla_delta_fwd (which=GLA_FWD) or gla_delta_bwd (GLA_BWD) needs."""
+    return _size(load_library().gla_delta_workspace_size, which, B, H, Hk, T, dk, dv, _dtype_code(dtype))
+
+
+@functools.lru_cache(maxsize=4096)
+def delta_saved_size(B: int, H: int, Hk: int, T: int, dk: int, dv: int, dtype) -> int:
+    """Bytes of the buffer that a training forward keeps for gla_delta_bwd."""
+    return _size(load_library().gla_delta_saved_size, B, H, Hk, T, dk, dv, _dtype_code(dtype))
+
+
+def _size(fn, *args):
+    n = fn(*args)
+    if n == 0:
+        raise GLAError(GLA_ERR_INVALID_ARG, load_library().gla_last_error().decode())
+    return int(n)
+
+
+def _gates(t, name, shape, device):
+    """(pointer, strides) of a [B, H, T] tensor of one value a token, at any strides."""
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != torch.float32 or t.device != device:
+        if isinstance(t, torch.Tensor):
+            t = t.contiguous()
+        _expect(t, name, shape, torch.float32, device)  # says which
+    st = t.stride()
+    return t.data_ptr(), (ctypes.c_longlong * 3)(st[0], st[1], st[2])
+
+
+def _delta_args(q, k, v, g, beta):
+    """((B, H, Hk, T, dk, dv, dtype code), the inputs' pointers and strides), checked."""
+    _on_gpu(q, "q")
+    if q.dim() != 4 or not isinstance(v, torch.Tensor) or v.dim() != 4:
+        raise ValueError("q and v must be [B, heads, T, d] tensors")
+    B, Hk, T, dk = q.shape
+    H, dv, dev = v.shape[1], v.shape[3], q.device
+    return ((B, H, Hk, T, dk, dv, _dtype_code(q.dtype)),
+            _view(q, "q", (B, Hk, T, dk), q.dtype, dev) + _view(k, "k", (B, Hk, T, dk), q.dtype, dev) +
+            _view(v, "v", (B, H, T, dv), q.dtype, dev) + _gates(g, "g", (B, H, T), dev) +
+            _gates(beta, "beta", (B, H, T), dev))
+
+
+def gla_delta_fwd(q, k, v, g, beta, h0=None, lens=None, o=None, h_final=None, saved=None, workspace=None,
+                  keep_saved: bool = True):
+    """The gated delta rule: S <- exp(g_t) S, then S <- S + beta_t k_t (v_t - S^T k_t)^T and o_t = S^T q_t, over q, k
+    [B, Hk, T, dk], v [B, H, T, dv] (bf16 or float32; value head h reads key head h // (H // Hk)) and g (log-gates <= 0,
+    or -inf for a reset), beta [B, H, T] (float32), from h0 [B, H, dk, dv] (float32, default zero).  lens: int32 [B], the
+    sequences' lengths in a padded batch (o is zero behind them).  q, k and v may be views whose last dimension is
+    contiguous, g and beta any views.  dk <= 128.
+    Returns (o [B, H, T, dv], h_final [B, H, dk, dv], saved): saved is what gla_delta_bwd needs besides, a buffer of
+    delta_saved_size bytes, None with keep_saved=False (a forward-only call)."""
+    dims, ptrs = _delta_args(q, k, v, g, beta)
+    B, H, Hk, T, dk, dv, dt = dims
+    dev, f32 = q.device, torch.float32
+    h0p = _out(h0, "h0", (B, H, dk, dv), f32, dev, optional=True)
+    lp = _out(lens, "lens", (B,), torch.int32, dev, optional=True)
+    ws, wp, wn = _scratch(workspace, delta_workspace_size(GLA_FWD, *dims[:6], q.dtype), dev)
+    svp, svn = None, 0
+    if keep_saved:
+        saved, svp, svn = _scratch(saved, delta_saved_size(*dims[:6], q.dtype), dev)
+    elif saved is not None:
+        raise ValueError("saved given with keep_saved=False")
+    o, op = _new(o, "o", (B, H, T, dv), q.dtype, dev, v)
+    h_final, fp = _new(h_final, "h_final", (B, H, dk, dv), f32, dev, h0)
+    _launch(load_library().gla_delta_fwd, dev, *ptrs, h0p, lp, op, fp, svp, svn, *dims, wp, wn)
+    return o, h_final, saved
+
+
+def gla_delta_bwd(q, k, v, g, beta, o, do, saved, lens=None, dhT=None, dq=None, dk=None, dv=None, dg=None, dbeta=None,
+                  dh0=None, workspace=None):
+    """Gradients of gla_delta_fwd for do [B, H, T, dv] (the gradient of o) and dhT [B, H, dk, dv] (of h_final, float32,
+    default zero), over the forward's inputs, the o and the saved it returned.  Returns (dq, dk [B, Hk, T, dk], dv
+    [B, H, T, dv] in q's dtype, dg, dbeta [B, H, T], dh0 [B, H, dk, dv], float32)."""
+    dims, ptrs = _delta_args(q, k, v, g, beta)
+    B, H, Hk, T, d_k, d_v, dt = dims
+    dev, f32 = q.device, torch.float32
+    op = _out(o, "o", (B, H, T, d_v), q.dtype, dev)
+    dop, dos = _view(do, "do", (B, H, T, d_v), q.dtype, dev)
+    lp = _out(lens, "lens", (B,), torch.int32, dev, optional=True)
+    tp = _out(dhT, "dhT", (B, H, d_k, d_v), f32, dev, optional=True)
+    if saved is None:
+        raise ValueError("saved is required (a forward with keep_saved=True returns it)")
+    _, svp, svn = _scratch(saved, 0, dev)
+    ws, wp, wn = _scratch(workspace, delta_workspace_size(GLA_BWD, *dims[:6], q.dtype), dev)
+    dq, dqp = _new(dq, "dq", (B, Hk, T, d_k), q.dtype, dev, q)
+    dk, dkp = _new(dk, "dk", (B, Hk, T, d_k), q.dtype, dev, k)
+    dv, dvp = _new(dv, "dv", (B, H, T, d_v), q.dtype, dev, v)
+    dg, dgp = _new(dg, "dg", (B, H, T), f32, dev, g)
+    dbeta, dbp = _new(dbeta, "dbeta", (B, H, T), f32, dev, beta)
+    dh0, dhp = _new(dh0, "dh0", (B, H, d_k, d_v), f32, dev, dhT)
+    _launch(load_library().gla_delta_bwd, dev, *ptrs, op, dop, dos, svp, svn, lp, tp, dqp, dkp, dvp, dgp, dbp, dhp, *dims,
+            wp, wn)
+    return dq, dk, dv, dg, dbeta, dh0
+
+
+def gla_delta_step(q, k, v, g, beta, state, slots=None, o=None):
+    """The next n tokens of the gated delta rule for every row of a batch (n = 1: decoding), in place on the pool
+    ``state`` [n_slots, H, dk, dv] (float32; gla_delta_fwd's h_final is B such states): q, k [B, Hk, n, dk], v
+    [B, H, n, dv], g, beta [B, H, n].  Row b's state is state[slots[b]], with the rules of gla_recur_step.  Views as in
+    gla_delta_fwd.  dk <= 256.  Returns o [B, H, n, dv]."""
+    dims, ptrs = _delta_args(q, k, v, g, beta)
+    B, H, Hk, n, dk, dv, dt = dims
+    dev = q.device
+    sp, ip, n_slots = _pool(state, slots, B, (H, dk, dv), dev)
+    o, op = _new(o, "o", (B, H, n, dv), q.dtype, dev, v)
+    _launch(load_library().gla_delta_step, dev, *ptrs, sp, ip, op, B, H, Hk, n, dk, dv, n_slots, dt)
+    return o
+
+
+# ------------------------------------------------------------------------------------- layer norm
+
+@functools.lru_cache(maxsize=4096)
+def layernorm_workspace_size(B: int, T: int, D: int) -> int:
+    """Bytes of workspace gla_layernorm_bwd needs for the weights' gradients."""
+    return _size(load_library().gla_layernorm_workspace_size, B, T, D)
+
+
+def _norm_args(x, w, residual):
+    _on_gpu(x, "x")
+    if x.dim() != 3:
+        raise ValueError("x must be a [B, T, D] tensor")
+    (B, T, D), dev, st = x.shape, x.device, x.dtype
+    dt = _dtype_code(x.dtype)
+    xp, xs = _view(x, "x", (B, T, D), x.dtype, dev)
+    rp = rs = None
+    if residual is not None:
+        if not isinstance(residual, torch.Tensor):
+            raise TypeError("residual must be a torch.Tensor")
+        st = residual.dtype
+        rp, rs = _view(residual, "residual", (B, T, D), st, dev)
+    return (B, T, D), st, dt, (xp, xs, rp, rs, _out(w, "w", (D,), torch.float32, dev, optional=True))
+
+
+def gla_layernorm_fwd(x, w=None, b=None, residual=None, eps: float = 1e-5, out=None, normed=None,
+                      keep_stats: bool = True):
+    """The residual add and layer norm before a block, in one pass over x [B, T, D] (bf16 or float32): out = residual + x,
+    normed = (out - mean) / sqrt(var + eps) * w + b.  residual [B, T, D] and out have one dtype (float32 or x's); without a
+    residual it is the norm of x alone.  w and b [D] (float32) may be None (1 and 0).  out may be the residual tensor
+    itself.  D <= 16384.
+    Returns a dict: out (None without a residual), normed, and mean, rstd [B, T] for gla_layernorm_bwd (None with
+    keep_stats=False)."""
+    (B, T, D), st, dt, ptrs = _norm_args(x, w, residual)
+    dev, f32 = x.device, torch.float32
+    bp = _out(b, "b", (D,), f32, dev, optional=True)
+    op = None
+    if residual is not None:
+        out, op = _new(out, "out", (B, T, D), st, dev, residual)
+    elif out is not None:
+        raise ValueError("out given without a residual")
+    normed, np_ = _new(normed, "normed", (B, T, D), x.dtype, dev, x)
+    mean = rstd = mp = rp = None
+    if keep_stats:
+        mean, mp = _new(None, "mean", (B, T), f32, dev)
+        rstd, rp = _new(None, "rstd", (B, T), f32, dev)
+    _launch(load_library().gla_layernorm_fwd, dev, *ptrs, bp, op, np_, mp, rp, B, T, D, eps, dt, _dtype_code(st))
+    return {"out": out, "normed": normed, "mean": mean, "rstd": rstd}
+
+
+def gla_layernorm_bwd(x, fwd: dict, d_normed, w=None, d_out=None, residual=None, bias: bool = True, workspace=None):
+    """Gradients of gla_layernorm_fwd for d_normed (the gradient of normed, x's dtype) and d_out (of out, out's dtype,
+    default zero), over the forward's inputs and the dict it returned.  Returns a dict: dx; d_residual (None without a
+    residual; dx itself where the dtypes are the same, as the values are); dw [D] (None without w) and db [D] (None with
+    bias=False), float32."""
+    (B, T, D), st, dt, ptrs = _norm_args(x, w, residual)
+    dev, f32 = x.device, torch.float32
+    if residual is not None and fwd["out"] is not None and fwd["out"].data_ptr() == residual.data_ptr():
+        raise ValueError("the forward wrote out in the residual's place: its inputs are gone")
+    mp = _out(fwd["mean"], "fwd['mean']", (B, T), f32, dev)
+    rp = _out(fwd["rstd"], "fwd['rstd']", (B, T), f32, dev)
+    dnp, dns = _view(d_normed, "d_normed", (B, T, D), x.dtype, dev)
+    dop, dos = (None, None) if d_out is None else _view(d_out, "d_out", (B, T, D), st, dev)
+    dx, dxp = _new(None, "dx", (B, T, D), x.dtype, dev, x)
+    d_residual, drp = None, None
+    if residual is not None and st == x.dtype:
+        d_residual = dx
+    elif residual is not None:
+        d_residual, drp = _new(None, "d_residual", (B, T, D), st, dev, residual)
+    dw, dwp = (None, None) if w is None else _new(None, "dw", (D,), f32, dev, w)
+    db, dbp = _new(None, "db", (D,), f32, dev, w) if bias else (None, None)
+    sums = dw is not None or db is not None
+    ws, wp, wn = _scratch(workspace, layernorm_workspace_size(B, T, D) if sums else 0, dev)
+    _launch(load_library().gla_layernorm_bwd, dev, *ptrs, mp, rp, dop, dos, dnp, dns, dxp, drp, dwp, dbp, B, T, D, dt,
+            _dtype_code(st), wp, wn)
+    return {"dx": dx, "d_residual": d_residual, "dw": dw, "db": db}
 
 
 # ------------------------------------------------------------------------------ method chains
