@@ -15,6 +15,7 @@ constexpr int kDeltaGates = 5 * kDeltaChunk;  // floats of a chunk's gate block:
 struct DeltaShape {
   int B, H, Hk, T, dk, dv, dtype;
   int N, P, L, DKP, DVP, marks;  // chunks, segments, their chunks, padded channels and values, marks
+  int dkr, dvr;                  // dk and dv rounded up to 8: the rows that the walks read
 };
 DeltaShape delta_shape(int B, int H, int Hk, int T, int dk, int dv, int dtype);
 
@@ -43,12 +44,14 @@ struct DeltaArgs : DeltaShape {
   float* mark;    // [BH][marks][DVP / 16][DKP / 16][256]: the state leaving every fourth chunk, in registers' order
   // scratch
   void* solve;    // [BH][N][64][64]: (I + B beta)^-1
+  void* trans_rows;  // [BH][P][DKP][DKP]: a segment's transition by rows (as trans)
   float *seg, *seg_in;  // [BH][P][DVP / 16][DKP / 16][256]: a segment's own end state, the state entering it
   float* z;       // [BH][N * 64][DVP]
   void* grad1;    // [BH][N][DVP][DKP]: the gradient of the state leaving a chunk, transposed
   float* carry;   // [BH][marks][DVP / 16]: <state, its gradient> at the marks
   float* at;      // [BH][N * 64]: o . do - v . dv
   float *dq_heads, *dk_heads;  // [B][H][T][dk], where heads share keys
+  void *qk_packed, *v_packed;  // q and k, v (and do), with rows of dkr, dvr elements, where dk, dv are no such numbers
 };
 
 // Bytes of the two buffers, and the pointers into them.
@@ -56,8 +59,11 @@ size_t delta_saved_bytes(const DeltaShape& s);
 size_t delta_scratch_bytes(const DeltaShape& s, bool backward, bool train);
 void delta_place(DeltaArgs& a, void* saved, void* scratch, bool backward);
 
-hipError_t launch_delta_fwd(const DeltaArgs& a, hipStream_t s);  // a.err null: forward only
-hipError_t launch_delta_bwd(const DeltaArgs& a, hipStream_t s);
+// Copies inputs whose rows are no multiple of 8 elements (the walks load 8 at a time, every lane, at any alignment) and
+// points the arguments at the copies.
+void delta_pack(DeltaArgs& a, bool backward, hipStream_t s);
+hipError_t launch_delta_fwd(DeltaArgs a, hipStream_t s);  // a.err null: forward only
+hipError_t launch_delta_bwd(DeltaArgs a, hipStream_t s);
 
 struct DeltaStepArgs {
   const void *q, *k, *v;
@@ -111,6 +117,14 @@ __device__ __forceinline__ f32x4 mma(f32x8 a, f32x8 b, f32x4 c) {
   return c;
 }
 
+// Two floats rounded to bf16, in one word.
+__device__ __forceinline__ unsigned round2(float x, float y) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const f32x2 v = {x, y};
+  return __builtin_bit_cast(unsigned, __builtin_convertvector(v, bf16x2));
+}
+
 template <typename E, int N = Num<E>::PARTS>
 struct Split {
   Frag<E> part[N];
@@ -123,15 +137,23 @@ template <typename E, int N = Num<E>::PARTS>
 __device__ __forceinline__ Split<E, N> split(f32x4 x, f32x4 y) {
   Split<E, N> s;
   if constexpr (sizeof(E) == 2) {
+    typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 #pragma unroll
-    for (int part = 0; part < N; ++part)
+    for (int part = 0; part < N; ++part) {
+      u32x4 w;  // two rounded values a word; their own values again by shift and mask
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s.part[part][i] = (bf16)x[i];
-        s.part[part][4 + i] = (bf16)y[i];
-        x[i] -= (float)s.part[part][i];
-        y[i] -= (float)s.part[part][4 + i];
+      for (int i = 0; i < 2; ++i) {
+        w[i] = round2(x[2 * i], x[2 * i + 1]);
+        w[2 + i] = round2(y[2 * i], y[2 * i + 1]);
+        if (part + 1 < N) {
+          x[2 * i] -= __uint_as_float(w[i] << 16);
+          x[2 * i + 1] -= __uint_as_float(w[i] & 0xffff0000u);
+          y[2 * i] -= __uint_as_float(w[2 + i] << 16);
+          y[2 * i + 1] -= __uint_as_float(w[2 + i] & 0xffff0000u);
+        }
       }
+      s.part[part] = __builtin_bit_cast(bf16x8, w);
+    }
   } else {
     s.part[0] = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
   }
@@ -169,60 +191,76 @@ __device__ __forceinline__ int row_of(int t, int m) { return 32 * (t >> 1) + 8 *
 // First of the accumulator's four rows in tile t.
 __device__ __forceinline__ int row4_of(int t, int g4) { return 32 * (t >> 1) + 8 * g4 + 4 * (t & 1); }
 
-// Leading dimension of an LDS tile of D columns (rows on 16 bytes).
-template <typename E>
-__host__ __device__ constexpr int ld_of(int D) { return D + (sizeof(E) == 2 ? 8 : 4); }
-
-// 8 consecutive elements of an LDS row.
-template <typename E>
-__device__ __forceinline__ Frag<E> row_frag(const E* p) {
-  if constexpr (sizeof(E) == 2) {
-    return *reinterpret_cast<const bf16x8*>(p);
-  } else {
-    const f32x4 x = *reinterpret_cast<const f32x4*>(p), y = *reinterpret_cast<const f32x4*>(p + 4);
-    return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
-  }
-}
-// 4 rows from row0 of the lane's column (of 16 from col0) of a row-major LDS tile; bf16 through the transposing read
-// (lane s of a 16-lane group addresses row s / 4, columns 4 (s % 4), and receives column s).
-template <typename E>
-__device__ __forceinline__ f32x4 rows4(const E* tile, int ld, int row0, int col0) {
-  const int s = lane_id() & 15;
-  f32x4 r;
-  if constexpr (sizeof(E) == 2) {
-    typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 v4;
-    const v4 x = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
-        (__attribute__((address_space(3))) v4*)(tile + (row0 + (s >> 2)) * ld + col0 + 4 * (s & 3)));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = (float)x[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = tile[(row0 + i) * ld + col0 + s];
-  }
-  return r;
-}
-// Rows kk + 8 g4 + (0 .. 7) of a column of a row-major LDS tile: column col0 + n16, or with PERM column
-// row_of(t, n16) for col0 = row4_of(t, 0).
-template <typename E, bool PERM>
-__device__ __forceinline__ Frag<E> col_frag(const E* tile, int ld, int kk, int col0) {
-  const int l = lane_id(), s = l & 15, g4 = l >> 4;
-  Frag<E> r;
-  if constexpr (sizeof(E) == 2) {
-    typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 v4;
-    const E* p = tile + (kk + 8 * g4 + (s >> 2)) * ld + col0 + (PERM ? 8 : 4) * (s & 3);
-    const v4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((__attribute__((address_space(3))) v4*)p);
-    const v4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((__attribute__((address_space(3))) v4*)(p + 4 * ld));
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      r[e] = lo[e];
-      r[4 + e] = hi[e];
+// A tile of D columns in LDS.  bf16: rows without padding, a row's 16-byte blocks in an order that depends on the row,
+// so that the 16 lanes a 16-byte read serves at once (lanes 0-3, 12-15, 20-23, 24-27 of a half, and the rest) fall on
+// distinct banks, both for rows n16 and for rows row_of(t, n16); D is 32, 64 or 128.  float: rows padded to 16 bytes more.
+template <typename E, int D>
+struct Tile {
+  static constexpr int LD = sizeof(E) == 2 ? D : D + 4;
+  __device__ __forceinline__ static int at(int row, int col) {
+    if constexpr (sizeof(E) == 2) {
+      const int own = D == 128 ? 4 * (row & 3) : D == 64 ? 4 * ((row >> 1) & 1) : 0, turn = -(row >> 3) & 3;
+      return row * D + (((col >> 3) ^ (own | turn)) << 3) + (col & 7);
+    } else {
+      return row * LD + col;
     }
-  } else {
-    const int col = col0 + (PERM ? 8 * (s >> 2) + (s & 3) : s);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) r[e] = tile[(kk + 8 * g4 + e) * ld + col];
   }
-  return r;
+  // 8 consecutive elements of a row, from a multiple of 8
+  __device__ __forceinline__ static Frag<E> row(const E* tile, int r, int col) {
+    const E* p = tile + at(r, col);
+    if constexpr (sizeof(E) == 2) {
+      return *reinterpret_cast<const bf16x8*>(p);
+    } else {
+      const f32x4 x = *reinterpret_cast<const f32x4*>(p), y = *reinterpret_cast<const f32x4*>(p + 4);
+      return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+  }
+  // (s: the lane's n16.)  4 rows from row0 (a multiple of 4) of the lane's column (of 16 from col0); bf16 through the transposing read (lane s
+  // of a 16-lane group addresses row s / 4, columns 4 (s % 4), and receives column s)
+  __device__ __forceinline__ static f32x4 rows4(const E* tile, int row0, int col0, int s) {
+    f32x4 r;
+    if constexpr (sizeof(E) == 2) {
+      const auto x = transposed(tile + at(row0 + (s >> 2), col0 + 4 * (s & 3)));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = (float)x[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = tile[at(row0 + i, col0 + s)];
+    }
+    return r;
+  }
+  // Rows kk + 8 g4 + (0 .. 7) of a column: col0 + n16, or with PERM row_of(t, n16) for col0 = row4_of(t, 0)
+  template <bool PERM>
+  __device__ __forceinline__ static Frag<E> col(const E* tile, int kk, int col0, int s, int g4) {
+    Frag<E> r;
+    if constexpr (sizeof(E) == 2) {
+      // (rows r and r + 4 of an aligned eight have their blocks in the same order)
+      const E* p = tile + at(kk + 8 * g4 + (s >> 2), col0 + (PERM ? 8 : 4) * (s & 3));
+      const auto lo = transposed(p), hi = transposed(p + 4 * LD);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        r[e] = lo[e];
+        r[4 + e] = hi[e];
+      }
+    } else {
+      const int c = col0 + (PERM ? 8 * (s >> 2) + (s & 3) : s);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r[e] = tile[at(kk + 8 * g4 + e, c)];
+    }
+    return r;
+  }
+  // 4 elements of a row, from a multiple of 4
+  __device__ __forceinline__ static void put4(E* tile, int r, int col, f32x4 x) { store4(tile + at(r, col), x); }
+
+ private:
+  typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 v4;
+  __device__ __forceinline__ static v4 transposed(const E* p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4bf16((__attribute__((address_space(3))) v4*)p);
+  }
+};
+__device__ __forceinline__ f32x8 load8(const float* p) {
+  const f32x4 x = *reinterpret_cast<const f32x4*>(p), y = *reinterpret_cast<const f32x4*>(p + 4);
+  return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
 // 8 (4) elements in memory at any alignment of the element.
@@ -254,25 +292,41 @@ __device__ __forceinline__ void store4_part(E* p, f32x4 x, int left) {
   }
 }
 
-// A tile of ROWS rows of D elements on its way from memory to LDS: rows past `rows` and columns past `cols` zero.
+// A tile of ROWS rows of D elements on its way from memory to LDS: rows past `rows` and columns past `cols` (at least 1
+// of the one, 8 of the other and a multiple of 8) are zero there.  Every lane loads, from a place inside the tile where
+// its own is outside: with loads under a condition the compiler waits for all those in flight before the next (4 heads
+// of 128 x 256 over 64k tokens: the walk 235 us).  Addresses are formed again at every use (fresh_tid): held over a
+// walk's loop they cost the registers that its products need.
 template <typename E, int ROWS, int D, int NT>
 struct TileIn {
-  static constexpr int UNITS = ROWS * D / 8, PER = (UNITS + NT - 1) / NT;
+  static constexpr int UPR = D / 8, UNITS = ROWS * UPR, PER = (UNITS + NT - 1) / NT;
+  static_assert(NT % UPR == 0, "whole rows a pass");
   typename Raw<E, 8>::type r[PER];
   __device__ __forceinline__ void load(const E* src, long stride, int rows, int cols) {
+    const int t = fresh_tid();
+    if (rows >= ROWS && cols >= D && stride < (1 << 20)) {  // the whole tile, from a base and one 32-bit offset
+      const int u = UNITS % NT == 0 ? t : t < UNITS ? t : 0;
+      const unsigned at = ((unsigned)(u / UPR) * (unsigned)stride + u % UPR * 8) * sizeof(E);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int u = threadIdx.x + i * NT, row = u / (D / 8), c = u % (D / 8) * 8;
-      r[i] = (typename Raw<E, 8>::type){};
-      if ((UNITS % NT == 0 || u < UNITS) && row < rows && c < cols) r[i] = load8_part<E>(src + row * stride + c, cols - c);
+      for (int i = 0; i < PER; ++i)
+        r[i] = *reinterpret_cast<const typename Raw<E, 8>::type*>(reinterpret_cast<const char*>(src + i * (NT / UPR) * stride) + at);
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int u = t + i * NT, c = u % UPR * 8;
+        r[i] = *reinterpret_cast<const typename Raw<E, 8>::type*>(src + min(u / UPR, min(rows, ROWS) - 1) * stride + (c < cols ? c : 0));
+      }
     }
   }
-  __device__ __forceinline__ void store(E* lds, int ld) const {
+  __device__ __forceinline__ void store(E* lds, int rows, int cols) const {
     typedef E v8 __attribute__((ext_vector_type(8), aligned(16)));
+    const int t = fresh_tid();
+    const bool whole = rows >= ROWS && cols >= D;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int u = threadIdx.x + i * NT;
-      if (UNITS % NT == 0 || u < UNITS) *reinterpret_cast<v8*>(lds + u / (D / 8) * ld + u % (D / 8) * 8) = r[i];
+      const int u = t + i * NT, row = u / UPR, c = u % UPR * 8;
+      if (UNITS % NT == 0 || u < UNITS)
+        *reinterpret_cast<v8*>(lds + Tile<E, D>::at(row, c)) = whole || (row < rows && c < cols) ? (v8)r[i] : (v8){};
     }
   }
 };
@@ -316,6 +370,13 @@ __device__ __forceinline__ void store_state(const f32x4 (&S)[CB], float* p, int 
       if (r < dk && col < dv) p[(long)r * dv + col] = S[cb][i];
     }
 }
+// Waits here for values on their way from memory, not where a loop first uses them: there the compiler would wait, in
+// every pass, for whatever else is in flight.
+template <int CB>
+__device__ __forceinline__ void arrived(f32x4 (&S)[CB]) {
+#pragma unroll
+  for (int cb = 0; cb < CB; ++cb) asm volatile("" : "+v"(S[cb]));
+}
 // The same in registers' order: [tile][lane][4].
 template <int CB>
 __device__ __forceinline__ void load_regs(f32x4 (&S)[CB], const float* p) {
@@ -329,8 +390,7 @@ __device__ __forceinline__ void store_regs(const f32x4 (&S)[CB], float* p) {
 }
 
 // An accumulator tile of 4 rows x the lane's column, stored by rows.  p: the first of its rows, the first of 16 columns.
-__device__ __forceinline__ void store_rows(f32x4 x, float* p, int pitch) {
-  const int s = lane_id() & 15;
+__device__ __forceinline__ void store_rows(f32x4 x, float* p, int pitch, int s) {
   *reinterpret_cast<f32x4*>(p + (s & 3) * pitch + 4 * (s >> 2)) = quad_transpose(x);
 }
 

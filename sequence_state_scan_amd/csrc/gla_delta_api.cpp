@@ -22,6 +22,8 @@ DeltaShape delta_shape(int B, int H, int Hk, int T, int dk, int dv, int dtype) {
   s.N = (T + kDeltaChunk - 1) / kDeltaChunk;
   s.DKP = dk <= 32 ? 32 : dk <= 64 ? 64 : 128;
   s.DVP = (dv + 15) / 16 * 16;
+  s.dkr = (dk + 7) / 8 * 8;
+  s.dvr = (dv + 7) / 8 * 8;
   s.marks = (s.N + kDeltaMarks - 1) / kDeltaMarks;
   const long long units = (long long)B * H * (dv <= 64 ? 1 : (dv + 127) / 128);
   long long P = (256 + units - 1) / units;
@@ -64,12 +66,16 @@ size_t place_saved(DeltaArgs& a, char* p) {
 size_t place_scratch(DeltaArgs& a, char* p, bool backward, bool train) {
   Regions r{p};
   const size_t heads = (size_t)a.B * a.H, chunks = heads * a.N, e = a.dtype == GLA_BF16 ? 2 : 4;
+  const size_t rows = (size_t)a.B * a.T * e * (backward ? 2 : 1);  // of v, and of do
+  if (a.dk % 8) r.take(a.qk_packed, (size_t)a.B * a.T * e * 2 * a.Hk * a.dkr);
+  if (a.dv % 8) r.take(a.v_packed, rows * a.H * a.dvr);
   if (a.P > 1) {
     r.take(a.seg, heads * a.P * a.DVP * a.DKP * 4);
     r.take(a.seg_in, heads * a.P * a.DVP * a.DKP * 4);
   }
   if (!backward) {
     r.take(a.solve, chunks * kDeltaChunk * kDeltaChunk * kFull);
+    if (a.P > 1) r.take(a.trans_rows, heads * a.P * a.DKP * a.DKP * kFull);
     if (!train) {
       r.take(a.gates, chunks * kDeltaGates * 4);
       if (a.P > 1) r.take(a.trans, heads * a.P * a.DKP * a.DKP * kFull);

@@ -19,8 +19,11 @@ namespace delta {
 template <typename E, int DK, int NW, bool STATE>
 __global__ __launch_bounds__(64 * NW) void delta_bwd_kernel(DeltaArgs a) {
   constexpr int NT = 64 * NW, CB = DK / 16, CP = DK / 32, CW = 16 * NW, PARTS = Num<E>::PARTS;
-  constexpr int LD = ld_of<E>(DK), LV = ld_of<E>(CW), LT = ld_of<E>(C), FINE = !STATE && PARTS == 2 ? 3 : PARTS;
-  __shared__ __attribute__((aligned(16))) E Ks[C * LD], Qs[C * LD], Os[C * LV], Ts[PARTS][C * LT], Ps[PARTS][C * LT];
+  constexpr int FINE = !STATE && PARTS == 2 ? 3 : PARTS;  // parts of dW
+  typedef Tile<E, DK> K;
+  typedef Tile<E, CW> V;
+  typedef Tile<E, C> M;
+  __shared__ __attribute__((aligned(16))) E Ks[C * K::LD], Qs[C * K::LD], Os[C * V::LD], Ts[PARTS][C * M::LD], Ps[PARTS][C * M::LD];
   __shared__ __attribute__((aligned(16))) GateBlock gates;
   const int segments = STATE ? a.P - 1 : a.P, units = a.B * a.H * segments;  // the first one's own gradient: no use
   const int unit = blockIdx.x % units, tile = blockIdx.x / units;
@@ -42,6 +45,8 @@ __global__ __launch_bounds__(64 * NW) void delta_bwd_kernel(DeltaArgs a) {
     load_state<CB>(D, a.dhT ? a.dhT + (long)bh * a.dk * a.dv : nullptr, a.dk, a.dv, cols ? j + n16 : a.dv);
   }
 
+  arrived<CB>(D);
+
   const E* kp = (const E*)a.k + b * a.ks.b + hk * a.ks.h;
   const E* qp = (const E*)a.q + b * a.qs.b + hk * a.qs.h;
   const E* op = (const E*)a.dO + b * a.dos.b + h * a.dos.h + col0;
@@ -55,113 +60,118 @@ __global__ __launch_bounds__(64 * NW) void delta_bwd_kernel(DeltaArgs a) {
   const auto load = [&](int n) {
     const long t0 = (long)n * C;
     const int left = len - n * C;
-    kin.load(kp + t0 * a.ks.t, a.ks.t, left, a.dk);
-    qin.load(qp + t0 * a.qs.t, a.qs.t, left, a.dk);
-    oin.load(op + t0 * a.dos.t, a.dos.t, left, a.dv - col0);
+    kin.load(kp + t0 * a.ks.t, a.ks.t, left, a.dkr);
+    qin.load(qp + t0 * a.qs.t, a.qs.t, left, a.dkr);
+    oin.load(op + t0 * a.dos.t, a.dos.t, left, a.dvr - col0);
 #pragma unroll
     for (int part = 0; part < PARTS; ++part) tin[part].load(tp + part * plane + (long)n * C * C, C, C, C);
-    if (threadIdx.x < kDeltaGates / 4) gin = reinterpret_cast<const f32x4*>(gp + (long)n * kDeltaGates)[threadIdx.x];
+    gin = reinterpret_cast<const f32x4*>(gp + (long)n * kDeltaGates)[fresh_tid() % (kDeltaGates / 4)];
   };
   if (first < end) load(end - 1);
-  for (int u = threadIdx.x; u < PARTS * C * LT / 8; u += NT) reinterpret_cast<Frag<E>*>(&Ps[0][0])[u] = Frag<E>{};
+  for (int u = threadIdx.x; u < PARTS * C * M::LD / 8; u += NT) reinterpret_cast<Frag<E>*>(&Ps[0][0])[u] = Frag<E>{};
   for (int n = end - 1; n >= first; --n) {
     __syncthreads();
-    kin.store(Ks, LD);
-    qin.store(Qs, LD);
-    oin.store(Os, LV);
+    const int left = len - n * C;
+    kin.store(Ks, left, a.dkr);
+    qin.store(Qs, left, a.dkr);
+    oin.store(Os, left, a.dvr - col0);
 #pragma unroll
-    for (int part = 0; part < PARTS; ++part) tin[part].store(Ts[part], LT);
+    for (int part = 0; part < PARTS; ++part) tin[part].store(Ts[part], C, C);
     if (threadIdx.x < kDeltaGates / 4) reinterpret_cast<f32x4*>(&gates)[threadIdx.x] = gin;
     __syncthreads();
+    if (!STATE && cols && (n % kDeltaMarks == kDeltaMarks - 1 || n == alive - 1)) {  // <state, D> here, for dg
+      const long at = ((long)bh * a.marks + n / kDeltaMarks) * tiles + j / 16;
+      f32x4 S[CB];
+      load_regs<CB>(S, a.mark + at * DK * 16);
+      arrived<CB>(S);
+      float dot = 0.f;
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dot = fmaf(S[cb][i], D[cb][i], dot);
+      for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o);
+      if (lane_id() == 0) a.carry[at] = dot;
+    }
     if (n > first) load(n - 1);
+    const int lane = fresh_tid() & 63, n16 = lane & 15, g4 = lane >> 4, k8 = 8 * g4;
     // P^T's ten tiles: a lane has four queries of one key
     for (int u = wave; u < 10; u += NW) {
       const int it = u < 1 ? 0 : u < 3 ? 1 : u < 6 ? 2 : 3, jt = u - it * (it + 1) / 2;
       f32x4 acc = zero4();
 #pragma unroll
-      for (int p = 0; p < CP; ++p)
-        acc = mma(row_frag(Qs + (16 * it + n16) * LD + 32 * p + 8 * g4), row_frag(Ks + (16 * jt + n16) * LD + 32 * p + 8 * g4), acc);
+      for (int p = 0; p < CP; ++p) acc = mma(K::row(Qs, 16 * it + n16, 32 * p + k8), K::row(Ks, 16 * jt + n16, 32 * p + k8), acc);
       const int key = 16 * jt + n16, i0 = 16 * it + 4 * g4;
 #pragma unroll
       for (int r = 0; r < 4; ++r) acc[r] = key <= i0 + r ? acc[r] * decay_between(gates, i0 + r, key) : 0.f;
+      M::put4(Ps[0], key, i0, acc);
       if constexpr (PARTS == 2) {
-        const bf16x4 hi = to_bf16x4(acc);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[r] -= (float)hi[r];
-        *reinterpret_cast<bf16x4*>(&Ps[0][key * LT + i0]) = hi;
-        *reinterpret_cast<bf16x4*>(&Ps[1][key * LT + i0]) = to_bf16x4(acc);
-      } else {
-        *reinterpret_cast<f32x4*>(&Ps[0][key * LT + i0]) = acc;
+        for (int r = 0; r < 4; ++r) acc[r] -= (float)(E)acc[r];
+        M::put4(Ps[1], key, i0, acc);
       }
     }
-    Split<E> Do[CP];
+    f32x4 dW[4], Y[4];
+    {
+      Split<E> Do[CP];
 #pragma unroll
-    for (int p = 0; p < CP; ++p) Do[p] = split<E>(D[2 * p], D[2 * p + 1]);
-    if (!STATE && cols) {
-      E* to = (E*)a.grad1 + (((long)bh * a.N + n) * a.DVP + j + n16) * DK + 8 * g4;
+      for (int p = 0; p < CP; ++p) Do[p] = split<E>(D[2 * p], D[2 * p + 1]);
+      if (!STATE && cols) {
+        E* to = (E*)a.grad1 + (((long)bh * a.N + n) * a.DVP + j + n16) * DK + k8;
 #pragma unroll
-      for (int p = 0; p < CP; ++p) *reinterpret_cast<Frag<E>*>(to + 32 * p) = Do[p].part[0];
-      if (n % kDeltaMarks == kDeltaMarks - 1 || n == alive - 1) {
-        const long at = ((long)bh * a.marks + n / kDeltaMarks) * tiles + j / 16;
-        f32x4 S[CB];
-        load_regs<CB>(S, a.mark + at * DK * 16);
-        float dot = 0.f;
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) dot = fmaf(S[cb][i], D[cb][i], dot);
-        for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o);
-        if (lane == 0) a.carry[at] = dot;
+        for (int p = 0; p < CP; ++p) *reinterpret_cast<Frag<E>*>(to + 32 * p) = Do[p].part[0];
       }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) dW[t] = zero4();
+#pragma unroll
+      for (int p = 0; p < CP; ++p)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) dW[t] = mma<E>(K::row(Ks, row_of(t, n16), 32 * p + k8), Do[p], dW[t]);
     }
-    f32x4 dW[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      f32x4 acc = zero4();
-      const E* row = Ks + row_of(t, n16) * LD + 8 * g4;
-#pragma unroll
-      for (int p = 0; p < CP; ++p) acc = mma<E>(row_frag(row + 32 * p), Do[p], acc);
       const f32x4 late = *reinterpret_cast<const f32x4*>(gates.late + row4_of(t, g4));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) dW[t][i] = late[i] * acc[i];
+      for (int i = 0; i < 4; ++i) dW[t][i] *= late[i];
     }
     __syncthreads();  // P^T
     Frag<E> dO[2];
 #pragma unroll
-    for (int p = 0; p < 2; ++p) dO[p] = col_frag<E, false>(Os, LV, 32 * p, 16 * wave);
+    for (int p = 0; p < 2; ++p) dO[p] = V::template col<false>(Os, 32 * p, 16 * wave, n16, g4);
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int p = 0; p < 2; ++p)
 #pragma unroll
-      for (int p = t / 2; p < 2; ++p) {
+      for (int t = 0; t < 2 * p + 2; ++t) {
         Split<E> Pf;
 #pragma unroll
-        for (int part = 0; part < PARTS; ++part) Pf.part[part] = row_frag(Ps[part] + row_of(t, n16) * LT + 32 * p + 8 * g4);
+        for (int part = 0; part < PARTS; ++part) Pf.part[part] = M::row(Ps[part], row_of(t, n16), 32 * p + k8);
         dW[t] = mma<E>(Pf, dO[p], dW[t]);
       }
     const Split<E, FINE> Wo[2] = {split<E, FINE>(dW[0], dW[1]), split<E, FINE>(dW[2], dW[3])};
-    f32x4 Y[4];  // -e^gamma dV
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      f32x4 acc = zero4();
+    for (int t = 0; t < 4; ++t) Y[t] = zero4();
 #pragma unroll
-      for (int p = t / 2; p < 2; ++p) {
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int t = 0; t < 2 * p + 2; ++t) {
         Split<E> T;
 #pragma unroll
-        for (int part = 0; part < PARTS; ++part) T.part[part] = row_frag(Ts[part] + row_of(t, n16) * LT + 32 * p + 8 * g4);
-        acc = mma<E>(T, Wo[p], acc);
+        for (int part = 0; part < PARTS; ++part) T.part[part] = M::row(Ts[part], row_of(t, n16), 32 * p + k8);
+        Y[t] = mma<E>(T, Wo[p], Y[t]);
       }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {  // z, then -e^gamma dV
       const int r0 = row4_of(t, g4);
-      if (!STATE && cols) store_rows(acc, a.z + (((long)bh * a.N + n) * C + r0) * a.DVP + j, a.DVP);
+      if (!STATE && cols) store_rows(Y[t], a.z + (((long)bh * a.N + n) * C + r0) * a.DVP + j, a.DVP, n16);
       const f32x4 beta = *reinterpret_cast<const f32x4*>(gates.beta + r0), lead = *reinterpret_cast<const f32x4*>(gates.lead + r0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) Y[t][i] = -lead[i] * beta[i] * acc[i];
+      for (int i = 0; i < 4; ++i) Y[t][i] *= -lead[i] * beta[i];
     }
     const Split<E> Yo[2] = {split<E>(Y[0], Y[1]), split<E>(Y[2], Y[3])};
     Split<E> Oo[2];  // e^gamma dO
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      const f32x4 l0 = *reinterpret_cast<const f32x4*>(gates.lead + 32 * p + 8 * g4);
-      const f32x4 l1 = *reinterpret_cast<const f32x4*>(gates.lead + 32 * p + 8 * g4 + 4);
+      const f32x4 l0 = *reinterpret_cast<const f32x4*>(gates.lead + 32 * p + k8);
+      const f32x4 l1 = *reinterpret_cast<const f32x4*>(gates.lead + 32 * p + k8 + 4);
       f32x4 x, y;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -172,14 +182,18 @@ __global__ __launch_bounds__(64 * NW) void delta_bwd_kernel(DeltaArgs a) {
     }
     const float whole = gates.lead[C - 1];
 #pragma unroll
-    for (int cb = 0; cb < CB; ++cb) {
+    for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
       for (int i = 0; i < 4; ++i) D[cb][i] *= whole;
+    {
+      const int lane = fresh_tid() & 63, n16 = lane & 15, g4 = lane >> 4;
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        D[cb] = mma<E>(col_frag<E, true>(Qs, LD, 32 * p, row4_of(cb, 0)), Oo[p], D[cb]);
-        D[cb] = mma<E>(col_frag<E, true>(Ks, LD, 32 * p, row4_of(cb, 0)), Yo[p], D[cb]);
-      }
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+          D[cb] = mma<E>(K::template col<true>(Qs, 32 * p, row4_of(cb, 0), n16, g4), Oo[p], D[cb]);
+          D[cb] = mma<E>(K::template col<true>(Ks, 32 * p, row4_of(cb, 0), n16, g4), Yo[p], D[cb]);
+        }
     }
   }
   if (!cols) return;
@@ -187,20 +201,24 @@ __global__ __launch_bounds__(64 * NW) void delta_bwd_kernel(DeltaArgs a) {
   else if (seg == 0 && a.dh0) store_state<CB>(D, a.dh0 + (long)bh * a.dk * a.dv, a.dk, a.dv, j + n16);
 }
 
-// One chunk's dq, dk, dv, dbeta and the terms of dg.  A wave has 16 tokens; the value columns come in blocks (dO, W,
-// dV by rows, S0 and D1 transposed), then K and Q take their place in LDS.  Products are transposed: a lane has
-// eight channels of one token.
+// One chunk's dq, dk, dv, dbeta and the terms of dg.  Waves w and w + 4 have 16 tokens, each half of the channels; one
+// of them forms the tokens' rows of H, the other those of G.  The value columns come in blocks (dO, W, dV by rows, S0
+// and D1 transposed), then K, Q, H and G take their place in LDS.  Products are transposed: a lane has eight channels of
+// one token.
 template <typename E, int DK>
-__global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
-  constexpr int CB = DK / 16, CP = DK / 32, BC = sizeof(E) == 2 ? 64 : 32, UPR = BC / 8, PER = C * UPR / 256;
-  constexpr int LD = ld_of<E>(DK), LC = ld_of<E>(BC), LT = ld_of<E>(C);
-  constexpr int STAGE = 3 * C * LC + 2 * BC * LD, LATER = 2 * C * LD + 2 * C * LT;
+__global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a) {
+  constexpr int NT = 512, CB = DK / 16, CH = CB / 2, CP = DK / 32, BC = sizeof(E) == 2 ? 64 : 32, UPR = BC / 8;
+  typedef Tile<E, DK> K;
+  typedef Tile<E, BC> V;
+  typedef Tile<E, C> M;
+  constexpr int STAGE = 3 * C * V::LD + 2 * BC * K::LD, LATER = 2 * C * K::LD + 2 * C * M::LD;
   __shared__ __attribute__((aligned(16))) E lds[STAGE > LATER ? STAGE : LATER];
   __shared__ __attribute__((aligned(16))) GateBlock gates;
-  E *Os = lds, *Ws = Os + C * LC, *Ys = Ws + C * LC, *S0 = Ys + C * LC, *D1 = S0 + BC * LD;
-  E *Ks = lds, *Qs = Ks + C * LD, *HT = Qs + C * LD, *GT = HT + C * LT;
+  E *Os = lds, *Ws = Os + C * V::LD, *Ys = Ws + C * V::LD, *S0 = Ys + C * V::LD, *D1 = S0 + BC * K::LD;
+  E *Ks = lds, *Qs = Ks + C * K::LD, *HT = Qs + C * K::LD, *GT = HT + C * M::LD;
   const int n = blockIdx.x % a.N, bh = blockIdx.x / a.N, b = bh / a.H, h = bh - b * a.H, hk = h / (a.H / a.Hk);
-  const int len = length_of(a, b), lane = lane_id(), wave = wave_id(), n16 = lane & 15, g4 = lane >> 4;
+  const int len = length_of(a, b), lane = lane_id(), n16 = lane & 15, g4 = lane >> 4;
+  const int wave = wave_id() & 3, half = wave_id() >> 2;  // half: channels CH * 16 half on, and G
   const long t0 = (long)n * C, row0 = (long)bh * a.N * C + t0;  // row0: in the padded tensors
   const int left = len - n * C, rows = min(C, a.T - n * C);     // rows of the chunk that exist
   const bool shared = a.H != a.Hk;
@@ -216,11 +234,11 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
     }
   };
   if (left <= 0) {  // behind the sequence's end
-    for (int u = threadIdx.x; u < C * CP * 4; u += 256) {
+    for (int u = threadIdx.x; u < C * CP * 4; u += NT) {
       put(a.dq, a.dq_heads, u / (CP * 4), u % (CP * 4) * 8, zero4(), zero4());
       put(a.dk_, a.dk_heads, u / (CP * 4), u % (CP * 4) * 8, zero4(), zero4());
     }
-    for (int u = threadIdx.x; u < rows * ((a.dv + 3) / 4); u += 256) {
+    for (int u = threadIdx.x; u < rows * ((a.dv + 3) / 4); u += NT) {
       const int r = u / ((a.dv + 3) / 4), c = (u - r * ((a.dv + 3) / 4)) * 4;
       store4_part<E>((E*)a.dv_ + ((long)bh * a.T + t0 + r) * a.dv + c, zero4(), a.dv - c);
     }
@@ -234,30 +252,36 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
   const E* v = (const E*)a.v + b * a.vs.b + h * a.vs.h + t0 * a.vs.t;
   const E* o = (const E*)a.o + ((long)bh * a.T + t0) * a.dv;
   typedef typename Raw<E, 8>::type R8;
-  f32x4 dQ[CB], dK[CB], dS[CB], dP[4], G[4];
+  f32x4 dQ[CH], dK[CH], dS[CH], H[4];  // H: or G
 #pragma unroll
-  for (int cb = 0; cb < CB; ++cb) dQ[cb] = dK[cb] = dS[cb] = zero4();
+  for (int cb = 0; cb < CH; ++cb) dQ[cb] = dK[cb] = dS[cb] = zero4();
 #pragma unroll
-  for (int t = 0; t < 4; ++t) dP[t] = G[t] = zero4();
-  float at[PER] = {}, db[PER] = {};
+  for (int t = 0; t < 4; ++t) H[t] = zero4();
+  float at = 0.f, db = 0.f;
+  const int r = threadIdx.x / UPR, cc = threadIdx.x % UPR * 8;  // the lane's row and columns of a block
   for (int c0 = 0; c0 < a.DVP; c0 += BC) {
+    TileIn<E, BC, DK, NT> s0, d1;
+    const long st = (((long)bh * a.N + n) * a.DVP + c0) * DK;
+    s0.load((const E*)a.state0 + st, DK, a.DVP - c0, DK);
+    d1.load((const E*)a.grad1 + st, DK, a.DVP - c0, DK);
     if (c0) __syncthreads();
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int u = threadIdx.x + i * 256, r = u / UPR, cc = u % UPR * 8, c = c0 + cc;
+    if (r < C) {
+      const int c = c0 + cc;
       typedef short S8 __attribute__((ext_vector_type(8)));
       R8 x = {}, ov = {}, vv = {};
       S8 rest = {};
       f32x8 z = {}, d = {};
-      if (r < left && c < a.dv) {
-        x = load8_part<E>(dO + r * a.dos.t + c, a.dv - c);
-        ov = load8_part<E>(o + (long)r * a.dv + c, a.dv - c);
-        vv = load8_part<E>(v + r * a.vs.t + c, a.dv - c);
-        if (sizeof(E) == 2) rest = *reinterpret_cast<const S8*>(a.o_rest + (row0 + r) * a.DVP + c);
-      }
-      if (c < a.DVP) {
-        z = row_frag(a.z + (row0 + r) * a.DVP + c);
-        d = row_frag(a.err + (row0 + r) * a.DVP + c);
+      const bool live = r < left && c < a.dv;
+      {  // every lane loads, as in TileIn
+        const int rr = min(r, min(left, rows) - 1), ci = c < a.dvr ? c : 0;
+        x = *reinterpret_cast<const R8*>(dO + rr * a.dos.t + ci);
+        vv = *reinterpret_cast<const R8*>(v + rr * a.vs.t + ci);
+        if (sizeof(E) == 2) rest = *reinterpret_cast<const S8*>(a.o_rest + (row0 + rr) * a.DVP + ci);
+        if (a.dv % 8 == 0) ov = *reinterpret_cast<const R8*>(o + (long)rr * a.dv + ci);
+        else ov = load8_part<E>(o + (long)rr * a.dv + min(ci, a.dv - 1), min(a.dv - ci, 8));
+        const int cz = c < a.DVP ? c : 0;
+        z = load8(a.z + (row0 + r) * a.DVP + cz);
+        d = load8(a.err + (row0 + r) * a.DVP + cz);
       }
       const float beta = gates.beta[r];
       typedef E v8 __attribute__((ext_vector_type(8), aligned(16)));
@@ -265,101 +289,83 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
       f32x4 y0, y1;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
+        if (c >= a.DVP) z[e] = d[e] = 0.f;
+        if (!live || c + e >= a.dv) x[e] = vv[e] = (E)0.f;
         const float yv = beta * z[e];
         float of = (float)ov[e];
-        if constexpr (sizeof(E) == 2) of = c + e < a.dv ? with_rest(ov[e], rest[e]) : 0.f;
-        at[i] = fmaf((float)x[e], of, at[i]);
-        at[i] = fmaf(-yv, (float)vv[e], at[i]);
-        db[i] = fmaf(z[e], d[e], db[i]);
+        if constexpr (sizeof(E) == 2) of = with_rest(ov[e], rest[e]);
+        if (!live || c + e >= a.dv) of = 0.f;
+        at = fmaf((float)x[e], of, at);
+        at = fmaf(-yv, (float)vv[e], at);
+        db = fmaf(z[e], d[e], db);
         (e < 4 ? y0 : y1)[e & 3] = yv;
         w[e] = (E)(beta * d[e]);
         y[e] = (E)yv;
         ox[e] = x[e];
       }
-      *reinterpret_cast<v8*>(Os + r * LC + cc) = ox;
-      *reinterpret_cast<v8*>(Ws + r * LC + cc) = w;
-      *reinterpret_cast<v8*>(Ys + r * LC + cc) = y;
+      *reinterpret_cast<v8*>(Os + V::at(r, cc)) = ox;
+      *reinterpret_cast<v8*>(Ws + V::at(r, cc)) = w;
+      *reinterpret_cast<v8*>(Ys + V::at(r, cc)) = y;
       if (r < rows && c < a.dv) {
         E* to = (E*)a.dv_ + ((long)bh * a.T + t0 + r) * a.dv + c;
         store4_part<E>(to, y0, a.dv - c);
         store4_part<E>(to + 4, y1, a.dv - c - 4);
       }
     }
-    {
-      const long st = (((long)bh * a.N + n) * a.DVP + c0) * DK;
-      TileIn<E, BC, DK, 256> in;
-      in.load((const E*)a.state0 + st, DK, a.DVP - c0, DK);
-      in.store(S0, LD);
-      in.load((const E*)a.grad1 + st, DK, a.DVP - c0, DK);
-      in.store(D1, LD);
-    }
+    s0.store(S0, a.DVP - c0, DK);
+    d1.store(D1, a.DVP - c0, DK);
     __syncthreads();
 #pragma unroll
     for (int p = 0; p < BC / 32; ++p) {
-      const int off = (16 * wave + n16) * LC + 32 * p + 8 * g4;
-      const Frag<E> fo = row_frag(Os + off), fw = row_frag(Ws + off), fy = row_frag(Ys + off);
+      const int row = 16 * wave + n16, col = 32 * p + 8 * g4;
+      const Frag<E> fo = V::row(Os, row, col), fw = V::row(Ws, row, col), fy = V::row(Ys, row, col);
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb) {
-        const Frag<E> s = col_frag<E, true>(S0, LD, 32 * p, row4_of(cb, 0));
+      for (int cb = 0; cb < CH; ++cb) {
+        const int ch = row4_of(CH * half + cb, 0);
+        const Frag<E> s = K::template col<true>(S0, 32 * p, ch, n16, g4);
         dQ[cb] = mma(s, fo, dQ[cb]);
         dS[cb] = mma(s, fy, dS[cb]);
-        dK[cb] = mma(col_frag<E, true>(D1, LD, 32 * p, row4_of(cb, 0)), fw, dK[cb]);
+        dK[cb] = mma(K::template col<true>(D1, 32 * p, ch, n16, g4), fw, dK[cb]);
       }
+      const Frag<E> f = half ? fy : fo;
 #pragma unroll
       for (int t = 0; t < 4; ++t)
-        if (t <= wave) {
-          const Frag<E> w = row_frag(Ws + (16 * t + n16) * LC + 32 * p + 8 * g4);
-          dP[t] = mma(fo, w, dP[t]);
-          G[t] = mma(fy, w, G[t]);
-        }
+        if (t <= wave) H[t] = mma(f, V::row(Ws, 16 * t + n16, col), H[t]);
     }
   }
+  TileIn<E, C, DK, NT> kin, qin;
+  kin.load((const E*)a.k + b * a.ks.b + hk * a.ks.h + t0 * a.ks.t, a.ks.t, left, a.dkr);
+  qin.load((const E*)a.q + b * a.qs.b + hk * a.qs.h + t0 * a.qs.t, a.qs.t, left, a.dkr);
   // the rows' sums
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-#pragma unroll
-    for (int s = 1; s < UPR; s *= 2) {
-      at[i] += __shfl_xor(at[i], s);
-      db[i] += __shfl_xor(db[i], s);
-    }
-    const int u = threadIdx.x + i * 256, r = u / UPR;
-    if (u % UPR == 0) {
-      a.at[row0 + r] = r < left ? at[i] : 0.f;
-      if (r < rows) a.dbeta[(long)bh * a.T + t0 + r] = r < left ? db[i] : 0.f;
-    }
+  for (int s = 1; s < UPR; s *= 2) {
+    at += __shfl_xor(at, s);
+    db += __shfl_xor(db, s);
+  }
+  if (cc == 0 && r < C) {
+    a.at[row0 + r] = r < left ? at : 0.f;
+    if (r < rows) a.dbeta[(long)bh * a.T + t0 + r] = r < left ? db : 0.f;
   }
   __syncthreads();
-  {
-    TileIn<E, C, DK, 256> in;
-    in.load((const E*)a.k + b * a.ks.b + hk * a.ks.h + t0 * a.ks.t, a.ks.t, left, a.dk);
-    in.store(Ks, LD);
-    in.load((const E*)a.q + b * a.qs.b + hk * a.qs.h + t0 * a.qs.t, a.qs.t, left, a.dk);
-    in.store(Qs, LD);
-  }
+  kin.store(Ks, left, a.dkr);
+  qin.store(Qs, left, a.dkr);
   // H^T and G^T: a lane has four queries of one key
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     if (t > (wave | 1)) continue;
     const int key = 16 * t + n16, i0 = 16 * wave + 4 * g4;
-    f32x4 x, y;
+    f32x4 x;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const float e = key <= i0 + r ? decay_between(gates, i0 + r, key) : 0.f;
-      x[r] = dP[t][r] * e;
-      y[r] = key < i0 + r ? -G[t][r] * e : 0.f;
+    for (int i = 0; i < 4; ++i) {
+      const bool below = half ? key < i0 + i : key <= i0 + i;
+      x[i] = below ? (half ? -H[t][i] : H[t][i]) * decay_between(gates, i0 + i, key) : 0.f;
     }
-    if constexpr (sizeof(E) == 2) {
-      *reinterpret_cast<bf16x4*>(HT + key * LT + i0) = to_bf16x4(x);
-      *reinterpret_cast<bf16x4*>(GT + key * LT + i0) = to_bf16x4(y);
-    } else {
-      *reinterpret_cast<f32x4*>(HT + key * LT + i0) = x;
-      *reinterpret_cast<f32x4*>(GT + key * LT + i0) = y;
-    }
+    M::put4(half ? GT : HT, key, i0, x);
   }
   const int row = 16 * wave + n16;
   const float lead = gates.lead[row], late = gates.late[row];
 #pragma unroll
-  for (int cb = 0; cb < CB; ++cb)
+  for (int cb = 0; cb < CH; ++cb)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       dQ[cb][i] *= lead;
@@ -371,30 +377,46 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
     const bool before = p <= wave / 2, after = p >= wave / 2;  // keys up to the wave's rows, queries from them on
     Frag<E> hi = {}, gi = {}, hj = {}, gj = {};
     if (before) {
-      hi = col_frag<E, false>(HT, LT, 32 * p, 16 * wave);
-      gi = col_frag<E, false>(GT, LT, 32 * p, 16 * wave);
+      hi = M::template col<false>(HT, 32 * p, 16 * wave, n16, g4);
+      gi = M::template col<false>(GT, 32 * p, 16 * wave, n16, g4);
     }
     if (after) {
-      hj = row_frag(HT + row * LT + 32 * p + 8 * g4);
-      gj = row_frag(GT + row * LT + 32 * p + 8 * g4);
+      hj = M::row(HT, row, 32 * p + 8 * g4);
+      gj = M::row(GT, row, 32 * p + 8 * g4);
     }
 #pragma unroll
-    for (int cb = 0; cb < CB; ++cb) {
-      const Frag<E> kf = col_frag<E, true>(Ks, LD, 32 * p, row4_of(cb, 0));
+    for (int cb = 0; cb < CH; ++cb) {
+      const int ch = row4_of(CH * half + cb, 0);
+      const Frag<E> kf = K::template col<true>(Ks, 32 * p, ch, n16, g4);
       if (before) {
         dQ[cb] = mma(kf, hi, dQ[cb]);
         dK[cb] = mma(kf, gi, dK[cb]);
       }
       if (after) {
         dK[cb] = mma(kf, gj, dK[cb]);
-        dK[cb] = mma(col_frag<E, true>(Qs, LD, 32 * p, row4_of(cb, 0)), hj, dK[cb]);
+        dK[cb] = mma(K::template col<true>(Qs, 32 * p, ch, n16, g4), hj, dK[cb]);
       }
     }
   }
+  // CH tiles: pairs of 8 channels a lane; one tile alone where a half has 16 channels
+  if constexpr (CH % 2 == 0) {
 #pragma unroll
-  for (int p = 0; p < CP; ++p) {
-    put(a.dq, a.dq_heads, row, 32 * p + 8 * g4, dQ[2 * p], dQ[2 * p + 1]);
-    put(a.dk_, a.dk_heads, row, 32 * p + 8 * g4, dK[2 * p], dK[2 * p + 1]);
+    for (int p = 0; p < CH / 2; ++p) {
+      put(a.dq, a.dq_heads, row, 32 * (CH / 2 * half + p) + 8 * g4, dQ[2 * p], dQ[2 * p + 1]);
+      put(a.dk_, a.dk_heads, row, 32 * (CH / 2 * half + p) + 8 * g4, dK[2 * p], dK[2 * p + 1]);
+    }
+  } else {
+    const int c = 8 * g4 + 4 * half;
+    if (row < rows && c < a.dk) {
+      const long to = ((long)bh * a.T + t0 + row) * a.dk + c;
+      if (shared) {
+        store4_part<float>(a.dq_heads + to, dQ[0], a.dk - c);
+        store4_part<float>(a.dk_heads + to, dK[0], a.dk - c);
+      } else {
+        store4_part<E>((E*)a.dq + to, dQ[0], a.dk - c);
+        store4_part<E>((E*)a.dk_ + to, dK[0], a.dk - c);
+      }
+    }
   }
 }
 
@@ -451,10 +473,10 @@ static void delta_bwd_run(const DeltaArgs& a, hipStream_t s) {
   const int heads = a.B * a.H, tiles = (a.dv + CW - 1) / CW;
   if (a.P > 1) {
     delta_bwd_kernel<E, DK, NW, true><<<heads * (a.P - 1) * tiles, 64 * NW, 0, s>>>(a);
-    delta_scan_kernel<E, DK, NW, true><<<heads * tiles, 64 * NW, 0, s>>>(a);
+    delta_scan_kernel<E, DK, true><<<heads * ((a.dv + 31) / 32), 4 * DK, 0, s>>>(a);
   }
   delta_bwd_kernel<E, DK, NW, false><<<heads * a.P * tiles, 64 * NW, 0, s>>>(a);
-  delta_grad_kernel<E, DK><<<heads * a.N, 256, 0, s>>>(a);
+  delta_grad_kernel<E, DK><<<heads * a.N, 512, 0, s>>>(a);
   delta_gate_grad_kernel<<<heads * a.marks, 256, 0, s>>>(a);
   if (a.H != a.Hk) {
     const long long blocks = ((long long)a.B * a.Hk * a.T * a.dk + 255) / 256;
@@ -473,7 +495,8 @@ static void delta_bwd_rows(const DeltaArgs& a, hipStream_t s) {
   else delta_bwd_cols<E, 128>(a, s);
 }
 
-hipError_t launch_delta_bwd(const DeltaArgs& a, hipStream_t s) {
+hipError_t launch_delta_bwd(DeltaArgs a, hipStream_t s) {
+  delta_pack(a, true, s);
   if (a.dtype == GLA_BF16) delta_bwd_rows<bf16>(a, s);
   else delta_bwd_rows<float>(a, s);
   return hipGetLastError();

@@ -15,6 +15,17 @@
 namespace gla {
 namespace delta {
 
+// Rows of d elements into rows of r, d rounded up to 8, the rest zero; 8 elements a lane.
+template <typename E>
+__global__ __launch_bounds__(256) void delta_pack_kernel(const E* from, Strides st, E* to, int heads, int T, int d, int r, long units) {
+  for (long u = (long)blockIdx.x * 256 + threadIdx.x; u < units; u += (long)gridDim.x * 256) {
+    const int c = (int)(u % (r / 8)) * 8;
+    const long row = u / (r / 8), bh = row / T, t = row - bh * T, b = bh / heads, h = bh - b * heads;
+    typedef E v8 __attribute__((ext_vector_type(8), aligned(16)));
+    *reinterpret_cast<v8*>(to + u * 8) = load8_part<E>(from + b * st.b + h * st.h + t * st.t + c, d - c);
+  }
+}
+
 // ---------------------------------------------------------------------------------------- gates, inverse
 
 // (I + L)^-1 of a unit lower triangular 64 x 64 matrix in float32: its 16 x 16 diagonal blocks by forward
@@ -22,8 +33,9 @@ namespace delta {
 // Two of them at once: L = B beta (columns scaled) and, transposed at the end, L = beta B for the backward.
 template <typename E, int DK, bool TRAIN>
 __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
-  constexpr int LD = ld_of<E>(DK), LF = 66;
-  constexpr int KBYTES = C * LD * sizeof(E), XBYTES = C * LF * 4;
+  constexpr int LF = 66;
+  typedef Tile<E, DK> K;
+  constexpr int KBYTES = C * K::LD * sizeof(E), XBYTES = C * LF * 4;
   __shared__ __attribute__((aligned(16))) unsigned char raw[KBYTES > XBYTES ? KBYTES : XBYTES];
   __shared__ __attribute__((aligned(16))) float Bm[C * LF], X1[C * LF];  // B; the inverse with scaled columns
   __shared__ __attribute__((aligned(16))) GateBlock gates;
@@ -35,7 +47,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
   const int lane = lane_id(), wave = wave_id(), n16 = lane & 15, g4 = lane >> 4;
   const long t0 = (long)n * C;
   TileIn<E, C, DK, 256> k;
-  k.load((const E*)a.k + b * a.ks.b + (h / (a.H / a.Hk)) * a.ks.h + t0 * a.ks.t, a.ks.t, len - n * C, a.dk);
+  k.load((const E*)a.k + b * a.ks.b + (h / (a.H / a.Hk)) * a.ks.h + t0 * a.ks.t, a.ks.t, len - n * C, a.dkr);
   if (wave == 0) {
     const long t = t0 + lane;
     const bool live = t < len;
@@ -54,14 +66,14 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
     gates.low[lane] = (float)(x - (double)(float)x);
     gates.beta[lane] = beta;
   }
-  k.store(Ks, LD);
+  k.store(Ks, len - n * C, a.dkr);
   __syncthreads();
   // B, one row tile a wave
   for (int jt = 0; jt <= wave; ++jt) {
     f32x4 acc = zero4();
 #pragma unroll
     for (int p = 0; p < DK / 32; ++p)
-      acc = mma(row_frag(Ks + (16 * wave + n16) * LD + 32 * p + 8 * g4), row_frag(Ks + (16 * jt + n16) * LD + 32 * p + 8 * g4), acc);
+      acc = mma(K::row(Ks, 16 * wave + n16, 32 * p + 8 * g4), K::row(Ks, 16 * jt + n16, 32 * p + 8 * g4), acc);
     const int j = 16 * jt + n16;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -158,9 +170,12 @@ enum { INFER = 0, TRAIN = 1, STATE = 2 };
 template <typename E, int DK, int NW, int MODE>
 __global__ __launch_bounds__(64 * NW) void delta_fwd_kernel(DeltaArgs a) {
   constexpr int NT = 64 * NW, CB = DK / 16, CP = DK / 32, CW = 16 * NW, PARTS = Num<E>::PARTS;
-  constexpr int LD = ld_of<E>(DK), LV = ld_of<E>(CW), LT = ld_of<E>(C), FINE = MODE == TRAIN && PARTS == 2 ? 3 : PARTS;
-  __shared__ __attribute__((aligned(16))) E Ks[C * LD], Vs[C * LV], Ts[PARTS][C * LT];
-  __shared__ __attribute__((aligned(16))) E Qs[MODE == STATE ? 8 : C * LD], Ps[MODE == STATE ? 1 : PARTS][MODE == STATE ? 8 : C * LT];
+  constexpr int FINE = MODE == TRAIN && PARTS == 2 ? 3 : PARTS, PP = MODE == TRAIN ? PARTS : 1;  // parts of W, of P
+  typedef Tile<E, DK> K;
+  typedef Tile<E, CW> V;
+  typedef Tile<E, C> M;
+  __shared__ __attribute__((aligned(16))) E Ks[C * K::LD], Vs[C * V::LD], Ts[PARTS][C * M::LD];
+  __shared__ __attribute__((aligned(16))) E Qs[MODE == STATE ? 8 : C * K::LD], Ps[PP][MODE == STATE ? 8 : C * M::LD];
   __shared__ __attribute__((aligned(16))) GateBlock gates;
   const bool chained = MODE == STATE && a.err;  // a backward follows
   const int segments = MODE == STATE && !chained ? a.P - 1 : a.P, units = a.B * a.H * segments;
@@ -189,6 +204,8 @@ __global__ __launch_bounds__(64 * NW) void delta_fwd_kernel(DeltaArgs a) {
     load_state<CB>(S, a.h0 ? a.h0 + (long)bh * a.dk * a.dv : nullptr, a.dk, a.dv, cols ? j + n16 : a.dv);
   }
 
+  arrived<CB>(S);
+
   const E* kp = (const E*)a.k + b * a.ks.b + hk * a.ks.h;
   const E* qp = (const E*)a.q + b * a.qs.b + hk * a.qs.h;
   const E* vp = (const E*)a.v + b * a.vs.b + h * a.vs.h + col0;
@@ -196,50 +213,48 @@ __global__ __launch_bounds__(64 * NW) void delta_fwd_kernel(DeltaArgs a) {
   const float* gp = a.gates + (long)bh * a.N * kDeltaGates;
   const long plane = (long)a.B * a.H * a.N * C * C;
   TileIn<E, C, DK, NT> kin, qin;
-  TileIn<E, C, CW, NT> vin;
+  TileIn<E, C, CW, NT> vin{};
   TileIn<E, C, C, NT> tin[PARTS];
   f32x4 gin = zero4();
   const auto load = [&](int n) {
     const long t0 = (long)n * C;
     const int left = len - n * C;
-    kin.load(kp + t0 * a.ks.t, a.ks.t, left, a.dk);
-    if (MODE != STATE) qin.load(qp + t0 * a.qs.t, a.qs.t, left, a.dk);
-    vin.load(vp + t0 * a.vs.t, a.vs.t, transition ? 0 : left, a.dv - col0);
+    kin.load(kp + t0 * a.ks.t, a.ks.t, left, a.dkr);
+    if (MODE != STATE) qin.load(qp + t0 * a.qs.t, a.qs.t, left, a.dkr);
+    if (!transition) vin.load(vp + t0 * a.vs.t, a.vs.t, left, a.dvr - col0);
 #pragma unroll
     for (int part = 0; part < PARTS; ++part) tin[part].load(tp + part * plane + (long)n * C * C, C, C, C);
-    if (threadIdx.x < kDeltaGates / 4) gin = reinterpret_cast<const f32x4*>(gp + (long)n * kDeltaGates)[threadIdx.x];
+    gin = reinterpret_cast<const f32x4*>(gp + (long)n * kDeltaGates)[fresh_tid() % (kDeltaGates / 4)];
   };
   if (first < end) load(first);
   if constexpr (MODE != STATE)  // the blocks of P above the diagonal that the products read
-    for (int u = threadIdx.x; u < PARTS * C * LT / 8; u += NT) reinterpret_cast<Frag<E>*>(&Ps[0][0])[u] = Frag<E>{};
+    for (int u = threadIdx.x; u < PP * C * M::LD / 8; u += NT) reinterpret_cast<Frag<E>*>(&Ps[0][0])[u] = Frag<E>{};
   for (int n = first; n < end; ++n) {
     __syncthreads();
-    kin.store(Ks, LD);
-    if (MODE != STATE) qin.store(Qs, LD);
-    vin.store(Vs, LV);
+    const int left = len - n * C;
+    kin.store(Ks, left, a.dkr);
+    if (MODE != STATE) qin.store(Qs, left, a.dkr);
+    vin.store(Vs, transition ? 0 : left, a.dvr - col0);
 #pragma unroll
-    for (int part = 0; part < PARTS; ++part) tin[part].store(Ts[part], LT);
+    for (int part = 0; part < PARTS; ++part) tin[part].store(Ts[part], C, C);
     if (threadIdx.x < kDeltaGates / 4) reinterpret_cast<f32x4*>(&gates)[threadIdx.x] = gin;
     __syncthreads();
     if (n + 1 < end) load(n + 1);
-    if (MODE != STATE) {  // P's ten tiles, transposed products: a lane has four keys of one query
+    const int lane = fresh_tid() & 63, n16 = lane & 15, g4 = lane >> 4, k8 = 8 * g4;
+    if constexpr (MODE != STATE) {  // P's ten tiles, transposed products: a lane has four keys of one query
       for (int u = wave; u < 10; u += NW) {
         const int it = u < 1 ? 0 : u < 3 ? 1 : u < 6 ? 2 : 3, jt = u - it * (it + 1) / 2;
         f32x4 acc = zero4();
 #pragma unroll
-        for (int p = 0; p < CP; ++p)
-          acc = mma(row_frag(Ks + (16 * jt + n16) * LD + 32 * p + 8 * g4), row_frag(Qs + (16 * it + n16) * LD + 32 * p + 8 * g4), acc);
+        for (int p = 0; p < CP; ++p) acc = mma(K::row(Ks, 16 * jt + n16, 32 * p + k8), K::row(Qs, 16 * it + n16, 32 * p + k8), acc);
         const int i = 16 * it + n16, k0 = 16 * jt + 4 * g4;
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[r] = k0 + r <= i ? acc[r] * decay_between(gates, i, k0 + r) : 0.f;
-        if constexpr (PARTS == 2) {
-          const bf16x4 hi = to_bf16x4(acc);
+        M::put4(Ps[0], i, k0, acc);
+        if constexpr (PP == 2) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[r] -= (float)hi[r];
-          *reinterpret_cast<bf16x4*>(&Ps[0][i * LT + k0]) = hi;
-          *reinterpret_cast<bf16x4*>(&Ps[1][i * LT + k0]) = to_bf16x4(acc);
-        } else {
-          *reinterpret_cast<f32x4*>(&Ps[0][i * LT + k0]) = acc;
+          for (int r = 0; r < 4; ++r) acc[r] -= (float)(E)acc[r];
+          M::put4(Ps[1], i, k0, acc);
         }
       }
     }
@@ -247,94 +262,111 @@ __global__ __launch_bounds__(64 * NW) void delta_fwd_kernel(DeltaArgs a) {
     Split<E> So[CP];
 #pragma unroll
     for (int p = 0; p < CP; ++p) So[p] = split<E>(S[2 * p], S[2 * p + 1]);
-    f32x4 Y[4];
+    f32x4 Y[4], W[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) Y[t] = zero4();
+#pragma unroll
+    for (int p = 0; p < CP; ++p)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) Y[t] = mma<E>(K::row(Ks, row_of(t, n16), 32 * p + k8), So[p], Y[t]);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      f32x4 acc = zero4();
-      const E* row = Ks + row_of(t, n16) * LD + 8 * g4;
-#pragma unroll
-      for (int p = 0; p < CP; ++p) acc = mma<E>(row_frag(row + 32 * p), So[p], acc);
       const int r0 = row4_of(t, g4);
-      const f32x4 lead = *reinterpret_cast<const f32x4*>(gates.lead + r0);
-      Y[t] = rows4<E>(Vs, LV, r0, 16 * wave);
+      const f32x4 lead = *reinterpret_cast<const f32x4*>(gates.lead + r0), v = V::rows4(Vs, r0, 16 * wave, n16);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) Y[t][i] = fmaf(-lead[i], acc[i], Y[t][i]);
+      for (int i = 0; i < 4; ++i) Y[t][i] = fmaf(-lead[i], Y[t][i], v[i]);
     }
     // delta, W and e^(gamma_C - gamma) W
     const Split<E, FINE> Yo[2] = {split<E, FINE>(Y[0], Y[1]), split<E, FINE>(Y[2], Y[3])};
-    f32x4 W[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      f32x4 acc = zero4();
+    for (int t = 0; t < 4; ++t) W[t] = zero4();
 #pragma unroll
-      for (int p = 0; p <= t / 2; ++p) {
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int t = 2 * p; t < 4; ++t) {
         Split<E> T;
 #pragma unroll
-        for (int part = 0; part < PARTS; ++part) T.part[part] = row_frag(Ts[part] + row_of(t, n16) * LT + 32 * p + 8 * g4);
-        acc = mma<E>(T, Yo[p], acc);
+        for (int part = 0; part < PARTS; ++part) T.part[part] = M::row(Ts[part], row_of(t, n16), 32 * p + k8);
+        W[t] = mma<E>(T, Yo[p], W[t]);
       }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
       const int r0 = row4_of(t, g4);
-      if (MODE == TRAIN && cols) store_rows(acc, a.err + (((long)bh * a.N + n) * C + r0) * a.DVP + j, a.DVP);
+      if (MODE == TRAIN && cols) store_rows(W[t], a.err + (((long)bh * a.N + n) * C + r0) * a.DVP + j, a.DVP, n16);
       const f32x4 beta = *reinterpret_cast<const f32x4*>(gates.beta + r0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) W[t][i] = beta[i] * acc[i];
+      for (int i = 0; i < 4; ++i) W[t][i] *= beta[i];
     }
     if (MODE == TRAIN && cols) {
-      E* to = (E*)a.state0 + (((long)bh * a.N + n) * a.DVP + j + n16) * DK + 8 * g4;
+      E* to = (E*)a.state0 + (((long)bh * a.N + n) * a.DVP + j + n16) * DK + k8;
 #pragma unroll
       for (int p = 0; p < CP; ++p) *reinterpret_cast<Frag<E>*>(to + 32 * p) = So[p].part[0];
     }
-    if (MODE != STATE) {
+    if constexpr (MODE != STATE) {
       const Split<E, FINE> Wo[2] = {split<E, FINE>(W[0], W[1]), split<E, FINE>(W[2], W[3])};
       __syncthreads();
       // O, transposed products: a lane has four columns of one token.  A forward-only call rounds the state, W and P
       // to one bf16 here: o is rounded to it after all.
+      const int lane = fresh_tid() & 63, n16 = lane & 15, g4 = lane >> 4, k8 = 8 * g4;
+      f32x4 O[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) O[t] = zero4();
+#pragma unroll
+      for (int p = 0; p < CP; ++p)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const Frag<E> q = K::row(Qs, 16 * t + n16, 32 * p + k8);
+          O[t] = MODE == TRAIN ? mma<E>(So[p], q, O[t]) : mma(So[p].part[0], q, O[t]);
+        }
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        f32x4 acc = zero4();
+        const float lead = gates.lead[16 * t + n16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) O[t][i] *= lead;
+      }
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int t = 2 * p; t < 4; ++t) {
+          Split<E, PP> Pf;
+#pragma unroll
+          for (int part = 0; part < PP; ++part) Pf.part[part] = M::row(Ps[part], 16 * t + n16, 32 * p + k8);
+          O[t] = MODE == TRAIN ? mma<E>(Wo[p], Pf, O[t]) : mma(Wo[p].part[0], Pf.part[0], O[t]);
+        }
+      const long row0 = (long)n * C;
+      E* to = (E*)a.o + ((long)bh * a.T + row0) * a.dv + j;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
         const int row = 16 * t + n16;
+        if (!cols || row >= len - n * C) continue;
+        store4_part<E>(to + row * a.dv + 4 * g4, O[t], a.dv - j - 4 * g4);
+        if constexpr (MODE == TRAIN && PARTS == 2) {
+          typedef short s16x4 __attribute__((ext_vector_type(4)));
+          s16x4 rest;
 #pragma unroll
-        for (int p = 0; p < CP; ++p) {
-          const Frag<E> q = row_frag(Qs + row * LD + 32 * p + 8 * g4);
-          acc = MODE == TRAIN ? mma<E>(So[p], q, acc) : mma(So[p].part[0], q, acc);
-        }
-        const float lead = gates.lead[row];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] *= lead;
-#pragma unroll
-        for (int p = 0; p <= t / 2; ++p) {
-          Split<E> Pf;
-#pragma unroll
-          for (int part = 0; part < (MODE == TRAIN ? PARTS : 1); ++part) Pf.part[part] = row_frag(Ps[part] + row * LT + 32 * p + 8 * g4);
-          acc = MODE == TRAIN ? mma<E>(Wo[p], Pf, acc) : mma(Wo[p].part[0], Pf.part[0], acc);
-        }
-        const long token = (long)n * C + row;
-        if (cols && token < len) {
-          store4_part<E>((E*)a.o + ((long)bh * a.T + token) * a.dv + j + 4 * g4, acc, a.dv - j - 4 * g4);
-          if constexpr (MODE == TRAIN && PARTS == 2) {
-            typedef short s16x4 __attribute__((ext_vector_type(4)));
-            s16x4 rest;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) rest[i] = rest_of(acc[i], (bf16)acc[i]);
-            *reinterpret_cast<s16x4*>(a.o_rest + ((long)bh * a.N * C + token) * a.DVP + j + 4 * g4) = rest;
-          }
+          for (int i = 0; i < 4; ++i) rest[i] = rest_of(O[t][i], (bf16)O[t][i]);
+          *reinterpret_cast<s16x4*>(a.o_rest + ((long)bh * a.N * C + row0 + row) * a.DVP + j + 4 * g4) = rest;
         }
       }
     }
+    {
+      const int lane = fresh_tid() & 63, n16 = lane & 15, g4 = lane >> 4;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const f32x4 late = *reinterpret_cast<const f32x4*>(gates.late + row4_of(t, g4));
+      for (int t = 0; t < 4; ++t) {
+        const f32x4 late = *reinterpret_cast<const f32x4*>(gates.late + row4_of(t, g4));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) W[t][i] *= late[i];
-    }
-    const Split<E> Wl[2] = {split<E>(W[0], W[1]), split<E>(W[2], W[3])};
-    const float whole = gates.lead[C - 1];
+        for (int i = 0; i < 4; ++i) W[t][i] *= late[i];
+      }
+      const Split<E> Wl[2] = {split<E>(W[0], W[1]), split<E>(W[2], W[3])};
+      const float whole = gates.lead[C - 1];
 #pragma unroll
-    for (int cb = 0; cb < CB; ++cb) {
+      for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) S[cb][i] *= whole;
+        for (int i = 0; i < 4; ++i) S[cb][i] *= whole;
 #pragma unroll
-      for (int p = 0; p < 2; ++p) S[cb] = mma<E>(col_frag<E, true>(Ks, LD, 32 * p, row4_of(cb, 0)), Wl[p], S[cb]);
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) S[cb] = mma<E>(K::template col<true>(Ks, 32 * p, row4_of(cb, 0), n16, g4), Wl[p], S[cb]);
     }
     if (MODE == TRAIN && cols && (n % kDeltaMarks == kDeltaMarks - 1 || n == alive - 1))
       store_regs<CB>(S, a.mark + (((long)bh * a.marks + n / kDeltaMarks) * (a.DVP / 16) + j / 16) * DK * 16);
@@ -344,13 +376,25 @@ __global__ __launch_bounds__(64 * NW) void delta_fwd_kernel(DeltaArgs a) {
     if (!transition) {
       store_regs<CB>(S, a.seg + (((long)bh * a.P + seg) * (a.DVP / 16) + j / 16) * DK * 16);
     } else {
-      E* to = (E*)a.trans + ((long)bh * a.P + seg) * DK * DK + (long)(j + n16) * DK + 8 * g4;
-      const long mplane = (long)a.B * a.H * a.P * DK * DK;
+      const long block = ((long)bh * a.P + seg) * DK * DK, mplane = (long)a.B * a.H * a.P * DK * DK;
+      E* to = (E*)a.trans + block + (long)(j + n16) * DK + 8 * g4;
 #pragma unroll
       for (int p = 0; p < CP; ++p) {
         const Split<E> s = split<E>(S[2 * p], S[2 * p + 1]);
 #pragma unroll
         for (int part = 0; part < PARTS; ++part) *reinterpret_cast<Frag<E>*>(to + part * mplane + 32 * p) = s.part[part];
+      }
+      E* by_rows = (E*)a.trans_rows + block + j + 4 * (n16 >> 2);
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb) {
+        f32x4 x = quad_transpose(S[cb]);
+        E* p = by_rows + (row4_of(cb, g4) + (n16 & 3)) * DK;
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part) {
+          store4(p + part * mplane, x);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] -= (float)(E)x[i];
+        }
       }
     }
     return;
@@ -375,7 +419,7 @@ static void delta_fwd_run(const DeltaArgs& a, hipStream_t s) {
   else delta_prep_kernel<E, DK, false><<<heads * a.N, 256, 0, s>>>(a);
   if (a.P > 1) {
     delta_fwd_kernel<E, DK, NW, STATE><<<heads * (train ? a.P : a.P - 1) * (tiles + (DK + CW - 1) / CW), 64 * NW, 0, s>>>(a);
-    delta_scan_kernel<E, DK, NW, false><<<heads * tiles, 64 * NW, 0, s>>>(a);
+    delta_scan_kernel<E, DK, false><<<heads * ((a.dv + 31) / 32), 4 * DK, 0, s>>>(a);
   }
   if (train) delta_fwd_kernel<E, DK, NW, TRAIN><<<heads * a.P * tiles, 64 * NW, 0, s>>>(a);
   else delta_fwd_kernel<E, DK, NW, INFER><<<heads * a.P * tiles, 64 * NW, 0, s>>>(a);
@@ -392,7 +436,32 @@ static void delta_fwd_rows(const DeltaArgs& a, hipStream_t s) {
   else delta_fwd_cols<E, 128>(a, s);
 }
 
-hipError_t launch_delta_fwd(const DeltaArgs& a, hipStream_t s) {
+template <typename E>
+static void pack_one(const void*& p, Strides& st, void* to, const DeltaArgs& a, int heads, int d, int r, hipStream_t s) {
+  const long units = (long)a.B * heads * a.T * (r / 8);
+  const long blocks = (units + 255) / 256;
+  delta_pack_kernel<E><<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, s>>>((const E*)p, st, (E*)to, heads, a.T, d, r, units);
+  p = to;
+  st = {(long long)heads * a.T * r, (long long)a.T * r, r};
+}
+template <typename E>
+static void pack_all(DeltaArgs& a, bool backward, hipStream_t s) {
+  if (a.qk_packed) {
+    pack_one<E>(a.q, a.qs, a.qk_packed, a, a.Hk, a.dk, a.dkr, s);
+    pack_one<E>(a.k, a.ks, (E*)a.qk_packed + (long)a.B * a.Hk * a.T * a.dkr, a, a.Hk, a.dk, a.dkr, s);
+  }
+  if (a.v_packed) {
+    pack_one<E>(a.v, a.vs, a.v_packed, a, a.H, a.dv, a.dvr, s);
+    if (backward) pack_one<E>(a.dO, a.dos, (E*)a.v_packed + (long)a.B * a.H * a.T * a.dvr, a, a.H, a.dv, a.dvr, s);
+  }
+}
+void delta_pack(DeltaArgs& a, bool backward, hipStream_t s) {
+  if (a.dtype == GLA_BF16) pack_all<bf16>(a, backward, s);
+  else pack_all<float>(a, backward, s);
+}
+
+hipError_t launch_delta_fwd(DeltaArgs a, hipStream_t s) {
+  delta_pack(a, false, s);
   if (a.dtype == GLA_BF16) delta_fwd_rows<bf16>(a, s);
   else delta_fwd_rows<float>(a, s);
   return hipGetLastError();
