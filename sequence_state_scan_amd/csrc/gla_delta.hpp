@@ -184,6 +184,26 @@ __device__ __forceinline__ f32x4 mma(const Split<E, N>& a, const Split<E, M>& b,
   return c;
 }
 
+// acc[t] += a[t] b (or b a[t]) for the tiles t0 .. t1 - 1, part by part, so that consecutive instructions do not wait
+// for each other; pairs of parts as in mma above.
+template <typename E, int T0, int T1, int N, int M, int TILES, bool SWAP = false>
+__device__ __forceinline__ void mma_tiles(f32x4 (&acc)[TILES], const Split<E, N> (&a)[TILES], const Split<E, M>& b) {
+  constexpr int MOST = N == 1 || M == 1 ? N + M - 2 : (N > M ? N : M) - 1;
+#pragma unroll
+  for (int sum = MOST; sum >= 0; --sum)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int t = T0; t < T1; ++t)
+        if (sum - i >= 0 && sum - i < M) acc[t] = SWAP ? mma(b.part[sum - i], a[t].part[i], acc[t]) : mma(a[t].part[i], b.part[sum - i], acc[t]);
+}
+// Keeps the compiler from moving anything over: LDS reads are issued a batch ahead of the products that take them.
+// Left to itself it reads, waits and multiplies one by one.
+template <typename E>
+__device__ __forceinline__ void batch() {
+  if constexpr (sizeof(E) == 2) __builtin_amdgcn_sched_barrier(0);  // (a float32 product takes 16 times as long, and its operands twice the registers)
+}
+
 // Row m of tile t where tiles 2p and 2p + 1 interleave the rows 32p .. 32p + 31: an accumulator's lane (4 rows of
 // group g4 in each) then holds 8 consecutive rows, 32p + 8 g4 + (0 .. 7), and can be the next product's operand as
 // it stands.
@@ -295,22 +315,22 @@ __device__ __forceinline__ void store4_part(E* p, f32x4 x, int left) {
 // A tile of ROWS rows of D elements on its way from memory to LDS: rows past `rows` and columns past `cols` (at least 1
 // of the one, 8 of the other and a multiple of 8) are zero there.  Every lane loads, from a place inside the tile where
 // its own is outside: with loads under a condition the compiler waits for all those in flight before the next (4 heads
-// of 128 x 256 over 64k tokens: the walk 235 us).  Addresses are formed again at every use (fresh_tid): held over a
-// walk's loop they cost the registers that its products need.
+// of 128 x 256 over 64k tokens: the walk 235 us).
 template <typename E, int ROWS, int D, int NT>
 struct TileIn {
   static constexpr int UPR = D / 8, UNITS = ROWS * UPR, PER = (UNITS + NT - 1) / NT;
   static_assert(NT % UPR == 0, "whole rows a pass");
   typename Raw<E, 8>::type r[PER];
   __device__ __forceinline__ void load(const E* src, long stride, int rows, int cols) {
-    const int t = fresh_tid();
+    const int t = threadIdx.x;
     if (rows >= ROWS && cols >= D && stride < (1 << 20)) {  // the whole tile, from a base and one 32-bit offset
       const int u = UNITS % NT == 0 ? t : t < UNITS ? t : 0;
       const unsigned at = ((unsigned)(u / UPR) * (unsigned)stride + u % UPR * 8) * sizeof(E);
 #pragma unroll
       for (int i = 0; i < PER; ++i)
         r[i] = *reinterpret_cast<const typename Raw<E, 8>::type*>(reinterpret_cast<const char*>(src + i * (NT / UPR) * stride) + at);
-    } else {
+    } else {  // (rare: no addresses held for it)
+      const int t = fresh_tid();
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int u = t + i * NT, c = u % UPR * 8;
@@ -320,13 +340,20 @@ struct TileIn {
   }
   __device__ __forceinline__ void store(E* lds, int rows, int cols) const {
     typedef E v8 __attribute__((ext_vector_type(8), aligned(16)));
-    const int t = fresh_tid();
-    const bool whole = rows >= ROWS && cols >= D;
+    const int t = threadIdx.x;
+    if (rows >= ROWS && cols >= D) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int u = t + i * NT, row = u / UPR, c = u % UPR * 8;
-      if (UNITS % NT == 0 || u < UNITS)
-        *reinterpret_cast<v8*>(lds + Tile<E, D>::at(row, c)) = whole || (row < rows && c < cols) ? (v8)r[i] : (v8){};
+      for (int i = 0; i < PER; ++i) {
+        const int u = t + i * NT;
+        if (UNITS % NT == 0 || u < UNITS) *reinterpret_cast<v8*>(lds + Tile<E, D>::at(u / UPR, u % UPR * 8)) = r[i];
+      }
+    } else {
+      const int t = fresh_tid();
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int u = t + i * NT, row = u / UPR, c = u % UPR * 8;
+        if (UNITS % NT == 0 || u < UNITS) *reinterpret_cast<v8*>(lds + Tile<E, D>::at(row, c)) = row < rows && c < cols ? (v8)r[i] : (v8){};
+      }
     }
   }
 };
@@ -337,10 +364,88 @@ struct GateBlock {
   float lead[C], late[C], high[C], low[C], beta[C];
 };
 static_assert(sizeof(GateBlock) == kDeltaGates * sizeof(float), "a gate block's floats");
-// The decay from token j to token i (gamma_i - gamma_j, not positive).
-__device__ __forceinline__ float decay_between(const GateBlock& s, int i, int j) {
-  return decay((s.high[i] - s.high[j]) + (s.low[i] - s.low[j]));
+
+// The decays from 4 tokens from `from` on to token `to`, zero where that comes before them (with ON, not where it is one
+// of them).
+template <bool ON>
+__device__ __forceinline__ f32x4 decays_from(const GateBlock& s, int to, int from) {
+  const f32x4 high = *reinterpret_cast<const f32x4*>(s.high + from), low = *reinterpret_cast<const f32x4*>(s.low + from);
+  const float h = s.high[to], l = s.low[to];
+  f32x4 e;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float x = decay((h - high[i]) + (l - low[i]));
+    e[i] = (ON ? from + i <= to : from + i < to) ? x : 0.f;
+  }
+  return e;
 }
+// The decays from token `from` to 4 tokens from `to` on, likewise.
+template <bool ON>
+__device__ __forceinline__ f32x4 decays_to(const GateBlock& s, int to, int from) {
+  const f32x4 high = *reinterpret_cast<const f32x4*>(s.high + to), low = *reinterpret_cast<const f32x4*>(s.low + to);
+  const float h = s.high[from], l = s.low[from];
+  f32x4 e;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float x = decay((high[i] - h) + (low[i] - l));
+    e[i] = (ON ? from <= to + i : from < to + i) ? x : 0.f;
+  }
+  return e;
+}
+
+// P by 16 x 16 tiles, spread over a workgroup's waves and held until its place in LDS is free: P itself (rows are
+// queries) or transposed.  Ten tiles, and the two above the diagonal that a 32-wide product reads as zeros.
+template <typename E, int DK, int NW, bool TRANSPOSED>
+struct ScoreTiles {
+  static constexpr int N = 12 / NW + (12 % NW != 0);
+  f32x4 x[N];
+  static constexpr int kTiles = 12;
+  __device__ __forceinline__ static void place(int u, int& it, int& jt) {  // query and key tile
+    it = u < 1 ? 0 : u < 3 ? 1 : u < 6 ? 2 : u < 10 ? 3 : u == 10 ? 0 : 2;
+    jt = u < 10 ? u - it * (it + 1) / 2 : it + 1;
+  }
+  __device__ __forceinline__ void form(const E* Qs, const E* Ks, const GateBlock& gates, int wave, int n16, int g4) {
+    typedef Tile<E, DK> K;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      x[i] = zero4();
+      const int u = wave + i * NW;
+      if (u >= 10) continue;
+      int it, jt;
+      place(u, it, jt);
+      Frag<E> q[DK / 32], k[DK / 32];
+#pragma unroll
+      for (int p = 0; p < DK / 32; ++p) {
+        q[p] = K::row(Qs, 16 * it + n16, 32 * p + 8 * g4);
+        k[p] = K::row(Ks, 16 * jt + n16, 32 * p + 8 * g4);
+      }
+      const f32x4 e = TRANSPOSED ? decays_to<true>(gates, 16 * it + 4 * g4, 16 * jt + n16) : decays_from<true>(gates, 16 * it + n16, 16 * jt + 4 * g4);
+      batch<E>();
+#pragma unroll
+      for (int p = 0; p < DK / 32; ++p) x[i] = TRANSPOSED ? mma(q[p], k[p], x[i]) : mma(k[p], q[p], x[i]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x[i][r] *= e[r];
+    }
+  }
+  template <int PARTS, int LEN>
+  __device__ __forceinline__ void put(E (&Ps)[PARTS][LEN], int parts, int wave, int n16, int g4) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int u = wave + i * NW;
+      if (u >= kTiles) continue;
+      int it, jt;
+      place(u, it, jt);
+#pragma unroll
+      for (int part = 0; part < PARTS; ++part) {
+        if (part >= parts) continue;
+        if (TRANSPOSED) Tile<E, C>::put4(Ps[part], 16 * jt + n16, 16 * it + 4 * g4, x[i]);
+        else Tile<E, C>::put4(Ps[part], 16 * it + n16, 16 * jt + 4 * g4, x[i]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[i][r] -= (float)(E)x[i][r];
+      }
+    }
+  }
+};
 
 __device__ __forceinline__ int length_of(const DeltaArgs& a, int b) {
   const int n = a.lens ? a.lens[b] : a.T;

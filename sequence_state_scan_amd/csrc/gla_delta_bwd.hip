@@ -23,7 +23,8 @@ __global__ __launch_bounds__(64 * NW) void delta_bwd_kernel(DeltaArgs a) {
   typedef Tile<E, DK> K;
   typedef Tile<E, CW> V;
   typedef Tile<E, C> M;
-  __shared__ __attribute__((aligned(16))) E Ks[C * K::LD], Qs[C * K::LD], Os[C * V::LD], Ts[PARTS][C * M::LD], Ps[PARTS][C * M::LD];
+  __shared__ __attribute__((aligned(16))) E Ks[C * K::LD], Qs[C * K::LD], Os[C * V::LD];
+  __shared__ __attribute__((aligned(16))) E Ts[PARTS][C * M::LD];  // P^T, then the transposed inverse in its place
   __shared__ __attribute__((aligned(16))) GateBlock gates;
   const int segments = STATE ? a.P - 1 : a.P, units = a.B * a.H * segments;  // the first one's own gradient: no use
   const int unit = blockIdx.x % units, tile = blockIdx.x / units;
@@ -31,7 +32,7 @@ __global__ __launch_bounds__(64 * NW) void delta_bwd_kernel(DeltaArgs a) {
   const int len = length_of(a, b), alive = (len + C - 1) / C;
   const int first = seg * a.L, end = min(first + a.L, alive);
   if (seg > 0 && first >= alive) return;
-  const int lane = lane_id(), wave = wave_id(), n16 = lane & 15, g4 = lane >> 4;
+  const int lane = lane_id(), wave = wave_id(), n16 = lane & 15, g4 = lane >> 4, k8 = 8 * g4;
   const int col0 = tile * CW, j = col0 + 16 * wave;
   const bool cols = j < a.dv;
   const long tiles = a.DVP / 16;
@@ -57,26 +58,28 @@ __global__ __launch_bounds__(64 * NW) void delta_bwd_kernel(DeltaArgs a) {
   TileIn<E, C, CW, NT> oin;
   TileIn<E, C, C, NT> tin[PARTS];
   f32x4 gin = zero4();
-  const auto load = [&](int n) {
+  const auto load_rows = [&](int n) {
     const long t0 = (long)n * C;
     const int left = len - n * C;
     kin.load(kp + t0 * a.ks.t, a.ks.t, left, a.dkr);
     qin.load(qp + t0 * a.qs.t, a.qs.t, left, a.dkr);
     oin.load(op + t0 * a.dos.t, a.dos.t, left, a.dvr - col0);
+    gin = reinterpret_cast<const f32x4*>(gp + (long)n * kDeltaGates)[threadIdx.x % (kDeltaGates / 4)];
+  };
+  const auto load_inverse = [&](int n) {
 #pragma unroll
     for (int part = 0; part < PARTS; ++part) tin[part].load(tp + part * plane + (long)n * C * C, C, C, C);
-    gin = reinterpret_cast<const f32x4*>(gp + (long)n * kDeltaGates)[fresh_tid() % (kDeltaGates / 4)];
   };
-  if (first < end) load(end - 1);
-  for (int u = threadIdx.x; u < PARTS * C * M::LD / 8; u += NT) reinterpret_cast<Frag<E>*>(&Ps[0][0])[u] = Frag<E>{};
+  if (first < end) {
+    load_rows(end - 1);
+    load_inverse(end - 1);
+  }
   for (int n = end - 1; n >= first; --n) {
     __syncthreads();
     const int left = len - n * C;
     kin.store(Ks, left, a.dkr);
     qin.store(Qs, left, a.dkr);
     oin.store(Os, left, a.dvr - col0);
-#pragma unroll
-    for (int part = 0; part < PARTS; ++part) tin[part].store(Ts[part], C, C);
     if (threadIdx.x < kDeltaGates / 4) reinterpret_cast<f32x4*>(&gates)[threadIdx.x] = gin;
     __syncthreads();
     if (!STATE && cols && (n % kDeltaMarks == kDeltaMarks - 1 || n == alive - 1)) {  // <state, D> here, for dg
@@ -92,108 +95,124 @@ __global__ __launch_bounds__(64 * NW) void delta_bwd_kernel(DeltaArgs a) {
       for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o);
       if (lane_id() == 0) a.carry[at] = dot;
     }
-    if (n > first) load(n - 1);
-    const int lane = fresh_tid() & 63, n16 = lane & 15, g4 = lane >> 4, k8 = 8 * g4;
-    // P^T's ten tiles: a lane has four queries of one key
-    for (int u = wave; u < 10; u += NW) {
-      const int it = u < 1 ? 0 : u < 3 ? 1 : u < 6 ? 2 : 3, jt = u - it * (it + 1) / 2;
-      f32x4 acc = zero4();
-#pragma unroll
-      for (int p = 0; p < CP; ++p) acc = mma(K::row(Qs, 16 * it + n16, 32 * p + k8), K::row(Ks, 16 * jt + n16, 32 * p + k8), acc);
-      const int key = 16 * jt + n16, i0 = 16 * it + 4 * g4;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) acc[r] = key <= i0 + r ? acc[r] * decay_between(gates, i0 + r, key) : 0.f;
-      M::put4(Ps[0], key, i0, acc);
-      if constexpr (PARTS == 2) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[r] -= (float)(E)acc[r];
-        M::put4(Ps[1], key, i0, acc);
-      }
-    }
+    const int lane = fresh_tid() & 63, n16 = lane & 15, g4 = lane >> 4, k8 = 8 * g4;  // (anew: see the forward)
+    ScoreTiles<E, DK, NW, true> P;
+    P.form(Qs, Ks, gates, wave, n16, g4);
+    P.put(Ts, PARTS, wave, n16, g4);
     f32x4 dW[4], Y[4];
     {
-      Split<E> Do[CP];
+      Split<E, 1> kf[2][4];
+      const auto fetch = [&](int p) {
 #pragma unroll
-      for (int p = 0; p < CP; ++p) Do[p] = split<E>(D[2 * p], D[2 * p + 1]);
-      if (!STATE && cols) {
-        E* to = (E*)a.grad1 + (((long)bh * a.N + n) * a.DVP + j + n16) * DK + k8;
-#pragma unroll
-        for (int p = 0; p < CP; ++p) *reinterpret_cast<Frag<E>*>(to + 32 * p) = Do[p].part[0];
-      }
+        for (int t = 0; t < 4; ++t) kf[p & 1][t].part[0] = K::row(Ks, row_of(t, n16), 32 * p + k8);
+      };
+      fetch(0);
 #pragma unroll
       for (int t = 0; t < 4; ++t) dW[t] = zero4();
 #pragma unroll
-      for (int p = 0; p < CP; ++p)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) dW[t] = mma<E>(K::row(Ks, row_of(t, n16), 32 * p + k8), Do[p], dW[t]);
+      for (int p = 0; p < CP; ++p) {
+        const Split<E> Do = split<E>(D[2 * p], D[2 * p + 1]);
+        if (!STATE && cols)
+          *reinterpret_cast<Frag<E>*>((E*)a.grad1 + (((long)bh * a.N + n) * a.DVP + j + n16) * DK + k8 + 32 * p) = Do.part[0];
+        if (p + 1 < CP) fetch(p + 1);
+        batch<E>();
+        mma_tiles<E, 0, 4>(dW, kf[p & 1], Do);
+        batch<E>();
+      }
     }
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const f32x4 late = *reinterpret_cast<const f32x4*>(gates.late + row4_of(t, g4));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) dW[t][i] *= late[i];
-    }
-    __syncthreads();  // P^T
+    f32x4 late[4], beta[4], lead[4];
     Frag<E> dO[2];
 #pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      late[t] = *reinterpret_cast<const f32x4*>(gates.late + row4_of(t, g4));
+      beta[t] = *reinterpret_cast<const f32x4*>(gates.beta + row4_of(t, g4));
+      lead[t] = *reinterpret_cast<const f32x4*>(gates.lead + row4_of(t, g4));
+    }
+#pragma unroll
     for (int p = 0; p < 2; ++p) dO[p] = V::template col<false>(Os, 32 * p, 16 * wave, n16, g4);
+    const float whole = gates.lead[C - 1];
+    if (n > first) load_rows(n - 1);
+    batch<E>();
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+    for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int t = 0; t < 2 * p + 2; ++t) {
-        Split<E> Pf;
+      for (int i = 0; i < 4; ++i) dW[t][i] *= late[t][i];
+    __syncthreads();  // P^T
+    Split<E> F[2][4];
+    const auto fetch = [&](int p) {
 #pragma unroll
-        for (int part = 0; part < PARTS; ++part) Pf.part[part] = M::row(Ps[part], row_of(t, n16), 32 * p + k8);
-        dW[t] = mma<E>(Pf, dO[p], dW[t]);
-      }
+      for (int t = 0; t < 2 * p + 2; ++t)
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part) F[p][t].part[part] = M::row(Ts[part], row_of(t, n16), 32 * p + k8);
+    };
+    fetch(0);
+    fetch(1);
+    batch<E>();
+    mma_tiles<E, 0, 2>(dW, F[0], Split<E, 1>{{dO[0]}});
+    mma_tiles<E, 0, 4>(dW, F[1], Split<E, 1>{{dO[1]}});
+    __syncthreads();
+#pragma unroll
+    for (int part = 0; part < PARTS; ++part) tin[part].store(Ts[part], C, C);
+    __syncthreads();
+    if (n > first) load_inverse(n - 1);
+    fetch(0);
+    fetch(1);
     const Split<E, FINE> Wo[2] = {split<E, FINE>(dW[0], dW[1]), split<E, FINE>(dW[2], dW[3])};
 #pragma unroll
     for (int t = 0; t < 4; ++t) Y[t] = zero4();
-#pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-      for (int t = 0; t < 2 * p + 2; ++t) {
-        Split<E> T;
-#pragma unroll
-        for (int part = 0; part < PARTS; ++part) T.part[part] = M::row(Ts[part], row_of(t, n16), 32 * p + k8);
-        Y[t] = mma<E>(T, Wo[p], Y[t]);
-      }
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {  // z, then -e^gamma dV
-      const int r0 = row4_of(t, g4);
-      if (!STATE && cols) store_rows(Y[t], a.z + (((long)bh * a.N + n) * C + r0) * a.DVP + j, a.DVP, n16);
-      const f32x4 beta = *reinterpret_cast<const f32x4*>(gates.beta + r0), lead = *reinterpret_cast<const f32x4*>(gates.lead + r0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) Y[t][i] *= -lead[i] * beta[i];
-    }
-    const Split<E> Yo[2] = {split<E>(Y[0], Y[1]), split<E>(Y[2], Y[3])};
-    Split<E> Oo[2];  // e^gamma dO
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const f32x4 l0 = *reinterpret_cast<const f32x4*>(gates.lead + 32 * p + k8);
-      const f32x4 l1 = *reinterpret_cast<const f32x4*>(gates.lead + 32 * p + k8 + 4);
-      f32x4 x, y;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = l0[i] * (float)dO[p][i];
-        y[i] = l1[i] * (float)dO[p][4 + i];
-      }
-      Oo[p] = split<E>(x, y);
-    }
-    const float whole = gates.lead[C - 1];
-#pragma unroll
-    for (int cb = 0; cb < CB; ++cb)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) D[cb][i] *= whole;
+    batch<E>();
+    mma_tiles<E, 0, 2>(Y, F[0], Wo[0]);
+    mma_tiles<E, 0, 4>(Y, F[1], Wo[1]);
+    batch<E>();
     {
       const int lane = fresh_tid() & 63, n16 = lane & 15, g4 = lane >> 4;
+      constexpr int TILES = 2;  // of Q and of K, a batch
+      Frag<E> qf[2][TILES], kf[2][TILES];
+      const auto fetch = [&](int s) {
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb) {
-          D[cb] = mma<E>(K::template col<true>(Qs, 32 * p, row4_of(cb, 0), n16, g4), Oo[p], D[cb]);
-          D[cb] = mma<E>(K::template col<true>(Ks, 32 * p, row4_of(cb, 0), n16, g4), Yo[p], D[cb]);
+        for (int i = 0; i < TILES; ++i) {
+          const int kk = 32 * (s * TILES / CB), ch = row4_of(s * TILES % CB + i, 0);
+          qf[s & 1][i] = K::template col<true>(Qs, kk, ch, n16, g4);
+          kf[s & 1][i] = K::template col<true>(Ks, kk, ch, n16, g4);
         }
+      };
+      fetch(0);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {  // z, then -e^gamma dV
+        if (!STATE && cols) store_rows(Y[t], a.z + (((long)bh * a.N + n) * C + row4_of(t, g4)) * a.DVP + j, a.DVP, n16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) Y[t][i] *= -lead[t][i] * beta[t][i];
+      }
+      const Split<E> Yo[2] = {split<E>(Y[0], Y[1]), split<E>(Y[2], Y[3])};
+      Split<E> Oo[2];  // e^gamma dO: its 8 tokens are those of tiles 2p and 2p + 1
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        f32x4 x, y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = lead[2 * p][i] * (float)dO[p][i];
+          y[i] = lead[2 * p + 1][i] * (float)dO[p][4 + i];
+        }
+        Oo[p] = split<E>(x, y);
+      }
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) D[cb][i] *= whole;
+#pragma unroll
+      for (int s = 0; s < 2 * CB / TILES; ++s) {
+        if (s + 1 < 2 * CB / TILES) fetch(s + 1);
+        batch<E>();
+        const int p = s * TILES / CB;
+#pragma unroll
+        for (int part = PARTS - 1; part >= 0; --part) {
+#pragma unroll
+          for (int i = 0; i < TILES; ++i) D[s * TILES % CB + i] = mma(qf[s & 1][i], Oo[p].part[part], D[s * TILES % CB + i]);
+#pragma unroll
+          for (int i = 0; i < TILES; ++i) D[s * TILES % CB + i] = mma(kf[s & 1][i], Yo[p].part[part], D[s * TILES % CB + i]);
+        }
+        batch<E>();
+      }
     }
   }
   if (!cols) return;
@@ -354,12 +373,9 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a) {
   for (int t = 0; t < 4; ++t) {
     if (t > (wave | 1)) continue;
     const int key = 16 * t + n16, i0 = 16 * wave + 4 * g4;
-    f32x4 x;
+    f32x4 x = half ? decays_to<false>(gates, i0, key) : decays_to<true>(gates, i0, key);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool below = half ? key < i0 + i : key <= i0 + i;
-      x[i] = below ? (half ? -H[t][i] : H[t][i]) * decay_between(gates, i0 + i, key) : 0.f;
-    }
+    for (int i = 0; i < 4; ++i) x[i] *= half ? -H[t][i] : H[t][i];
     M::put4(half ? GT : HT, key, i0, x);
   }
   const int row = 16 * wave + n16;

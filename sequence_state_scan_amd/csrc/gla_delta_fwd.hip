@@ -74,12 +74,10 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
 #pragma unroll
     for (int p = 0; p < DK / 32; ++p)
       acc = mma(K::row(Ks, 16 * wave + n16, 32 * p + 8 * g4), K::row(Ks, 16 * jt + n16, 32 * p + 8 * g4), acc);
-    const int j = 16 * jt + n16;
+    const int j = 16 * jt + n16, i = 16 * wave + 4 * g4;
+    const f32x4 e = decays_to<false>(gates, i, j);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int i = 16 * wave + 4 * g4 + r;
-      Bm[i * LF + j] = i > j ? acc[r] * decay_between(gates, i, j) : 0.f;
-    }
+    for (int r = 0; r < 4; ++r) Bm[(i + r) * LF + j] = acc[r] * e[r];
   }
   __syncthreads();
   if (threadIdx.x < kDeltaGates / 4)
@@ -165,17 +163,18 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
 
 enum { INFER = 0, TRAIN = 1, STATE = 2 };
 
-// Workgroup: one segment and 16 NW columns.  STATE: the segment's own end state where another follows, and past the
-// value columns its transition where another follows or, for the backward's chain, precedes.
+// Workgroup: one segment and 16 NW columns.  STATE: the segment's own end state where another follows,
+// and past the value columns its transition where another follows or, for the backward's chain, precedes.
+// (The state pass alone leaves the order of its LDS reads to the compiler: in half the registers two workgroups fit a CU.)
 template <typename E, int DK, int NW, int MODE>
-__global__ __launch_bounds__(64 * NW) void delta_fwd_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(64 * NW, MODE == STATE && sizeof(E) == 2 && NW == 8 ? 4 : 1) void delta_fwd_kernel(DeltaArgs a) {
   constexpr int NT = 64 * NW, CB = DK / 16, CP = DK / 32, CW = 16 * NW, PARTS = Num<E>::PARTS;
   constexpr int FINE = MODE == TRAIN && PARTS == 2 ? 3 : PARTS, PP = MODE == TRAIN ? PARTS : 1;  // parts of W, of P
   typedef Tile<E, DK> K;
   typedef Tile<E, CW> V;
   typedef Tile<E, C> M;
-  __shared__ __attribute__((aligned(16))) E Ks[C * K::LD], Vs[C * V::LD], Ts[PARTS][C * M::LD];
-  __shared__ __attribute__((aligned(16))) E Qs[MODE == STATE ? 8 : C * K::LD], Ps[PP][MODE == STATE ? 8 : C * M::LD];
+  __shared__ __attribute__((aligned(16))) E Ks[C * K::LD], Vs[C * V::LD], Qs[MODE == STATE ? 8 : C * K::LD];
+  __shared__ __attribute__((aligned(16))) E Ts[PARTS][C * M::LD];  // the inverse, then P in its place
   __shared__ __attribute__((aligned(16))) GateBlock gates;
   const bool chained = MODE == STATE && a.err;  // a backward follows
   const int segments = MODE == STATE && !chained ? a.P - 1 : a.P, units = a.B * a.H * segments;
@@ -183,12 +182,13 @@ __global__ __launch_bounds__(64 * NW) void delta_fwd_kernel(DeltaArgs a) {
   const int bh = unit / segments, seg = unit - bh * segments, b = bh / a.H, h = bh - b * a.H, hk = h / (a.H / a.Hk);
   const int len = length_of(a, b), alive = (len + C - 1) / C;
   const int first = seg * a.L, last = min(first + a.L, a.N), end = min(last, alive);
-  const int lane = lane_id(), wave = wave_id(), n16 = lane & 15, g4 = lane >> 4;
+  const int lane = lane_id(), wave = wave_id(), n16 = lane & 15, g4 = lane >> 4, k8 = 8 * g4;
   const int value_tiles = (a.dv + CW - 1) / CW;
   const bool transition = MODE == STATE && tile >= value_tiles;
   if (MODE == STATE && last >= alive && !(transition && chained && seg > 0 && first < alive)) return;
   const int col0 = (transition ? tile - value_tiles : tile) * CW, j = col0 + 16 * wave;  // the wave's columns
   const bool cols = j < (transition ? a.DKP : a.dv);
+  const long tiles = a.DVP / 16;
 
   f32x4 S[CB];
   if (MODE == STATE) {
@@ -199,11 +199,10 @@ __global__ __launch_bounds__(64 * NW) void delta_fwd_kernel(DeltaArgs a) {
   } else if (a.P > 1) {
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb) S[cb] = zero4();
-    if (cols && (seg == 0 || first < alive)) load_regs<CB>(S, a.seg_in + (((long)bh * a.P + seg) * (a.DVP / 16) + j / 16) * DK * 16);
+    if (cols && (seg == 0 || first < alive)) load_regs<CB>(S, a.seg_in + (((long)bh * a.P + seg) * tiles + j / 16) * DK * 16);
   } else {
-    load_state<CB>(S, a.h0 ? a.h0 + (long)bh * a.dk * a.dv : nullptr, a.dk, a.dv, cols ? j + n16 : a.dv);
+    load_state<CB>(S, a.h0 ? a.h0 + (long)bh * a.dk * a.dv : nullptr, a.dk, a.dv, j + n16);
   }
-
   arrived<CB>(S);
 
   const E* kp = (const E*)a.k + b * a.ks.b + hk * a.ks.h;
@@ -224,11 +223,9 @@ __global__ __launch_bounds__(64 * NW) void delta_fwd_kernel(DeltaArgs a) {
     if (!transition) vin.load(vp + t0 * a.vs.t, a.vs.t, left, a.dvr - col0);
 #pragma unroll
     for (int part = 0; part < PARTS; ++part) tin[part].load(tp + part * plane + (long)n * C * C, C, C, C);
-    gin = reinterpret_cast<const f32x4*>(gp + (long)n * kDeltaGates)[fresh_tid() % (kDeltaGates / 4)];
+    gin = reinterpret_cast<const f32x4*>(gp + (long)n * kDeltaGates)[threadIdx.x % (kDeltaGates / 4)];
   };
   if (first < end) load(first);
-  if constexpr (MODE != STATE)  // the blocks of P above the diagonal that the products read
-    for (int u = threadIdx.x; u < PP * C * M::LD / 8; u += NT) reinterpret_cast<Frag<E>*>(&Ps[0][0])[u] = Frag<E>{};
   for (int n = first; n < end; ++n) {
     __syncthreads();
     const int left = len - n * C;
@@ -240,105 +237,150 @@ __global__ __launch_bounds__(64 * NW) void delta_fwd_kernel(DeltaArgs a) {
     if (threadIdx.x < kDeltaGates / 4) reinterpret_cast<f32x4*>(&gates)[threadIdx.x] = gin;
     __syncthreads();
     if (n + 1 < end) load(n + 1);
+    // (the lane's number anew in every phase: the LDS addresses formed from it would not fit the registers all at once)
     const int lane = fresh_tid() & 63, n16 = lane & 15, g4 = lane >> 4, k8 = 8 * g4;
-    if constexpr (MODE != STATE) {  // P's ten tiles, transposed products: a lane has four keys of one query
-      for (int u = wave; u < 10; u += NW) {
-        const int it = u < 1 ? 0 : u < 3 ? 1 : u < 6 ? 2 : 3, jt = u - it * (it + 1) / 2;
-        f32x4 acc = zero4();
+    ScoreTiles<E, DK, NW, false> P;
+    if constexpr (MODE != STATE) P.form(Qs, Ks, gates, wave, n16, g4);
+    // K S0 and Q S0 (transposed: a lane has four columns of one token).  A forward-only call rounds the state, W and P to
+    // one bf16 for o, which is rounded to it after all.
+    f32x4 Y[4], W[4], O[4];
+    {
+      Split<E, 1> kf[2][4], qf[2][4];
+      const auto fetch = [&](int p) {
 #pragma unroll
-        for (int p = 0; p < CP; ++p) acc = mma(K::row(Ks, 16 * jt + n16, 32 * p + k8), K::row(Qs, 16 * it + n16, 32 * p + k8), acc);
-        const int i = 16 * it + n16, k0 = 16 * jt + 4 * g4;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[r] = k0 + r <= i ? acc[r] * decay_between(gates, i, k0 + r) : 0.f;
-        M::put4(Ps[0], i, k0, acc);
-        if constexpr (PP == 2) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[r] -= (float)(E)acc[r];
-          M::put4(Ps[1], i, k0, acc);
+        for (int t = 0; t < 4; ++t) {
+          kf[p & 1][t].part[0] = K::row(Ks, row_of(t, n16), 32 * p + k8);
+          if constexpr (MODE != STATE) qf[p & 1][t].part[0] = K::row(Qs, 16 * t + n16, 32 * p + k8);
         }
+      };
+      fetch(0);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) Y[t] = O[t] = zero4();
+#pragma unroll
+      for (int p = 0; p < CP; ++p) {
+        const Split<E> So = split<E>(S[2 * p], S[2 * p + 1]);
+        if (MODE == TRAIN && cols)
+          *reinterpret_cast<Frag<E>*>((E*)a.state0 + (((long)bh * a.N + n) * a.DVP + j + n16) * DK + k8 + 32 * p) = So.part[0];
+        if (p + 1 < CP) fetch(p + 1);
+        if constexpr (MODE != STATE) batch<E>();
+        mma_tiles<E, 0, 4>(Y, kf[p & 1], So);
+        if constexpr (MODE == TRAIN) mma_tiles<E, 0, 4, 1, PARTS, 4, true>(O, qf[p & 1], So);
+        if constexpr (MODE == INFER) mma_tiles<E, 0, 4, 1, 1, 4, true>(O, qf[p & 1], Split<E, 1>{{So.part[0]}});
+        if constexpr (MODE != STATE) batch<E>();
       }
-    }
-    // V - e^gamma K S0
-    Split<E> So[CP];
-#pragma unroll
-    for (int p = 0; p < CP; ++p) So[p] = split<E>(S[2 * p], S[2 * p + 1]);
-    f32x4 Y[4], W[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) Y[t] = zero4();
-#pragma unroll
-    for (int p = 0; p < CP; ++p)
-#pragma unroll
-      for (int t = 0; t < 4; ++t) Y[t] = mma<E>(K::row(Ks, row_of(t, n16), 32 * p + k8), So[p], Y[t]);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int r0 = row4_of(t, g4);
-      const f32x4 lead = *reinterpret_cast<const f32x4*>(gates.lead + r0), v = V::rows4(Vs, r0, 16 * wave, n16);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) Y[t][i] = fmaf(-lead[i], Y[t][i], v[i]);
     }
     // delta, W and e^(gamma_C - gamma) W
-    const Split<E, FINE> Yo[2] = {split<E, FINE>(Y[0], Y[1]), split<E, FINE>(Y[2], Y[3])};
+    {
+      Split<E> T[2][4];
+      const auto fetch = [&](int p) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) W[t] = zero4();
+        for (int t = 2 * p; t < 4; ++t)
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+          for (int part = 0; part < PARTS; ++part) T[p][t].part[part] = M::row(Ts[part], row_of(t, n16), 32 * p + k8);
+      };
+      f32x4 lead[4], v[4];
 #pragma unroll
-      for (int t = 2 * p; t < 4; ++t) {
-        Split<E> T;
-#pragma unroll
-        for (int part = 0; part < PARTS; ++part) T.part[part] = M::row(Ts[part], row_of(t, n16), 32 * p + k8);
-        W[t] = mma<E>(T, Yo[p], W[t]);
+      for (int t = 0; t < 4; ++t) {
+        lead[t] = *reinterpret_cast<const f32x4*>(gates.lead + row4_of(t, g4));
+        v[t] = V::rows4(Vs, row4_of(t, g4), 16 * wave, n16);
       }
+      fetch(0);
+      if constexpr (MODE != STATE) batch<E>();
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) Y[t][i] = fmaf(-lead[t][i], Y[t][i], v[t][i]);
+        W[t] = zero4();
+      }
+      const Split<E, FINE> Yo[2] = {split<E, FINE>(Y[0], Y[1]), split<E, FINE>(Y[2], Y[3])};
+      fetch(1);
+      if constexpr (MODE != STATE) batch<E>();
+      mma_tiles<E, 0, 4>(W, T[0], Yo[0]);
+      mma_tiles<E, 2, 4>(W, T[1], Yo[1]);
+      if constexpr (MODE != STATE) batch<E>();
+    }
+    f32x4 beta[4], late[4];
+    float leads[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      const int r0 = row4_of(t, g4);
-      if (MODE == TRAIN && cols) store_rows(W[t], a.err + (((long)bh * a.N + n) * C + r0) * a.DVP + j, a.DVP, n16);
-      const f32x4 beta = *reinterpret_cast<const f32x4*>(gates.beta + r0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) W[t][i] *= beta[i];
+      beta[t] = *reinterpret_cast<const f32x4*>(gates.beta + row4_of(t, g4));
+      late[t] = *reinterpret_cast<const f32x4*>(gates.late + row4_of(t, g4));
+      leads[t] = gates.lead[16 * t + n16];
     }
-    if (MODE == TRAIN && cols) {
-      E* to = (E*)a.state0 + (((long)bh * a.N + n) * a.DVP + j + n16) * DK + k8;
+    const float whole = gates.lead[C - 1];
+    if constexpr (MODE != STATE) batch<E>();
 #pragma unroll
-      for (int p = 0; p < CP; ++p) *reinterpret_cast<Frag<E>*>(to + 32 * p) = So[p].part[0];
+    for (int t = 0; t < 4; ++t) {
+      if (MODE == TRAIN && cols) store_rows(W[t], a.err + (((long)bh * a.N + n) * C + row4_of(t, g4)) * a.DVP + j, a.DVP, n16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) W[t][i] *= beta[t][i];
     }
     if constexpr (MODE != STATE) {
       const Split<E, FINE> Wo[2] = {split<E, FINE>(W[0], W[1]), split<E, FINE>(W[2], W[3])};
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) O[t][i] *= leads[t];
       __syncthreads();
-      // O, transposed products: a lane has four columns of one token.  A forward-only call rounds the state, W and P
-      // to one bf16 here: o is rounded to it after all.
+      P.put(Ts, PP, wave, n16, g4);
+      __syncthreads();
       const int lane = fresh_tid() & 63, n16 = lane & 15, g4 = lane >> 4, k8 = 8 * g4;
-      f32x4 O[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) O[t] = zero4();
-#pragma unroll
-      for (int p = 0; p < CP; ++p)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const Frag<E> q = K::row(Qs, 16 * t + n16, 32 * p + k8);
-          O[t] = MODE == TRAIN ? mma<E>(So[p], q, O[t]) : mma(So[p].part[0], q, O[t]);
-        }
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const float lead = gates.lead[16 * t + n16];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) O[t][i] *= lead;
-      }
+      Split<E, PP> Pf[2][4];
 #pragma unroll
       for (int p = 0; p < 2; ++p)
 #pragma unroll
-        for (int t = 2 * p; t < 4; ++t) {
-          Split<E, PP> Pf;
+        for (int t = 2 * p; t < 4; ++t)
 #pragma unroll
-          for (int part = 0; part < PP; ++part) Pf.part[part] = M::row(Ps[part], 16 * t + n16, 32 * p + k8);
-          O[t] = MODE == TRAIN ? mma<E>(Wo[p], Pf, O[t]) : mma(Wo[p].part[0], Pf.part[0], O[t]);
-        }
+          for (int part = 0; part < PP; ++part) Pf[p][t].part[part] = M::row(Ts[part], 16 * t + n16, 32 * p + k8);
+      if constexpr (MODE != STATE) batch<E>();
+      if constexpr (MODE == TRAIN) {
+        mma_tiles<E, 0, 4, PP, FINE, 4, true>(O, Pf[0], Wo[0]);
+        mma_tiles<E, 2, 4, PP, FINE, 4, true>(O, Pf[1], Wo[1]);
+      } else {
+        mma_tiles<E, 0, 4, 1, 1, 4, true>(O, Pf[0], Split<E, 1>{{Wo[0].part[0]}});
+        mma_tiles<E, 2, 4, 1, 1, 4, true>(O, Pf[1], Split<E, 1>{{Wo[1].part[0]}});
+      }
+    }
+    {
+      const int lane = fresh_tid() & 63, n16 = lane & 15, g4 = lane >> 4;
+      constexpr int TILES = CB < 4 ? CB : 4;  // a batch
+      Split<E, 1> kf[2][TILES];
+      const auto fetch = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) kf[s & 1][i].part[0] = K::template col<true>(Ks, 32 * (s * TILES / CB), row4_of(s * TILES % CB + i, 0), n16, g4);
+      };
+      fetch(0);
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) W[t][i] *= late[t][i];
+      const Split<E> Wl[2] = {split<E>(W[0], W[1]), split<E>(W[2], W[3])};
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) S[cb][i] *= whole;
+#pragma unroll
+      for (int s = 0; s < 2 * CB / TILES; ++s) {
+        if (s + 1 < 2 * CB / TILES) fetch(s + 1);
+        if constexpr (MODE != STATE) batch<E>();
+#pragma unroll
+        for (int part = PARTS - 1; part >= 0; --part)
+#pragma unroll
+          for (int i = 0; i < TILES; ++i) {
+            f32x4& acc = S[s * TILES % CB + i];
+            acc = mma(kf[s & 1][i].part[0], Wl[s * TILES / CB].part[part], acc);
+          }
+        if constexpr (MODE != STATE) batch<E>();
+      }
+    }
+    if constexpr (MODE != STATE) {
+      const int lane = fresh_tid() & 63, n16 = lane & 15, g4 = lane >> 4;
       const long row0 = (long)n * C;
       E* to = (E*)a.o + ((long)bh * a.T + row0) * a.dv + j;
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const int row = 16 * t + n16;
-        if (!cols || row >= len - n * C) continue;
+        if (!cols || row >= left) continue;
         store4_part<E>(to + row * a.dv + 4 * g4, O[t], a.dv - j - 4 * g4);
         if constexpr (MODE == TRAIN && PARTS == 2) {
           typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -349,52 +391,33 @@ __global__ __launch_bounds__(64 * NW) void delta_fwd_kernel(DeltaArgs a) {
         }
       }
     }
-    {
-      const int lane = fresh_tid() & 63, n16 = lane & 15, g4 = lane >> 4;
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const f32x4 late = *reinterpret_cast<const f32x4*>(gates.late + row4_of(t, g4));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) W[t][i] *= late[i];
-      }
-      const Split<E> Wl[2] = {split<E>(W[0], W[1]), split<E>(W[2], W[3])};
-      const float whole = gates.lead[C - 1];
-#pragma unroll
-      for (int cb = 0; cb < CB; ++cb)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) S[cb][i] *= whole;
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb) S[cb] = mma<E>(K::template col<true>(Ks, 32 * p, row4_of(cb, 0), n16, g4), Wl[p], S[cb]);
-    }
     if (MODE == TRAIN && cols && (n % kDeltaMarks == kDeltaMarks - 1 || n == alive - 1))
-      store_regs<CB>(S, a.mark + (((long)bh * a.marks + n / kDeltaMarks) * (a.DVP / 16) + j / 16) * DK * 16);
+      store_regs<CB>(S, a.mark + (((long)bh * a.marks + n / kDeltaMarks) * tiles + j / 16) * DK * 16);
   }
   if (!cols) return;
   if (MODE == STATE) {
     if (!transition) {
-      store_regs<CB>(S, a.seg + (((long)bh * a.P + seg) * (a.DVP / 16) + j / 16) * DK * 16);
-    } else {
-      const long block = ((long)bh * a.P + seg) * DK * DK, mplane = (long)a.B * a.H * a.P * DK * DK;
-      E* to = (E*)a.trans + block + (long)(j + n16) * DK + 8 * g4;
+      store_regs<CB>(S, a.seg + (((long)bh * a.P + seg) * tiles + j / 16) * DK * 16);
+      return;
+    }
+    const long block = ((long)bh * a.P + seg) * DK * DK, mplane = (long)a.B * a.H * a.P * DK * DK;
+    E* to = (E*)a.trans + block + (long)(j + n16) * DK + k8;
 #pragma unroll
-      for (int p = 0; p < CP; ++p) {
-        const Split<E> s = split<E>(S[2 * p], S[2 * p + 1]);
+    for (int p = 0; p < CP; ++p) {
+      const Split<E> s = split<E>(S[2 * p], S[2 * p + 1]);
 #pragma unroll
-        for (int part = 0; part < PARTS; ++part) *reinterpret_cast<Frag<E>*>(to + part * mplane + 32 * p) = s.part[part];
-      }
-      E* by_rows = (E*)a.trans_rows + block + j + 4 * (n16 >> 2);
+      for (int part = 0; part < PARTS; ++part) *reinterpret_cast<Frag<E>*>(to + part * mplane + 32 * p) = s.part[part];
+    }
+    E* by_rows = (E*)a.trans_rows + block + j + 4 * (n16 >> 2);
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb) {
-        f32x4 x = quad_transpose(S[cb]);
-        E* p = by_rows + (row4_of(cb, g4) + (n16 & 3)) * DK;
+    for (int cb = 0; cb < CB; ++cb) {
+      f32x4 x = quad_transpose(S[cb]);
+      E* p = by_rows + (row4_of(cb, g4) + (n16 & 3)) * DK;
 #pragma unroll
-        for (int part = 0; part < PARTS; ++part) {
-          store4(p + part * mplane, x);
+      for (int part = 0; part < PARTS; ++part) {
+        store4(p + part * mplane, x);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] -= (float)(E)x[i];
-        }
+        for (int i = 0; i < 4; ++i) x[i] -= (float)(E)x[i];
       }
     }
     return;

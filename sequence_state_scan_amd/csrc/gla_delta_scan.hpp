@@ -6,11 +6,12 @@ namespace gla {
 namespace delta {
 
 // S <- M S + S_own over the segments; backward from the last segment with M transposed, from the gradient of the last
-// state.  A workgroup has 32 columns of a head, a wave of it 16 rows of the state: its rows of the next M and of S_own
-// are on their way while the waves exchange the state as the product's operand through LDS, one barrier a step.
+// state.  A workgroup has 32 columns of a head, a wave of it 16 rows of the state: the waves exchange the state as the
+// product's operand through LDS, one barrier a step, while their rows of the next M and S_own are on their way, AHEAD
+// steps before their use.  31 steps of 4 heads of 128 x 256 take 66 us, of 16 and 64 columns a workgroup 64 and 118.
 template <typename E, int DK, bool BWD>
 __global__ __launch_bounds__(4 * DK) void delta_scan_kernel(DeltaArgs a) {
-  constexpr int CP = DK / 32, PARTS = Num<E>::PARTS, COLS = 2;
+  constexpr int CP = DK / 32, PARTS = Num<E>::PARTS, COLS = 2, AHEAD = 2;
   typedef Tile<E, DK> T;  // [column][row of the state]
   __shared__ __attribute__((aligned(16))) E Ss[2][PARTS][16 * COLS * T::LD];
   const int heads = a.B * a.H, bh = blockIdx.x % heads, b = bh / a.H, lane = lane_id(), n16 = lane & 15, g4 = lane >> 4;
@@ -19,31 +20,38 @@ __global__ __launch_bounds__(4 * DK) void delta_scan_kernel(DeltaArgs a) {
   const long tiles = a.DVP / 16, plane = (long)heads * a.P * DK * DK;
   const float* from = BWD ? a.dhT : a.h0;
   const E* mp = (const E*)(BWD ? a.trans : a.trans_rows) + (long)bh * a.P * DK * DK + row_of(cb, n16) * DK + 8 * g4;
-  const auto place = [&](int seg, int c) { return (((long)bh * a.P + seg) * tiles + j0 / 16 + c) * DK * 16 + cb * 256 + lane * 4; };
-  const auto have = [&](int c) { return j0 + 16 * c < a.dv; };
-  f32x4 S[COLS], own[COLS];
-  Split<E> M[CP];
+  // (a column tile behind the last: the last's place and the last's values)
+  const auto place = [&](int seg, int c) { return (((long)bh * a.P + seg) * tiles + min(j0 / 16 + c, (int)tiles - 1)) * DK * 16 + cb * 256 + lane * 4; };
+  f32x4 S[COLS], own[AHEAD][COLS];
+  Split<E> M[AHEAD][CP];
 #pragma unroll
   for (int c = 0; c < COLS; ++c)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int col = j0 + 16 * c + n16;
+      const int col = min(j0 + 16 * c, a.DVP - 16) + n16;
       S[c][i] = from && r0 + i < a.dk && col < a.dv ? from[((long)bh * a.dk + r0 + i) * a.dv + col] : 0.f;
     }
-  const auto load = [&](int step) {
-    const int seg = BWD ? steps - step : step;
+  arrived<COLS>(S);
+  const auto load = [&](int step, Split<E> (&m)[CP], f32x4 (&o)[COLS]) {  // every step loads, the last ones again
+    const int at = min(step, steps - 1), seg = BWD ? steps - at : at;
 #pragma unroll
     for (int p = 0; p < CP; ++p)
 #pragma unroll
-      for (int part = 0; part < PARTS; ++part) M[p].part[part] = *reinterpret_cast<const Frag<E>*>(mp + part * plane + (long)seg * DK * DK + 32 * p);
+      for (int part = 0; part < PARTS; ++part) m[p].part[part] = *reinterpret_cast<const Frag<E>*>(mp + part * plane + (long)seg * DK * DK + 32 * p);
 #pragma unroll
-    for (int c = 0; c < COLS; ++c) own[c] = have(c) ? *reinterpret_cast<const f32x4*>(a.seg + place(seg, c)) : zero4();
+    for (int c = 0; c < COLS; ++c) o[c] = *reinterpret_cast<const f32x4*>(a.seg + place(seg, c));
   };
-  if (steps > 0) load(0);
-  for (int step = 0; step < steps; ++step) {
+  if (steps > 0) {
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      load(k, M[k], own[k]);
+      batch<E>();  // in the order of their use
+    }
+  }
+  const auto advance = [&](int step, const Split<E> (&m)[CP], const f32x4 (&o)[COLS]) {
 #pragma unroll
     for (int c = 0; c < COLS; ++c) {
-      if (have(c)) *reinterpret_cast<f32x4*>(a.seg_in + place(BWD ? steps - step : step, c)) = S[c];
+      *reinterpret_cast<f32x4*>(a.seg_in + place(BWD ? steps - step : step, c)) = S[c];
       f32x4 x = S[c];
 #pragma unroll
       for (int part = 0; part < PARTS; ++part) {
@@ -52,23 +60,35 @@ __global__ __launch_bounds__(4 * DK) void delta_scan_kernel(DeltaArgs a) {
         for (int i = 0; i < 4; ++i) x[i] -= (float)(E)x[i];
       }
     }
-    __syncthreads();  // (the other half is free: every wave has read it before this barrier's last pass)
-#pragma unroll
-    for (int c = 0; c < COLS; ++c) S[c] = own[c];
+    __syncthreads();  // (the other half is free: every wave has read it before the barrier after)
+    Split<E> s[CP][COLS];
 #pragma unroll
     for (int p = 0; p < CP; ++p)
 #pragma unroll
-      for (int c = 0; c < COLS; ++c) {
-        Split<E> s;
+      for (int c = 0; c < COLS; ++c)
 #pragma unroll
-        for (int part = 0; part < PARTS; ++part) s.part[part] = T::row(Ss[step & 1][part], 16 * c + n16, 32 * p + 8 * g4);
-        S[c] = mma<E>(M[p], s, S[c]);
-      }
-    if (step + 1 < steps) load(step + 1);
-  }
+        for (int part = 0; part < PARTS; ++part) s[p][c].part[part] = T::row(Ss[step & 1][part], 16 * c + n16, 32 * p + 8 * g4);
+    batch<E>();
+#pragma unroll
+    for (int c = 0; c < COLS; ++c) S[c] = o[c];
+#pragma unroll
+    for (int p = 0; p < CP; ++p) mma_tiles<E, 0, COLS, PARTS, PARTS, COLS, true>(S, s[p], m[p]);
+    batch<E>();
+  };
+  int step = 0;
+  for (; step + AHEAD <= steps; step += AHEAD)  // (whole rounds: a way out of one would make every round wait for all loads)
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      advance(step + k, M[k], own[k]);
+      load(step + k + AHEAD, M[k], own[k]);
+      batch<E>();
+    }
+#pragma unroll
+  for (int k = 0; k < AHEAD - 1; ++k)
+    if (step + k < steps) advance(step + k, M[k], own[k]);
 #pragma unroll
   for (int c = 0; c < COLS; ++c)
-    if (have(c)) *reinterpret_cast<f32x4*>(a.seg_in + place(BWD ? 0 : steps, c)) = S[c];
+    *reinterpret_cast<f32x4*>(a.seg_in + place(BWD ? 0 : steps, c)) = S[c];
 }
 
 }  // namespace delta
