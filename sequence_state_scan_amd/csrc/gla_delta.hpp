@@ -37,17 +37,19 @@ struct DeltaArgs : DeltaShape {
   // scratch there
   float* gates;   // [BH][N][5][64]
   void* solveT;   // [BH][N][64][64]: (I + beta B)^-1, transposed (bf16: the high parts, then the low parts)
-  void* trans;    // [BH][P][DKP][DKP]: a segment's transition, transposed (the same)
-  float* err;     // [BH][N * 64][DVP]: delta
-  short* o_rest;  // [BH][N * 64][DVP]: what o's rounding left (bf16; see rest_of)
-  void* state0;   // [BH][N][DVP][DKP]: the state entering a chunk, transposed, in dtype
-  float* mark;    // [BH][marks][DVP / 16][DKP / 16][256]: the state leaving every fourth chunk, in registers' order
+  void* trans;    // [BH][P]: a segment's transition M, transposed, in operands' order (frag_at; bf16: high, then low parts)
+  // a chunk's tensors in the order of the registers that hold them, so that a wave stores 1024 bytes on end: 16 value
+  // columns after the other, [BH][N][DVP / 16]
+  float* err;     // [4][64][4]: delta, see rows_at
+  short* o_rest;  // [4][64][4]: what o's rounding left (bf16; see rest_of), lane 16 (c / 4) + r % 16 of tile r / 16
+  void* state0;   // [DKP / 32][64][8]: the state entering a chunk, in dtype, lane 16 (channel / 8 % 4) + column
+  float* mark;    // [BH][marks][DVP / 16][DKP / 16][256]: the state leaving every fourth chunk
   // scratch
   void* solve;    // [BH][N][64][64]: (I + B beta)^-1
-  void* trans_rows;  // [BH][P][DKP][DKP]: a segment's transition by rows (as trans)
+  void* trans_rows;  // a segment's transition, not transposed (as trans)
   float *seg, *seg_in;  // [BH][P][DVP / 16][DKP / 16][256]: a segment's own end state, the state entering it
-  float* z;       // [BH][N * 64][DVP]
-  void* grad1;    // [BH][N][DVP][DKP]: the gradient of the state leaving a chunk, transposed
+  float* z;       // as err
+  void* grad1;    // the gradient of the state leaving a chunk, as state0
   float* carry;   // [BH][marks][DVP / 16]: <state, its gradient> at the marks
   float* at;      // [BH][N * 64]: o . do - v . dv
   float *dq_heads, *dk_heads;  // [B][H][T][dk], where heads share keys
@@ -278,11 +280,6 @@ struct Tile {
     return __builtin_amdgcn_ds_read_tr16_b64_v4bf16((__attribute__((address_space(3))) v4*)p);
   }
 };
-__device__ __forceinline__ f32x8 load8(const float* p) {
-  const f32x4 x = *reinterpret_cast<const f32x4*>(p), y = *reinterpret_cast<const f32x4*>(p + 4);
-  return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-
 // 8 (4) elements in memory at any alignment of the element.
 template <typename E, int N>
 struct Raw {
@@ -494,9 +491,17 @@ __device__ __forceinline__ void store_regs(const f32x4 (&S)[CB], float* p) {
   for (int cb = 0; cb < CB; ++cb) *reinterpret_cast<f32x4*>(p + cb * 256 + lane_id() * 4) = S[cb];
 }
 
-// An accumulator tile of 4 rows x the lane's column, stored by rows.  p: the first of its rows, the first of 16 columns.
-__device__ __forceinline__ void store_rows(f32x4 x, float* p, int pitch, int s) {
-  *reinterpret_cast<f32x4*>(p + (s & 3) * pitch + 4 * (s >> 2)) = quad_transpose(x);
+// Where an operand of 8 values lies: row r, columns 8 k .. 8 k + 7 of a DK x DK matrix, one 1024-byte block for the 64
+// lanes of a product's operand (rows row_of(cb, .), columns 32 p + ..).
+template <int DK>
+__device__ __forceinline__ int frag_at(int r, int k) {
+  const int cb = 2 * (r >> 5) + ((r >> 2) & 1), n16 = 4 * ((r >> 3) & 3) + (r & 3);
+  return (cb * (DK / 32) + (k >> 2)) * 512 + (16 * (k & 3) + n16) * 8;
+}
+// Where 4 columns from c (a multiple of 4) of a chunk's row r lie in 16 columns' accumulators, transposed by quads.
+__device__ __forceinline__ int rows_at(int r, int c) {
+  const int t = 2 * (r >> 5) + ((r >> 2) & 1);
+  return t * 256 + (16 * ((r >> 3) & 3) + 4 * (c >> 2) + (r & 3)) * 4;
 }
 
 // A float32's place beside its bf16 rounding: the difference of their bit patterns fits 16 bits (of a tie, up to one

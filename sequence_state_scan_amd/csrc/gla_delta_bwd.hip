@@ -113,7 +113,7 @@ __global__ __launch_bounds__(64 * NW) void delta_bwd_kernel(DeltaArgs a) {
       for (int p = 0; p < CP; ++p) {
         const Split<E> Do = split<E>(D[2 * p], D[2 * p + 1]);
         if (!STATE && cols)
-          *reinterpret_cast<Frag<E>*>((E*)a.grad1 + (((long)bh * a.N + n) * a.DVP + j + n16) * DK + k8 + 32 * p) = Do.part[0];
+          *reinterpret_cast<Frag<E>*>((E*)a.grad1 + ((((long)bh * a.N + n) * tiles + j / 16) * CP + p) * 512 + lane * 8) = Do.part[0];
         if (p + 1 < CP) fetch(p + 1);
         batch<E>();
         mma_tiles<E, 0, 4>(dW, kf[p & 1], Do);
@@ -179,7 +179,7 @@ __global__ __launch_bounds__(64 * NW) void delta_bwd_kernel(DeltaArgs a) {
       fetch(0);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {  // z, then -e^gamma dV
-        if (!STATE && cols) store_rows(Y[t], a.z + (((long)bh * a.N + n) * C + row4_of(t, g4)) * a.DVP + j, a.DVP, n16);
+        if (!STATE && cols) *reinterpret_cast<f32x4*>(a.z + ((((long)bh * a.N + n) * tiles + j / 16) * 4 + t) * 256 + lane * 4) = quad_transpose(Y[t]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) Y[t][i] *= -lead[t][i] * beta[t][i];
       }
@@ -238,7 +238,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a) {
   const int n = blockIdx.x % a.N, bh = blockIdx.x / a.N, b = bh / a.H, h = bh - b * a.H, hk = h / (a.H / a.Hk);
   const int len = length_of(a, b), lane = lane_id(), n16 = lane & 15, g4 = lane >> 4;
   const int wave = wave_id() & 3, half = wave_id() >> 2;  // half: channels CH * 16 half on, and G
-  const long t0 = (long)n * C, row0 = (long)bh * a.N * C + t0;  // row0: in the padded tensors
+  const long t0 = (long)n * C, chunk = (long)bh * a.N + n, row0 = chunk * C;  // row0: in the padded tensor
   const int left = len - n * C, rows = min(C, a.T - n * C);     // rows of the chunk that exist
   const bool shared = a.H != a.Hk;
   const auto put = [&](void* out, float* heads, int row, int c, f32x4 x, f32x4 y) {
@@ -279,10 +279,16 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a) {
   float at = 0.f, db = 0.f;
   const int r = threadIdx.x / UPR, cc = threadIdx.x % UPR * 8;  // the lane's row and columns of a block
   for (int c0 = 0; c0 < a.DVP; c0 += BC) {
-    TileIn<E, BC, DK, NT> s0, d1;
-    const long st = (((long)bh * a.N + n) * a.DVP + c0) * DK;
-    s0.load((const E*)a.state0 + st, DK, a.DVP - c0, DK);
-    d1.load((const E*)a.grad1 + st, DK, a.DVP - c0, DK);
+    constexpr int UNITS = BC * DK / 8, PER = UNITS / NT < 1 ? 1 : UNITS / NT;
+    typedef E v8 __attribute__((ext_vector_type(8), aligned(16)));
+    v8 s0[PER], d1[PER];
+    const long st = (chunk * (a.DVP / 16) + c0 / 16) * DK * 16;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {  // every lane loads, as in TileIn
+      const int u = min((int)threadIdx.x + i * NT, min(UNITS, (a.DVP - c0) * DK / 8) - 1);
+      s0[i] = *reinterpret_cast<const v8*>((const E*)a.state0 + st + u * 8);
+      d1[i] = *reinterpret_cast<const v8*>((const E*)a.grad1 + st + u * 8);
+    }
     if (c0) __syncthreads();
     if (r < C) {
       const int c = c0 + cc;
@@ -295,15 +301,19 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a) {
         const int rr = min(r, min(left, rows) - 1), ci = c < a.dvr ? c : 0;
         x = *reinterpret_cast<const R8*>(dO + rr * a.dos.t + ci);
         vv = *reinterpret_cast<const R8*>(v + rr * a.vs.t + ci);
-        if (sizeof(E) == 2) rest = *reinterpret_cast<const S8*>(a.o_rest + (row0 + rr) * a.DVP + ci);
+        if constexpr (sizeof(E) == 2) {
+          const short* p = a.o_rest + (chunk * (a.DVP / 16) + ci / 16) * 1024 + (rr >> 4) * 256 + (16 * ((ci & 15) >> 2) + (rr & 15)) * 4;
+          typedef short S4 __attribute__((ext_vector_type(4)));
+          rest = __builtin_shufflevector(*reinterpret_cast<const S4*>(p), *reinterpret_cast<const S4*>(p + 64), 0, 1, 2, 3, 4, 5, 6, 7);
+        }
         if (a.dv % 8 == 0) ov = *reinterpret_cast<const R8*>(o + (long)rr * a.dv + ci);
         else ov = load8_part<E>(o + (long)rr * a.dv + min(ci, a.dv - 1), min(a.dv - ci, 8));
         const int cz = c < a.DVP ? c : 0;
-        z = load8(a.z + (row0 + r) * a.DVP + cz);
-        d = load8(a.err + (row0 + r) * a.DVP + cz);
+        const long p = (chunk * (a.DVP / 16) + cz / 16) * 1024 + rows_at(r, cz & 15);
+        z = __builtin_shufflevector(load4(a.z + p), load4(a.z + p + 16), 0, 1, 2, 3, 4, 5, 6, 7);
+        d = __builtin_shufflevector(load4(a.err + p), load4(a.err + p + 16), 0, 1, 2, 3, 4, 5, 6, 7);
       }
       const float beta = gates.beta[r];
-      typedef E v8 __attribute__((ext_vector_type(8), aligned(16)));
       v8 w, y, ox;
       f32x4 y0, y1;
 #pragma unroll
@@ -331,8 +341,14 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a) {
         store4_part<E>(to + 4, y1, a.dv - c - 4);
       }
     }
-    s0.store(S0, a.DVP - c0, DK);
-    d1.store(D1, a.DVP - c0, DK);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int u = threadIdx.x + i * NT, l = u & 63, col = u / (64 * CP) * 16 + (l & 15), at = K::at(col, 32 * (u / 64 % CP) + 8 * (l >> 4));
+      if (UNITS % NT == 0 || u < UNITS) {
+        *reinterpret_cast<v8*>(S0 + at) = c0 + col < a.DVP ? s0[i] : (v8){};
+        *reinterpret_cast<v8*>(D1 + at) = c0 + col < a.DVP ? d1[i] : (v8){};
+      }
+    }
     __syncthreads();
 #pragma unroll
     for (int p = 0; p < BC / 32; ++p) {

@@ -260,7 +260,7 @@ __global__ __launch_bounds__(64 * NW, MODE == STATE && sizeof(E) == 2 && NW == 8
       for (int p = 0; p < CP; ++p) {
         const Split<E> So = split<E>(S[2 * p], S[2 * p + 1]);
         if (MODE == TRAIN && cols)
-          *reinterpret_cast<Frag<E>*>((E*)a.state0 + (((long)bh * a.N + n) * a.DVP + j + n16) * DK + k8 + 32 * p) = So.part[0];
+          *reinterpret_cast<Frag<E>*>((E*)a.state0 + ((((long)bh * a.N + n) * tiles + j / 16) * CP + p) * 512 + lane * 8) = So.part[0];
         if (p + 1 < CP) fetch(p + 1);
         if constexpr (MODE != STATE) batch<E>();
         mma_tiles<E, 0, 4>(Y, kf[p & 1], So);
@@ -311,7 +311,7 @@ __global__ __launch_bounds__(64 * NW, MODE == STATE && sizeof(E) == 2 && NW == 8
     if constexpr (MODE != STATE) batch<E>();
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      if (MODE == TRAIN && cols) store_rows(W[t], a.err + (((long)bh * a.N + n) * C + row4_of(t, g4)) * a.DVP + j, a.DVP, n16);
+      if (MODE == TRAIN && cols) *reinterpret_cast<f32x4*>(a.err + ((((long)bh * a.N + n) * tiles + j / 16) * 4 + t) * 256 + lane * 4) = quad_transpose(W[t]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) W[t][i] *= beta[t][i];
     }
@@ -387,7 +387,7 @@ __global__ __launch_bounds__(64 * NW, MODE == STATE && sizeof(E) == 2 && NW == 8
           s16x4 rest;
 #pragma unroll
           for (int i = 0; i < 4; ++i) rest[i] = rest_of(O[t][i], (bf16)O[t][i]);
-          *reinterpret_cast<s16x4*>(a.o_rest + ((long)bh * a.N * C + row0 + row) * a.DVP + j + 4 * g4) = rest;
+          *reinterpret_cast<s16x4*>(a.o_rest + ((((long)bh * a.N + n) * tiles + j / 16) * 4 + t) * 256 + lane * 4) = rest;
         }
       }
     }
@@ -401,18 +401,19 @@ __global__ __launch_bounds__(64 * NW, MODE == STATE && sizeof(E) == 2 && NW == 8
       return;
     }
     const long block = ((long)bh * a.P + seg) * DK * DK, mplane = (long)a.B * a.H * a.P * DK * DK;
-    E* to = (E*)a.trans + block + (long)(j + n16) * DK + k8;
+    E* to = (E*)a.trans + block;
 #pragma unroll
     for (int p = 0; p < CP; ++p) {
       const Split<E> s = split<E>(S[2 * p], S[2 * p + 1]);
 #pragma unroll
-      for (int part = 0; part < PARTS; ++part) *reinterpret_cast<Frag<E>*>(to + part * mplane + 32 * p) = s.part[part];
+      for (int part = 0; part < PARTS; ++part) *reinterpret_cast<Frag<E>*>(to + part * mplane + frag_at<DK>(j + n16, 4 * p + g4)) = s.part[part];
     }
-    E* by_rows = (E*)a.trans_rows + block + j + 4 * (n16 >> 2);
+    const int c = j + 4 * (n16 >> 2);
+    E* by_rows = (E*)a.trans_rows + block + (c & 7);
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb) {
       f32x4 x = quad_transpose(S[cb]);
-      E* p = by_rows + (row4_of(cb, g4) + (n16 & 3)) * DK;
+      E* p = by_rows + frag_at<DK>(row4_of(cb, g4) + (n16 & 3), c >> 3);
 #pragma unroll
       for (int part = 0; part < PARTS; ++part) {
         store4(p + part * mplane, x);

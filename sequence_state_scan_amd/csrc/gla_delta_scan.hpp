@@ -8,7 +8,9 @@ namespace delta {
 // S <- M S + S_own over the segments; backward from the last segment with M transposed, from the gradient of the last
 // state.  A workgroup has 32 columns of a head, a wave of it 16 rows of the state: the waves exchange the state as the
 // product's operand through LDS, one barrier a step, while their rows of the next M and S_own are on their way, AHEAD
-// steps before their use.  31 steps of 4 heads of 128 x 256 take 66 us, of 16 and 64 columns a workgroup 64 and 118.
+// steps before their use.  What bounds a step is issuing the loads of M, 64 KB a CU, so M lies in the order of its
+// operands and a load takes whole lines (31 steps of 4 heads of 128 x 256: 39 us; by rows, 16 half lines a load, 66, and
+// with 16 or 64 columns a workgroup 64 and 118).
 template <typename E, int DK, bool BWD>
 __global__ __launch_bounds__(4 * DK) void delta_scan_kernel(DeltaArgs a) {
   constexpr int CP = DK / 32, PARTS = Num<E>::PARTS, COLS = 2, AHEAD = 2;
@@ -19,7 +21,7 @@ __global__ __launch_bounds__(4 * DK) void delta_scan_kernel(DeltaArgs a) {
   const int alive = (length_of(a, b) + C - 1) / C, steps = max(1, (alive + a.L - 1) / a.L) - 1;
   const long tiles = a.DVP / 16, plane = (long)heads * a.P * DK * DK;
   const float* from = BWD ? a.dhT : a.h0;
-  const E* mp = (const E*)(BWD ? a.trans : a.trans_rows) + (long)bh * a.P * DK * DK + row_of(cb, n16) * DK + 8 * g4;
+  const E* mp = (const E*)(BWD ? a.trans : a.trans_rows) + (long)bh * a.P * DK * DK + cb * CP * 512 + lane * 8;
   // (a column tile behind the last: the last's place and the last's values)
   const auto place = [&](int seg, int c) { return (((long)bh * a.P + seg) * tiles + min(j0 / 16 + c, (int)tiles - 1)) * DK * 16 + cb * 256 + lane * 4; };
   f32x4 S[COLS], own[AHEAD][COLS];
@@ -37,7 +39,7 @@ __global__ __launch_bounds__(4 * DK) void delta_scan_kernel(DeltaArgs a) {
 #pragma unroll
     for (int p = 0; p < CP; ++p)
 #pragma unroll
-      for (int part = 0; part < PARTS; ++part) m[p].part[part] = *reinterpret_cast<const Frag<E>*>(mp + part * plane + (long)seg * DK * DK + 32 * p);
+      for (int part = 0; part < PARTS; ++part) m[p].part[part] = *reinterpret_cast<const Frag<E>*>(mp + part * plane + (long)seg * DK * DK + p * 512);
 #pragma unroll
     for (int c = 0; c < COLS; ++c) o[c] = *reinterpret_cast<const f32x4*>(a.seg + place(seg, c));
   };
