@@ -14,7 +14,7 @@ constexpr int kDeltaGates = 5 * kDeltaChunk;  // floats of a chunk's gate block:
 // Sizes that follow from a call's.  The sequence's chunks are cut into P segments of L chunks.
 struct DeltaShape {
   int B, H, Hk, T, dk, dv, dtype;
-  int N, P, L, DKP, DVP, marks;  // chunks, segments, their chunks, padded channels and values, marks
+  int N, P, L, NW, DKP, DVP, marks;  // chunks, segments, their chunks, a walk's waves, padded channels and values, marks
   int dkr, dvr;                  // dk and dv rounded up to 8: the rows that the walks read
 };
 DeltaShape delta_shape(int B, int H, int Hk, int T, int dk, int dv, int dtype);

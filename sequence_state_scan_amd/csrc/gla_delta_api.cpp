@@ -10,6 +10,13 @@
 namespace gla {
 
 // A sequence's chunks are cut into segments where the heads and their column tiles would leave CUs idle.
+// Segments: as many as give each of the 256 CUs a walk of its own, never more than one (200 heads of 2048 tokens in two
+// segments, bf16 128 x 128: forward 366 us, whole 239; 128 heads in two 222, whole 211), and no more than 3 sqrt(N):
+// a segment's two walks of L = N / P chunks take about 6 us a chunk each, the chain between them 1.3 us a segment, so the
+// best P is near 3 sqrt(N) (4 heads of 8192 tokens: P = 128 127 us, 64 (and 3 sqrt(N)) 98, 32 97, 16 110; of 1024, N = 16:
+// P = 16 53, 8 48, 4 57, 1 86).  Two segments' walks take as long as the one whole.
+// Columns: 128 a workgroup, 64 where even then half the CUs have none (float32 6 heads of 333 tokens, 48 x 80: training
+// step 104 us with 128, 92 with 64).
 DeltaShape delta_shape(int B, int H, int Hk, int T, int dk, int dv, int dtype) {
   DeltaShape s{};
   s.B = B;
@@ -25,10 +32,13 @@ DeltaShape delta_shape(int B, int H, int Hk, int T, int dk, int dv, int dtype) {
   s.dkr = (dk + 7) / 8 * 8;
   s.dvr = (dv + 7) / 8 * 8;
   s.marks = (s.N + kDeltaMarks - 1) / kDeltaMarks;
-  const long long units = (long long)B * H * (dv <= 64 ? 1 : (dv + 127) / 128);
-  long long P = (256 + units - 1) / units;
-  if (P > s.N / 8) P = s.N / 8;
-  if (P < 1) P = 1;
+  long long most = 1;
+  while (most < s.N && (most + 1) * (most + 1) <= 9LL * s.N) ++most;
+  const long long heads = (long long)B * H, wide = heads * ((dv + 127) / 128);
+  s.NW = dv <= 64 || wide * most <= 128 ? 4 : 8;
+  const long long units = heads * ((dv + 16 * s.NW - 1) / (16 * s.NW));
+  long long P = 256 / units < most ? 256 / units : most;
+  if (P < 3) P = 1;
   s.L = (int)((s.N + P - 1) / P);
   s.P = (s.N + s.L - 1) / s.L;
   return s;

@@ -450,7 +450,7 @@ static void delta_fwd_run(const DeltaArgs& a, hipStream_t s) {
 }
 template <typename E, int DK>
 static void delta_fwd_cols(const DeltaArgs& a, hipStream_t s) {
-  if (a.dv <= 64) delta_fwd_run<E, DK, 4>(a, s);
+  if (a.NW == 4) delta_fwd_run<E, DK, 4>(a, s);
   else delta_fwd_run<E, DK, 8>(a, s);
 }
 template <typename E>
