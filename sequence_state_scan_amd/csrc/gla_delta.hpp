@@ -313,13 +313,15 @@ __device__ __forceinline__ void store4_part(E* p, f32x4 x, int left) {
 // of the one, 8 of the other and a multiple of 8) are zero there.  Every lane loads, from a place inside the tile where
 // its own is outside: with loads under a condition the compiler waits for all those in flight before the next (4 heads
 // of 128 x 256 over 64k tokens: the walk 235 us).
-template <typename E, int ROWS, int D, int NT>
+// FRESH: every load and store forms its addresses anew, for a kernel that has no registers to keep them: one that comes
+// back from memory waits for the loads before it.
+template <typename E, int ROWS, int D, int NT, bool FRESH = false>
 struct TileIn {
   static constexpr int UPR = D / 8, UNITS = ROWS * UPR, PER = (UNITS + NT - 1) / NT;
   static_assert(NT % UPR == 0, "whole rows a pass");
   typename Raw<E, 8>::type r[PER];
   __device__ __forceinline__ void load(const E* src, long stride, int rows, int cols) {
-    const int t = threadIdx.x;
+    const int t = FRESH ? fresh_tid() : threadIdx.x;
     if (rows >= ROWS && cols >= D && stride < (1 << 20)) {  // the whole tile, from a base and one 32-bit offset
       const int u = UNITS % NT == 0 ? t : t < UNITS ? t : 0;
       const unsigned at = ((unsigned)(u / UPR) * (unsigned)stride + u % UPR * 8) * sizeof(E);
@@ -337,7 +339,7 @@ struct TileIn {
   }
   __device__ __forceinline__ void store(E* lds, int rows, int cols) const {
     typedef E v8 __attribute__((ext_vector_type(8), aligned(16)));
-    const int t = threadIdx.x;
+    const int t = FRESH ? fresh_tid() : threadIdx.x;
     if (rows >= ROWS && cols >= D) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
@@ -361,6 +363,22 @@ struct GateBlock {
   float lead[C], late[C], high[C], low[C], beta[C];
 };
 static_assert(sizeof(GateBlock) == kDeltaGates * sizeof(float), "a gate block's floats");
+
+// A gate block on its way, as TileIn.
+template <int NT>
+struct GateIn {
+  static constexpr int PER = (kDeltaGates + NT - 1) / NT;
+  float r[PER];
+  __device__ __forceinline__ void load(const float* src) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) r[i] = src[min((int)threadIdx.x + i * NT, kDeltaGates - 1)];
+  }
+  __device__ __forceinline__ void store(GateBlock& s) const {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if ((int)threadIdx.x + i * NT < kDeltaGates) reinterpret_cast<float*>(&s)[threadIdx.x + i * NT] = r[i];
+  }
+};
 
 // The decays from 4 tokens from `from` on to token `to`, zero where that comes before them (with ON, not where it is one
 // of them).

@@ -57,14 +57,14 @@ __global__ __launch_bounds__(64 * NW) void delta_bwd_kernel(DeltaArgs a) {
   TileIn<E, C, DK, NT> kin, qin;
   TileIn<E, C, CW, NT> oin;
   TileIn<E, C, C, NT> tin[PARTS];
-  f32x4 gin = zero4();
+  GateIn<NT> gin;
   const auto load_rows = [&](int n) {
     const long t0 = (long)n * C;
     const int left = len - n * C;
     kin.load(kp + t0 * a.ks.t, a.ks.t, left, a.dkr);
     qin.load(qp + t0 * a.qs.t, a.qs.t, left, a.dkr);
     oin.load(op + t0 * a.dos.t, a.dos.t, left, a.dvr - col0);
-    gin = reinterpret_cast<const f32x4*>(gp + (long)n * kDeltaGates)[threadIdx.x % (kDeltaGates / 4)];
+    gin.load(gp + (long)n * kDeltaGates);
   };
   const auto load_inverse = [&](int n) {
 #pragma unroll
@@ -80,7 +80,7 @@ __global__ __launch_bounds__(64 * NW) void delta_bwd_kernel(DeltaArgs a) {
     kin.store(Ks, left, a.dkr);
     qin.store(Qs, left, a.dkr);
     oin.store(Os, left, a.dvr - col0);
-    if (threadIdx.x < kDeltaGates / 4) reinterpret_cast<f32x4*>(&gates)[threadIdx.x] = gin;
+    gin.store(gates);
     __syncthreads();
     if (!STATE && cols && (n % kDeltaMarks == kDeltaMarks - 1 || n == alive - 1)) {  // <state, D> here, for dg
       const long at = ((long)bh * a.marks + n / kDeltaMarks) * tiles + j / 16;

@@ -167,7 +167,7 @@ enum { INFER = 0, TRAIN = 1, STATE = 2 };
 // and past the value columns its transition where another follows or, for the backward's chain, precedes.
 // (The state pass alone leaves the order of its LDS reads to the compiler: in half the registers two workgroups fit a CU.)
 template <typename E, int DK, int NW, int MODE>
-__global__ __launch_bounds__(64 * NW, MODE == STATE && sizeof(E) == 2 && NW == 8 ? 4 : 1) void delta_fwd_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(64 * NW, MODE == STATE && NW == 8 && sizeof(E) == 2 ? 4 : 1) void delta_fwd_kernel(DeltaArgs a) {
   constexpr int NT = 64 * NW, CB = DK / 16, CP = DK / 32, CW = 16 * NW, PARTS = Num<E>::PARTS;
   constexpr int FINE = MODE == TRAIN && PARTS == 2 ? 3 : PARTS, PP = MODE == TRAIN ? PARTS : 1;  // parts of W, of P
   typedef Tile<E, DK> K;
@@ -211,10 +211,11 @@ __global__ __launch_bounds__(64 * NW, MODE == STATE && sizeof(E) == 2 && NW == 8
   const E* tp = (const E*)a.solve + (long)bh * a.N * C * C;
   const float* gp = a.gates + (long)bh * a.N * kDeltaGates;
   const long plane = (long)a.B * a.H * a.N * C * C;
-  TileIn<E, C, DK, NT> kin, qin;
-  TileIn<E, C, CW, NT> vin{};
-  TileIn<E, C, C, NT> tin[PARTS];
-  f32x4 gin = zero4();
+  constexpr bool TIGHT = MODE == STATE && NW == 8 && PARTS == 2;
+  TileIn<E, C, DK, NT, TIGHT> kin, qin;
+  TileIn<E, C, CW, NT, TIGHT> vin{};
+  TileIn<E, C, C, NT, TIGHT> tin[PARTS];
+  GateIn<NT> gin;
   const auto load = [&](int n) {
     const long t0 = (long)n * C;
     const int left = len - n * C;
@@ -223,7 +224,7 @@ __global__ __launch_bounds__(64 * NW, MODE == STATE && sizeof(E) == 2 && NW == 8
     if (!transition) vin.load(vp + t0 * a.vs.t, a.vs.t, left, a.dvr - col0);
 #pragma unroll
     for (int part = 0; part < PARTS; ++part) tin[part].load(tp + part * plane + (long)n * C * C, C, C, C);
-    gin = reinterpret_cast<const f32x4*>(gp + (long)n * kDeltaGates)[threadIdx.x % (kDeltaGates / 4)];
+    gin.load(gp + (long)n * kDeltaGates);
   };
   if (first < end) load(first);
   for (int n = first; n < end; ++n) {
@@ -234,7 +235,7 @@ __global__ __launch_bounds__(64 * NW, MODE == STATE && sizeof(E) == 2 && NW == 8
     vin.store(Vs, transition ? 0 : left, a.dvr - col0);
 #pragma unroll
     for (int part = 0; part < PARTS; ++part) tin[part].store(Ts[part], C, C);
-    if (threadIdx.x < kDeltaGates / 4) reinterpret_cast<f32x4*>(&gates)[threadIdx.x] = gin;
+    gin.store(gates);
     __syncthreads();
     if (n + 1 < end) load(n + 1);
     // (the lane's number anew in every phase: the LDS addresses formed from it would not fit the registers all at once)
