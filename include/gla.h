@@ -504,8 +504,8 @@ gla_status gla_join_bwd(const void* y, const gla_strides* y_st, const void* z, c
 
 /*
  * gla_delta_workspace_size -- bytes of device workspace gla_delta_fwd (which == GLA_FWD) or gla_delta_bwd (GLA_BWD)
- * needs; gla_delta_saved_size -- bytes of the buffer a training forward fills for its backward (about 8 (dk + 2 dv)
- * bytes a token and head in bf16).  0, with gla_last_error() set, if the sizes are rejected.  Both buffers lie on 16
+ * needs; gla_delta_saved_size -- bytes of the buffer a training forward fills for its backward (in bf16 about
+ * 6 dv + dk dv / 21 + 280 a token and head).  0, with gla_last_error() set, if the sizes are rejected.  Both buffers lie on 16
  * bytes.  The workspace is written before it is read and must not be shared by calls that may run at the same time.
  */
 size_t gla_delta_workspace_size(int which, int B, int H, int Hk, int T, int dk, int dv, int dtype);

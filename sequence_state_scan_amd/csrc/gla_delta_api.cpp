@@ -131,7 +131,7 @@ gla_status check_delta(const char* fn, int B, int H, int Hk, int T, int dk, int 
   GLA_TRY(check_dtype(fn, dtype));
   if (dk > gla::kDeltaMaxDk || dv > gla::kDeltaMaxDv)
     return set_error(GLA_ERR_UNSUPPORTED, "%s: dk=%d or dv=%d is above %d, %d", fn, dk, dv, gla::kDeltaMaxDk, gla::kDeltaMaxDv);
-  // a workgroup a chunk of a head, and in the walk one of at least 8 chunks and 64 columns or a head's only one
+  // a workgroup a chunk of a head; in the walk at most 256 of segments, or 16 a head (64 columns each)
   const long long heads = (long long)B * H, chunks = ((long long)T + gla::kDeltaChunk - 1) / gla::kDeltaChunk;
   if (heads > kMaxGrid / 16 || heads * chunks > kMaxGrid)
     return set_error(GLA_ERR_UNSUPPORTED, "%s: B*H=%lld heads of T=%d tokens are too many for one call", fn, heads, T);

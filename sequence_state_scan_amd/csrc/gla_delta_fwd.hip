@@ -9,6 +9,12 @@
 // A sequence of too few heads to fill the chip is cut into P segments: a state pass finds each segment's own end
 // state from zero and its transition M (the same walk from the identity with V = 0), delta_scan_kernel chains
 // S <- M S + S_own, and the walk then starts from the true states.
+// What bounds it: a chunk's steps follow one another, so a CU's 8 waves share their time between the vector ALU (half of
+// the cycles: the splits, the scaling of states and errors, the decays), the matrix cores (28 %) and LDS (35 %); a training
+// walk also writes 115 KB a chunk and 128 columns and runs at HBM's rate, 4.6 TB/s.  bf16, 4 heads of 64k tokens, 128 x 256,
+// P = 32: gates and inverses 46 us, state pass 186, chain 39, walk 190, where q, k, v and o are 83 us of HBM.  P formed once
+// in delta_prep_kernel and loaded by the walks takes 184 of the walk and 61 of the other; 32 columns a wave or half the
+// waves, two workgroups a CU, take as long as these.
 #include "gla_delta.hpp"
 #include "gla_delta_scan.hpp"
 
@@ -31,6 +37,8 @@ __global__ __launch_bounds__(256) void delta_pack_kernel(const E* from, Strides 
 // (I + L)^-1 of a unit lower triangular 64 x 64 matrix in float32: its 16 x 16 diagonal blocks by forward
 // substitution, a column a lane, then joined two and two, X21 = -X22 L21 X11, on the float32 matrix instructions.
 // Two of them at once: L = B beta (columns scaled) and, transposed at the end, L = beta B for the backward.
+// Bound by what it writes (4096 chunks, 128 channels, bf16: 46 us, 3.1 TB/s; with the second inverse 58 us, 3.6 TB/s), and
+// where there are few chunks by the substitution's 16 steps (7 us).
 template <typename E, int DK, bool TRAIN>
 __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
   constexpr int LF = 66;
@@ -165,7 +173,8 @@ enum { INFER = 0, TRAIN = 1, STATE = 2 };
 
 // Workgroup: one segment and 16 NW columns.  STATE: the segment's own end state where another follows,
 // and past the value columns its transition where another follows or, for the backward's chain, precedes.
-// (The state pass alone leaves the order of its LDS reads to the compiler: in half the registers two workgroups fit a CU.)
+// (The state pass alone leaves the order of its LDS reads to the compiler: in half the registers two workgroups fit a CU:
+// 193 us of 4 heads of 64k, 128 x 256, where one with its reads in order takes 210.)
 template <typename E, int DK, int NW, int MODE>
 __global__ __launch_bounds__(64 * NW, MODE == STATE && NW == 8 && sizeof(E) == 2 ? 4 : 1) void delta_fwd_kernel(DeltaArgs a) {
   constexpr int NT = 64 * NW, CB = DK / 16, CP = DK / 32, CW = 16 * NW, PARTS = Num<E>::PARTS;
