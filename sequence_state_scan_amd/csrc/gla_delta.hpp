@@ -43,15 +43,15 @@ struct DeltaArgs : DeltaShape {
   float* err;     // [4][64][4]: delta, see rows_at
   short* o_rest;  // [4][64][4]: what o's rounding left (bf16; see rest_of), lane 16 (c / 4) + r % 16 of tile r / 16
   void* state0;   // [DKP / 32][64][8]: the state entering a chunk, in dtype, lane 16 (channel / 8 % 4) + column
-  float* mark;    // [BH][marks][DVP / 16][DKP / 16][256]: the state leaving every fourth chunk
+  float* mark;    // [BH][1 + marks][DVP / 16][DKP / 16][256]: the first state, the states leaving every fourth chunk
   // scratch
   void* solve;    // [BH][N][64][64]: (I + B beta)^-1
   void* trans_rows;  // a segment's transition, not transposed (as trans)
   float *seg, *seg_in;  // [BH][P][DVP / 16][DKP / 16][256]: a segment's own end state, the state entering it
   float* z;       // as err
   void* grad1;    // the gradient of the state leaving a chunk, as state0
-  float* carry;   // [BH][marks][DVP / 16]: <state, its gradient> at the marks
-  float* at;      // [BH][N * 64]: o . do - v . dv
+  float* carry;   // [BH][1 + marks][DVP / 16]: <state, its gradient> there
+  float* at;      // [BH][N * 64][2]: o . do - v . dv; the sum of its terms' sizes
   float *dq_heads, *dk_heads;  // [B][H][T][dk], where heads share keys
   void *qk_packed, *v_packed;  // q and k, v (and do), with rows of dkr, dvr elements, where dk, dv are no such numbers
 };

@@ -69,7 +69,7 @@ size_t place_saved(DeltaArgs& a, char* p) {
   r.take(a.err, chunks * kDeltaChunk * a.DVP * 4);
   if (a.dtype == GLA_BF16) r.take(a.o_rest, chunks * kDeltaChunk * a.DVP * 2);
   r.take(a.state0, chunks * a.DVP * a.DKP * e);
-  r.take(a.mark, heads * a.marks * a.DVP * a.DKP * 4);
+  r.take(a.mark, heads * (a.marks + 1) * a.DVP * a.DKP * 4);
   return r.used;
 }
 
@@ -94,8 +94,8 @@ size_t place_scratch(DeltaArgs& a, char* p, bool backward, bool train) {
   }
   r.take(a.z, chunks * kDeltaChunk * a.DVP * 4);
   r.take(a.grad1, chunks * a.DVP * a.DKP * e);
-  r.take(a.carry, heads * a.marks * (a.DVP / 16) * 4);
-  r.take(a.at, chunks * kDeltaChunk * 4);
+  r.take(a.carry, heads * (a.marks + 1) * (a.DVP / 16) * 4);
+  r.take(a.at, chunks * kDeltaChunk * 8);
   if (a.H != a.Hk) {
     r.take(a.dq_heads, heads * a.T * a.dk * 4);
     r.take(a.dk_heads, heads * a.T * a.dk * 4);

@@ -213,6 +213,7 @@ __global__ __launch_bounds__(64 * NW, MODE == STATE && NW == 8 && sizeof(E) == 2
     load_state<CB>(S, a.h0 ? a.h0 + (long)bh * a.dk * a.dv : nullptr, a.dk, a.dv, j + n16);
   }
   arrived<CB>(S);
+  if (MODE == TRAIN && cols && seg == 0) store_regs<CB>(S, a.mark + ((long)bh * (a.marks + 1) * tiles + j / 16) * DK * 16);
 
   const E* kp = (const E*)a.k + b * a.ks.b + hk * a.ks.h;
   const E* qp = (const E*)a.q + b * a.qs.b + hk * a.qs.h;
@@ -402,7 +403,7 @@ __global__ __launch_bounds__(64 * NW, MODE == STATE && NW == 8 && sizeof(E) == 2
       }
     }
     if (MODE == TRAIN && cols && (n % kDeltaMarks == kDeltaMarks - 1 || n == alive - 1))
-      store_regs<CB>(S, a.mark + (((long)bh * a.marks + n / kDeltaMarks) * tiles + j / 16) * DK * 16);
+      store_regs<CB>(S, a.mark + (((long)bh * (a.marks + 1) + n / kDeltaMarks + 1) * tiles + j / 16) * DK * 16);
   }
   if (!cols) return;
   if (MODE == STATE) {

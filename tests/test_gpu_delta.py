@@ -199,6 +199,19 @@ def test_delta_segments(T, dk, dv, dt):
     check(x, lens=torch.tensor([T - 517, 400]), label="segments, lens")
 
 
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("T,dk,dv", [(40, 16, 16), (4400, 16, 16), (700, 128, 100)])
+def test_delta_first_gate(T, dk, dv, dt):
+    # the first gate scales h0, so its gradient is <h0, dh0> whatever the tokens after it add up to: sums of dk / 4 products a
+    # lane, six exchanges, a number per 16 columns, and four roundings of the result
+    c = on_gpu(inputs(T, 2, 2, 2, T, dk, dv, dt))
+    got = call(c)
+    terms = c["h0"].double() * got["dh0"].double()
+    steps = max(32, 1 << (dk - 1).bit_length()) / 4 + 6 + math.ceil(dv / 16) + 4
+    off = (got["dg"][:, :, 0].double() - terms.sum((-1, -2))).abs()
+    assert bool((off <= steps * 2.0 ** -24 * terms.abs().sum((-1, -2))).all())
+
+
 def test_delta_without_the_optional_tensors():
     x = inputs(5, 2, 2, 2, 150, 40, 30, F32)
     x["h0"] = x["dhT"] = None
