@@ -561,6 +561,24 @@ def test_offsets_past_32_bits():
     assert torch.equal(a["normed"], b["normed"])
 
 
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_token_strides_of_a_million(dt):
+    # tokens so far apart that a tile's rows are no 32-bit offsets from one base
+    T, dk, dv, far = 200, 32, 40, (1 << 20) + 24
+    x = on_gpu(inputs(4, 1, 1, 1, T, dk, dv, dt))
+    pool, gates = torch.empty(T * far, dtype=dt, device="cuda"), torch.empty(T * far, device="cuda")
+    c = dict(x)
+    for i, n in enumerate(("q", "k", "v", "do")):
+        c[n] = pool.as_strided(x[n].shape, (T * far, T * far, far, 1), i * 64)
+        c[n].copy_(x[n])
+    for i, n in enumerate(("g", "beta")):
+        c[n] = gates.as_strided(x[n].shape, (T * far, T * far, far), i)
+        c[n].copy_(x[n])
+    want, got = call(x), call(c)
+    for n in want:
+        assert torch.equal(want[n], got[n]), n
+
+
 def test_a_block_of_them_together():
     # norm, projections, the rule, and the join with the residual stream: values and the weights' gradients against
     # autograd of the same block in float64
