@@ -504,7 +504,7 @@ __global__ __launch_bounds__(256) void delta_gate_grad_kernel(DeltaArgs a) {
       whole += red[1][w];
     }
     off = before - off;
-    if (whole > 0.f && whole < __builtin_inff()) s = fmaf(off, size / whole, s);
+    if (whole > 0.f && whole < __builtin_inff() && fabsf(off) < __builtin_inff()) s = fmaf(off, size / whole, s);
     if (decay(g) != 0.f) dg = s;  // a decay of exactly zero has no slope
   }
   a.dg[(long)bh * a.T + t] = dg;
