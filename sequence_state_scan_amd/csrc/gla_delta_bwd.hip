@@ -4,7 +4,7 @@
 //   D0 = e^gamma_C D1 + (e^gamma Q)^T dO - (e^gamma K)^T dV
 //   dQ = e^gamma dO S0^T + H K,   H = (dO W^T) . E on and below the diagonal
 //   dK = H^T Q + (G + G^T) K - e^gamma dV S0^T + e^(gamma_C - gamma) W D1^T,   G = -(dV W^T) . E below it
-//   dg_t = sum from the token on of (o . do - v . dv) + <S, D> at a later chunk's end
+//   dg_t = sum from the token on of (o . do - v . dv) + <S, D> at a later chunk's end, both up to the next reset
 // (scaling a decay scales what the states before it give to the later outputs, and those are linear in v).
 // delta_bwd_kernel walks a segment's chunks from its end, D in accumulators as the forward holds S; what it leaves
 // (z, D1) lets delta_grad_kernel form every chunk's gradients on its own.  Segments as in the forward, with the
@@ -460,52 +460,75 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a) {
   }
 }
 
-// dg: the sums of `at` from a token to the next mark (256 tokens a workgroup), and <S, D> there.  The whole span's sum has
-// to come out as <S, D> at the mark before; what it is off by is the errors' sum, and goes back to the tokens by the sizes
-// of their terms.  That leaves the largest error in the middle of a span instead of a larger one at its start (bf16, 16 x 16:
-// dg 7e-6 off instead of 1.1e-5; a mark every chunk 6.5e-6).
+// dg: the sums of `at` from a token to the next reset, where they end in zero, or to the next mark (256 tokens a workgroup),
+// where they end in <S, D>.  A run of tokens between resets and marks has to sum up to what is known of its start, too:
+// <S, D> at the mark before, or zero at a reset.  What it is off by is the errors' sum, and goes back to the run's tokens by
+// the sizes of their terms.  That leaves the largest error in the middle of a run instead of a larger one at its start (bf16,
+// 16 x 16: dg 7e-6 off instead of 1.1e-5; a mark every chunk 6.5e-6), and nothing of one document in another's dg.
 __global__ __launch_bounds__(256) void delta_gate_grad_kernel(DeltaArgs a) {
   constexpr int SPAN = C * kDeltaMarks;
   static_assert(SPAN == 256, "a lane a token");
   const int m = blockIdx.x % a.marks, bh = blockIdx.x / a.marks, b = bh / a.H, h = bh - b * a.H;
   const int len = length_of(a, b), lane = lane_id(), wave = wave_id();
   const long t = (long)m * SPAN + threadIdx.x;
-  __shared__ float red[2][4];
+  __shared__ float first[2][4], total[2][SPAN];  // the sums (of `at`, of sizes) from a wave's first token; from every token
+  __shared__ unsigned long long starts[4];       // a wave's resets
   float2 x = make_float2(0.f, 0.f);
-  if (t < len) x = *reinterpret_cast<const float2*>(a.at + 2 * ((long)bh * a.N * C + t));
+  bool reset = false;
+  if (t < len) {
+    x = *reinterpret_cast<const float2*>(a.at + 2 * ((long)bh * a.N * C + t));
+    reset = decay(a.g[b * a.gs.b + h * a.gs.h + t * a.gs.t]) == 0.f;
+  }
+  const unsigned long long here = __ballot(reset);
+  const unsigned long long after = lane < 63 ? here >> (lane + 1) : 0;
+  const int end = after ? lane + __ffsll((long long)after) : 64;  // of the lane's run, in its wave
   for (int o = 1; o < 64; o *= 2) {
     const float y = __shfl_down(x.x, o), size = __shfl_down(x.y, o);
-    if (lane + o < 64) {
+    if (lane + o < end) {
       x.x += y;
       x.y += size;
     }
   }
   if (lane == 0) {
-    red[0][wave] = x.x;
-    red[1][wave] = x.y;
+    first[0][wave] = x.x;
+    first[1][wave] = x.y;
+    starts[wave] = here;
+  }
+  __syncthreads();
+  const float* c = a.carry + ((long)bh * (a.marks + 1) + m) * (a.DVP / 16);
+  float before = 0.f, s = 0.f, size = 0.f;
+  if (t < len) {
+    float off = 0.f, whole = 0.f;  // from behind a wave to its last run's end
+    for (int i = 0; i < a.DVP / 16; ++i) {
+      before += c[i];
+      off += c[a.DVP / 16 + i];
+    }
+    for (int w = 3; w > wave; --w) {
+      const unsigned long long r = starts[w];
+      off = r & 1 ? 0.f : r ? first[0][w] : off + first[0][w];
+      whole = r & 1 ? 0.f : r ? first[1][w] : whole + first[1][w];
+    }
+    s = end < 64 ? x.x : off + x.x;
+    size = end < 64 ? x.y : whole + x.y;
+    total[0][threadIdx.x] = s;
+    total[1][threadIdx.x] = size;
   }
   __syncthreads();
   if (t >= a.T) return;
   float dg = 0.f;
   if (t < len) {
-    const float g = a.g[b * a.gs.b + h * a.gs.h + t * a.gs.t];
-    const float* c = a.carry + ((long)bh * (a.marks + 1) + m) * (a.DVP / 16);
-    float before = 0.f, s = 0.f, size = 0.f, off = 0.f, whole = 0.f;
-    for (int i = 0; i < a.DVP / 16; ++i) {
-      before += c[i];
-      off += c[a.DVP / 16 + i];
+    int from = 0;  // the run's first token
+    const unsigned long long upto = here & (~0ull >> (63 - lane));
+    if (upto) {
+      from = 64 * wave + 63 - __clzll((long long)upto);
+    } else {
+      for (int w = wave - 1; w >= 0 && !from; --w)
+        if (starts[w]) from = 64 * w + 63 - __clzll((long long)starts[w]);
     }
-    for (int w = 3; w >= 0; --w) {
-      if (w == wave) {
-        s = off + x.x;
-        size = whole + x.y;
-      }
-      off += red[0][w];
-      whole += red[1][w];
-    }
-    off = before - off;
+    if (starts[from >> 6] >> (from & 63) & 1) before = 0.f;
+    const float off = before - total[0][from], whole = total[1][from];
     if (whole > 0.f && whole < __builtin_inff() && fabsf(off) < __builtin_inff()) s = fmaf(off, size / whole, s);
-    if (decay(g) != 0.f) dg = s;  // a decay of exactly zero has no slope
+    if (!reset) dg = s;  // a decay of exactly zero has no slope
   }
   a.dg[(long)bh * a.T + t] = dg;
 }
