@@ -493,7 +493,9 @@ gla_status gla_join_bwd(const void* y, const gla_strides* y_st, const void* z, c
  * (float32).  The conventions of the section above hold; a stride of g and beta's last dimension is given too (their
  * gla_strides name all three), so that a [B][T][H] projection can be passed as it stands.
  *   - g is finite and <= 0, or -inf (a reset: the token starts from no state).  beta, and everything else, is finite.
- *     A rule that is to stay bounded wants |k| <= 1 and 0 <= beta <= 2; nothing here relies on it.
+ *     A rule that is to stay bounded wants |k| <= 1 and 0 <= beta <= 2; nothing here relies on it.  What is not finite all
+ *     the same shows: a gate that is NaN leaves NaN in its head's results from its token on (in the chunked calls from its
+ *     chunk of 64 tokens on) and in the gradients before it.
  *   - lens: int32 [B] or NULL: sequence b has lens[b] tokens (limited to 0..T).  What stands behind is ignored whatever
  *     it holds; outputs there are zero.
  *   - States, errors and the float32 results are computed to float32's accuracy also beside bf16 inputs (split operands

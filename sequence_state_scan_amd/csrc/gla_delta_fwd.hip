@@ -59,8 +59,9 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
   if (wave == 0) {
     const long t = t0 + lane;
     const bool live = t < len;
-    // below -200 every decay over the token is an exact zero
-    double x = live ? fmaxf(a.g[b * a.gs.b + h * a.gs.h + t * a.gs.t], -200.f) : 0.f;
+    // below -200 every decay over the token is an exact zero; NaN (which a maximum would drop) stays
+    const float g = live ? a.g[b * a.gs.b + h * a.gs.h + t * a.gs.t] : 0.f;
+    double x = g < -200.f ? -200.f : g;
     const float beta = live ? a.beta[b * a.bs.b + h * a.bs.h + t * a.bs.t] : 0.f;
 #pragma unroll
     for (int o = 1; o < 64; o *= 2) {
