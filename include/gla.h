@@ -495,7 +495,9 @@ gla_status gla_join_bwd(const void* y, const gla_strides* y_st, const void* z, c
  *   - g is finite and <= 0, or -inf (a reset: the token starts from no state).  beta, and everything else, is finite.
  *     A rule that is to stay bounded wants |k| <= 1 and 0 <= beta <= 2; nothing here relies on it.  What is not finite all
  *     the same shows: a gate that is NaN leaves NaN in its head's results from its token on (in the chunked calls from its
- *     chunk of 64 tokens on) and in the gradients before it.
+ *     chunk of 64 tokens on) and in the gradients before it.  A reset at a sequence's first token drops h0 whatever it holds
+ *     (a state of a pool that is used again), and in gla_delta_step every reset drops the state so; a later reset in the
+ *     chunked calls multiplies the state by zero, which keeps one that has overflowed.
  *   - lens: int32 [B] or NULL: sequence b has lens[b] tokens (limited to 0..T).  What stands behind is ignored whatever
  *     it holds; outputs there are zero.
  *   - States, errors and the float32 results are computed to float32's accuracy also beside bf16 inputs (split operands

@@ -467,6 +467,12 @@ __device__ __forceinline__ int length_of(const DeltaArgs& a, int b) {
   return n < 0 ? 0 : n > a.T ? a.T : n;
 }
 
+// Whether a sequence starts from no state although there is an h0: its first token is a reset, which drops a state whatever
+// it holds (a product with a decay of zero would keep what is not finite).
+__device__ __forceinline__ bool starts_anew(const DeltaArgs& a, int b, int h, int alive) {
+  return a.h0 && alive > 0 && decay(a.g[b * a.gs.b + h * a.gs.h]) == 0.f;
+}
+
 // Row-major [dk][dv] states in an accumulator: lane's rows row4_of(cb, g4) + i, column j + n16.
 template <int CB>
 __device__ __forceinline__ void load_state(f32x4 (&S)[CB], const float* p, int dk, int dv, int col) {

@@ -212,6 +212,9 @@ __global__ __launch_bounds__(64 * NW, MODE == STATE && NW == 8 && sizeof(E) == 2
     if (cols && (seg == 0 || first < alive)) load_regs<CB>(S, a.seg_in + (((long)bh * a.P + seg) * tiles + j / 16) * DK * 16);
   } else {
     load_state<CB>(S, a.h0 ? a.h0 + (long)bh * a.dk * a.dv : nullptr, a.dk, a.dv, j + n16);
+    if (starts_anew(a, b, h, alive))
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb) S[cb] = zero4();
   }
   arrived<CB>(S);
   if (MODE == TRAIN && cols && seg == 0) store_regs<CB>(S, a.mark + ((long)bh * (a.marks + 1) * tiles + j / 16) * DK * 16);

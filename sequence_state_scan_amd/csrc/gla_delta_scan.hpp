@@ -33,6 +33,9 @@ __global__ __launch_bounds__(4 * DK) void delta_scan_kernel(DeltaArgs a) {
       const int col = min(j0 + 16 * c, a.DVP - 16) + n16;
       S[c][i] = from && r0 + i < a.dk && col < a.dv ? from[((long)bh * a.dk + r0 + i) * a.dv + col] : 0.f;
     }
+  if (!BWD && starts_anew(a, b, bh - b * a.H, alive))
+#pragma unroll
+    for (int c = 0; c < COLS; ++c) S[c] = zero4();
   arrived<COLS>(S);
   const auto load = [&](int step, Split<E> (&m)[CP], f32x4 (&o)[COLS]) {  // every step loads, the last ones again
     const int at = min(step, steps - 1), seg = BWD ? steps - at : at;
