@@ -518,7 +518,8 @@ size_t gla_delta_saved_size(int B, int H, int Hk, int T, int dk, int dv, int dty
 /*
  * gla_delta_fwd -- o, and h_final (the state after the last token, h0 for an empty sequence; may be NULL), from h0
  * (NULL = 0).  saved: NULL in a forward-only call, else gla_delta_saved_size bytes for gla_delta_bwd (a private layout;
- * a forward-only call rounds o's operands to bf16, so its o may differ from a training one's in the last place).
+ * a training call splits some operands finer for the gradients' sake, so its o may differ from a forward-only one's in the
+ * last place).
  * Results do not depend on the timing of the run, bit for bit.
  */
 gla_status gla_delta_fwd(const void* q, const gla_strides* q_st, const void* k, const gla_strides* k_st, const void* v,

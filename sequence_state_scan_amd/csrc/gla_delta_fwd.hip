@@ -179,7 +179,7 @@ enum { INFER = 0, TRAIN = 1, STATE = 2 };
 template <typename E, int DK, int NW, int MODE>
 __global__ __launch_bounds__(64 * NW, MODE == STATE && NW == 8 && sizeof(E) == 2 ? 4 : 1) void delta_fwd_kernel(DeltaArgs a) {
   constexpr int NT = 64 * NW, CB = DK / 16, CP = DK / 32, CW = 16 * NW, PARTS = Num<E>::PARTS;
-  constexpr int FINE = MODE == TRAIN && PARTS == 2 ? 3 : PARTS, PP = MODE == TRAIN ? PARTS : 1;  // parts of W, of P
+  constexpr int FINE = MODE == TRAIN && PARTS == 2 ? 3 : PARTS;  // parts of W in o, and of Y
   typedef Tile<E, DK> K;
   typedef Tile<E, CW> V;
   typedef Tile<E, C> M;
@@ -256,8 +256,7 @@ __global__ __launch_bounds__(64 * NW, MODE == STATE && NW == 8 && sizeof(E) == 2
     const int lane = fresh_tid() & 63, n16 = lane & 15, g4 = lane >> 4, k8 = 8 * g4;
     ScoreTiles<E, DK, NW, false> P;
     if constexpr (MODE != STATE) P.form(Qs, Ks, gates, wave, n16, g4);
-    // K S0 and Q S0 (transposed: a lane has four columns of one token).  A forward-only call rounds the state, W and P to
-    // one bf16 for o, which is rounded to it after all.
+    // K S0 and Q S0 (transposed: a lane has four columns of one token)
     f32x4 Y[4], W[4], O[4];
     {
       Split<E, 1> kf[2][4], qf[2][4];
@@ -279,8 +278,7 @@ __global__ __launch_bounds__(64 * NW, MODE == STATE && NW == 8 && sizeof(E) == 2
         if (p + 1 < CP) fetch(p + 1);
         if constexpr (MODE != STATE) batch<E>();
         mma_tiles<E, 0, 4>(Y, kf[p & 1], So);
-        if constexpr (MODE == TRAIN) mma_tiles<E, 0, 4, 1, PARTS, 4, true>(O, qf[p & 1], So);
-        if constexpr (MODE == INFER) mma_tiles<E, 0, 4, 1, 1, 4, true>(O, qf[p & 1], Split<E, 1>{{So.part[0]}});
+        if constexpr (MODE != STATE) mma_tiles<E, 0, 4, 1, PARTS, 4, true>(O, qf[p & 1], So);
         if constexpr (MODE != STATE) batch<E>();
       }
     }
@@ -337,24 +335,19 @@ __global__ __launch_bounds__(64 * NW, MODE == STATE && NW == 8 && sizeof(E) == 2
 #pragma unroll
         for (int i = 0; i < 4; ++i) O[t][i] *= leads[t];
       __syncthreads();
-      P.put(Ts, PP, wave, n16, g4);
+      P.put(Ts, PARTS, wave, n16, g4);
       __syncthreads();
       const int lane = fresh_tid() & 63, n16 = lane & 15, g4 = lane >> 4, k8 = 8 * g4;
-      Split<E, PP> Pf[2][4];
+      Split<E> Pf[2][4];
 #pragma unroll
       for (int p = 0; p < 2; ++p)
 #pragma unroll
         for (int t = 2 * p; t < 4; ++t)
 #pragma unroll
-          for (int part = 0; part < PP; ++part) Pf[p][t].part[part] = M::row(Ts[part], 16 * t + n16, 32 * p + k8);
+          for (int part = 0; part < PARTS; ++part) Pf[p][t].part[part] = M::row(Ts[part], 16 * t + n16, 32 * p + k8);
       if constexpr (MODE != STATE) batch<E>();
-      if constexpr (MODE == TRAIN) {
-        mma_tiles<E, 0, 4, PP, FINE, 4, true>(O, Pf[0], Wo[0]);
-        mma_tiles<E, 2, 4, PP, FINE, 4, true>(O, Pf[1], Wo[1]);
-      } else {
-        mma_tiles<E, 0, 4, 1, 1, 4, true>(O, Pf[0], Split<E, 1>{{Wo[0].part[0]}});
-        mma_tiles<E, 2, 4, 1, 1, 4, true>(O, Pf[1], Split<E, 1>{{Wo[1].part[0]}});
-      }
+      mma_tiles<E, 0, 4, PARTS, FINE, 4, true>(O, Pf[0], Wo[0]);
+      mma_tiles<E, 2, 4, PARTS, FINE, 4, true>(O, Pf[1], Wo[1]);
     }
     {
       const int lane = fresh_tid() & 63, n16 = lane & 15, g4 = lane >> 4;
