@@ -33,8 +33,7 @@ struct DeltaArgs : DeltaShape {
   const float* dhT;
   void *dq, *dk_, *dv_;
   float *dg, *dbeta, *dh0;
-  // saved by a training forward for the backward (null in a forward-only call), but for trans and gates, which are
-  // scratch there
+  // saved by a training forward for the backward (null in a forward-only call, but for the gates, which are scratch there)
   float* gates;   // [BH][N][5][64]
   void* solveT;   // [BH][N][64][64]: (I + beta B)^-1, transposed (bf16: the high parts, then the low parts)
   void* trans;    // [BH][P]: a segment's transition M, transposed, in operands' order (frag_at; bf16: high, then low parts)

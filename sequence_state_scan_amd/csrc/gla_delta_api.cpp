@@ -86,10 +86,7 @@ size_t place_scratch(DeltaArgs& a, char* p, bool backward, bool train) {
   if (!backward) {
     r.take(a.solve, chunks * kDeltaChunk * kDeltaChunk * kFull);
     if (a.P > 1) r.take(a.trans_rows, heads * a.P * a.DKP * a.DKP * kFull);
-    if (!train) {
-      r.take(a.gates, chunks * kDeltaGates * 4);
-      if (a.P > 1) r.take(a.trans, heads * a.P * a.DKP * a.DKP * kFull);
-    }
+    if (!train) r.take(a.gates, chunks * kDeltaGates * 4);
     return r.used;
   }
   r.take(a.z, chunks * kDeltaChunk * a.DVP * 4);

@@ -409,12 +409,14 @@ __global__ __launch_bounds__(64 * NW, MODE == STATE && NW == 8 && sizeof(E) == 2
       return;
     }
     const long block = ((long)bh * a.P + seg) * DK * DK, mplane = (long)a.B * a.H * a.P * DK * DK;
-    E* to = (E*)a.trans + block;
+    if (chained) {  // (only the backward's chain reads it)
+      E* to = (E*)a.trans + block;
 #pragma unroll
-    for (int p = 0; p < CP; ++p) {
-      const Split<E> s = split<E>(S[2 * p], S[2 * p + 1]);
+      for (int p = 0; p < CP; ++p) {
+        const Split<E> s = split<E>(S[2 * p], S[2 * p + 1]);
 #pragma unroll
-      for (int part = 0; part < PARTS; ++part) *reinterpret_cast<Frag<E>*>(to + part * mplane + frag_at<DK>(j + n16, 4 * p + g4)) = s.part[part];
+        for (int part = 0; part < PARTS; ++part) *reinterpret_cast<Frag<E>*>(to + part * mplane + frag_at<DK>(j + n16, 4 * p + g4)) = s.part[part];
+      }
     }
     const int c = j + 4 * (n16 >> 2);
     E* by_rows = (E*)a.trans_rows + block + (c & 7);
