@@ -8,11 +8,13 @@
 // (scaling a decay scales what the states before it give to the later outputs, and those are linear in v).
 // delta_bwd_kernel walks a segment's chunks from its end, D in accumulators as the forward holds S; what it leaves
 // (z, D1) lets delta_grad_kernel form every chunk's gradients on its own.  Segments as in the forward, with the
-// forward's transitions.  The float32 results (dg, dbeta, dh0) come from split operands throughout; the products
-// that only go into dq and dk round the states, z and W to one bf16 each, as those are rounded themselves.
-// What bounds it: HBM.  bf16, 16 heads of 16384 tokens, 128 x 128, P = 16: state pass 110 us, chain 31, walk 137 (628 MB, 4.6
-// TB/s), delta_grad_kernel 283 (1148 MB, 4.0 TB/s), dg 4.5; in the forward gates and inverses 58, state pass 106, chain 22,
-// walk 159 (762 MB, 4.8 TB/s).
+// forward's transitions.  Operands are split as in the forward; only the state entering a chunk and the gradient leaving it,
+// which pass through memory, are one bf16 each in dq and dk, as those are rounded themselves: dq and dk are 1.78e-3 off in the
+// 2-norm where their own rounding is 1.66e-3, up to 2.3e-3 where hardly anything decays (with W, dV, H and G one bf16 too 2.9e-3,
+// for 27 us less of the gradients' 314; the states' second parts would be another 0.5 of 3.0 GB).
+// What bounds it: HBM.  bf16, 16 heads of 16384 tokens, 128 x 128, P = 16, kernels traced one by one (954 us in all, where a
+// call of both directions takes 910 in a row): state pass 112 us, chain 31, walk 140 (628 MB, 4.5 TB/s), delta_grad_kernel 314
+// (1148 MB, 3.7 TB/s), dg 6; in the forward gates and inverses 59, state pass 109, chain 23, walk 160 (762 MB, 4.8 TB/s).
 #include "gla_delta.hpp"
 #include "gla_delta_scan.hpp"
 
@@ -228,18 +230,19 @@ __global__ __launch_bounds__(64 * NW) void delta_bwd_kernel(DeltaArgs a) {
 // One chunk's dq, dk, dv, dbeta and the terms of dg.  Waves w and w + 4 have 16 tokens, each half of the channels; one
 // of them forms the tokens' rows of H, the other those of G.  The value columns come in blocks (dO, W, dV by rows, S0
 // and D1 transposed), then K, Q, H and G take their place in LDS.  Products are transposed: a lane has eight channels of
-// one token.  64 columns a block in bf16, 32 in float32 (59 and 104 KB of LDS).
+// one token.  64 columns a block in bf16, 32 in float32 (75 and 104 KB of LDS).
 template <typename E, int DK>
 __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a) {
-  constexpr int NT = 512, CB = DK / 16, CH = CB / 2, CP = DK / 32, BC = sizeof(E) == 2 ? 64 : 32, UPR = BC / 8;
+  constexpr int NT = 512, CB = DK / 16, CH = CB / 2, CP = DK / 32, BC = sizeof(E) == 2 ? 64 : 32, UPR = BC / 8, PARTS = Num<E>::PARTS;
   typedef Tile<E, DK> K;
   typedef Tile<E, BC> V;
   typedef Tile<E, C> M;
-  constexpr int STAGE = 3 * C * V::LD + 2 * BC * K::LD, LATER = 2 * C * K::LD + 2 * C * M::LD;
+  constexpr int STAGE = (1 + 2 * PARTS) * C * V::LD + 2 * BC * K::LD, LATER = 2 * C * K::LD + 2 * PARTS * C * M::LD;
   __shared__ __attribute__((aligned(16))) E lds[STAGE > LATER ? STAGE : LATER];
   __shared__ __attribute__((aligned(16))) GateBlock gates;
-  E *Os = lds, *Ws = Os + C * V::LD, *Ys = Ws + C * V::LD, *S0 = Ys + C * V::LD, *D1 = S0 + BC * K::LD;
-  E *Ks = lds, *Qs = Ks + C * K::LD, *HT = Qs + C * K::LD, *GT = HT + C * M::LD;
+  // (W, dV, and later H and G: PARTS tiles each)
+  E *Os = lds, *Ws = Os + C * V::LD, *Ys = Ws + PARTS * C * V::LD, *S0 = Ys + PARTS * C * V::LD, *D1 = S0 + BC * K::LD;
+  E *Ks = lds, *Qs = Ks + C * K::LD, *HT = Qs + C * K::LD, *GT = HT + PARTS * C * M::LD;
   const int n = blockIdx.x % a.N, bh = blockIdx.x / a.N, b = bh / a.H, h = bh - b * a.H, hk = h / (a.H / a.Hk);
   const int len = length_of(a, b), lane = lane_id(), n16 = lane & 15, g4 = lane >> 4;
   const int wave = wave_id() & 3, half = wave_id() >> 2;  // half: channels CH * 16 half on, and G
@@ -319,7 +322,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a) {
         d = __builtin_shufflevector(load4(a.err + p), load4(a.err + p + 16), 0, 1, 2, 3, 4, 5, 6, 7);
       }
       const float beta = gates.beta[r];
-      v8 w, y, ox;
+      v8 w[PARTS], y[PARTS], ox;
       f32x4 y0, y1;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -335,13 +338,22 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a) {
         size += fabsf(yv * (float)vv[e]);
         db = fmaf(z[e], d[e], db);
         (e < 4 ? y0 : y1)[e & 3] = yv;
-        w[e] = (E)(beta * d[e]);
-        y[e] = (E)yv;
+        float wr = beta * d[e], yr = yv;
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part) {
+          w[part][e] = (E)wr;
+          y[part][e] = (E)yr;
+          wr -= (float)w[part][e];
+          yr -= (float)y[part][e];
+        }
         ox[e] = x[e];
       }
       *reinterpret_cast<v8*>(Os + V::at(r, cc)) = ox;
-      *reinterpret_cast<v8*>(Ws + V::at(r, cc)) = w;
-      *reinterpret_cast<v8*>(Ys + V::at(r, cc)) = y;
+#pragma unroll
+      for (int part = 0; part < PARTS; ++part) {
+        *reinterpret_cast<v8*>(Ws + part * C * V::LD + V::at(r, cc)) = w[part];
+        *reinterpret_cast<v8*>(Ys + part * C * V::LD + V::at(r, cc)) = y[part];
+      }
       if (r < rows && c < a.dv) {
         E* to = (E*)a.dv_ + ((long)bh * a.T + t0 + r) * a.dv + c;
         store4_part<E>(to, y0, a.dv - c);
@@ -360,7 +372,14 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a) {
 #pragma unroll
     for (int p = 0; p < BC / 32; ++p) {
       const int row = 16 * wave + n16, col = 32 * p + 8 * g4;
-      const Frag<E> fo = V::row(Os, row, col), fw = V::row(Ws, row, col), fy = V::row(Ys, row, col);
+      const auto parts = [&](const E* tile, int r) {
+        Split<E> s;
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part) s.part[part] = V::row(tile + part * C * V::LD, r, col);
+        return s;
+      };
+      const Frag<E> fo = V::row(Os, row, col);
+      const Split<E> fw = parts(Ws, row), fy = parts(Ys, row);
 #pragma unroll
       for (int cb = 0; cb < CH; ++cb) {
         const int ch = row4_of(CH * half + cb, 0);
@@ -369,10 +388,12 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a) {
         dS[cb] = mma(s, fy, dS[cb]);
         dK[cb] = mma(K::template col<true>(D1, 32 * p, ch, n16, g4), fw, dK[cb]);
       }
-      const Frag<E> f = half ? fy : fo;
 #pragma unroll
       for (int t = 0; t < 4; ++t)
-        if (t <= wave) H[t] = mma(f, V::row(Ws, 16 * t + n16, col), H[t]);
+        if (t <= wave) {
+          const Split<E> w = parts(Ws, 16 * t + n16);
+          H[t] = half ? mma(fy, w, H[t]) : mma(fo, w, H[t]);
+        }
     }
   }
   TileIn<E, C, DK, NT> kin, qin;
@@ -400,7 +421,12 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a) {
     f32x4 x = half ? decays_to<false>(gates, i0, key) : decays_to<true>(gates, i0, key);
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] *= half ? -H[t][i] : H[t][i];
-    M::put4(half ? GT : HT, key, i0, x);
+#pragma unroll
+    for (int part = 0; part < PARTS; ++part) {
+      M::put4((half ? GT : HT) + part * C * M::LD, key, i0, x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] -= (float)(E)x[i];
+    }
   }
   const int row = 16 * wave + n16;
   const float lead = gates.lead[row], late = gates.late[row];
@@ -415,14 +441,18 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a) {
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
     const bool before = p <= wave / 2, after = p >= wave / 2;  // keys up to the wave's rows, queries from them on
-    Frag<E> hi = {}, gi = {}, hj = {}, gj = {};
-    if (before) {
-      hi = M::template col<false>(HT, 32 * p, 16 * wave, n16, g4);
-      gi = M::template col<false>(GT, 32 * p, 16 * wave, n16, g4);
-    }
-    if (after) {
-      hj = M::row(HT, row, 32 * p + 8 * g4);
-      gj = M::row(GT, row, 32 * p + 8 * g4);
+    Split<E> hi = {}, gi = {}, hj = {}, gj = {};
+#pragma unroll
+    for (int part = 0; part < PARTS; ++part) {
+      const E *h = HT + part * C * M::LD, *g = GT + part * C * M::LD;
+      if (before) {
+        hi.part[part] = M::template col<false>(h, 32 * p, 16 * wave, n16, g4);
+        gi.part[part] = M::template col<false>(g, 32 * p, 16 * wave, n16, g4);
+      }
+      if (after) {
+        hj.part[part] = M::row(h, row, 32 * p + 8 * g4);
+        gj.part[part] = M::row(g, row, 32 * p + 8 * g4);
+      }
     }
 #pragma unroll
     for (int cb = 0; cb < CH; ++cb) {
