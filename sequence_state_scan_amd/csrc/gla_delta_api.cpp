@@ -11,12 +11,16 @@ namespace gla {
 
 // A sequence's chunks are cut into segments where the heads and their column tiles would leave CUs idle.
 // Segments: as many as give each of the 256 CUs a walk of its own, never more than one (200 heads of 2048 tokens in two
-// segments, bf16 128 x 128: forward 366 us, whole 239; 128 heads in two 222, whole 211), and no more than 3 sqrt(N):
-// a segment's two walks of L = N / P chunks take about 6 us a chunk each, the chain between them 1.3 us a segment, so the
-// best P is near 3 sqrt(N) (4 heads of 8192 tokens: P = 128 127 us, 64 (and 3 sqrt(N)) 98, 32 97, 16 110; of 1024, N = 16:
-// P = 16 53, 8 48, 4 57, 1 86).  Two segments' walks take as long as the one whole.
-// Columns: 128 a workgroup, 64 where even then half the CUs have none (float32 6 heads of 333 tokens, 48 x 80: training
-// step 104 us with 128, 92 with 64).
+// segments, bf16 128 x 128: forward 369 us, whole 262; training step 1349 and 1046; 128 heads in two 223 and 846, whole 206 and
+// 786), and no more than 3 sqrt(N): a segment's two walks of L = N / P chunks take about 6 us a chunk each, the chain between
+// them 1.3 us a segment, so the best P is near 3 sqrt(N) (4 heads of 8192 tokens, N = 128: P = 128 201 us, 64 125, 32 (33, in
+// whole chunks) 97, 16 107; of 1024, N = 16: P = 16 51, 8 (12) 46, 4 52, 1 87).  Two segments' walks take as long as the one
+// whole.
+// Columns: 128 a workgroup, 64 where the tiles of 128 and their segments would leave half the CUs or more without a walk (one
+// segment of 2048 tokens, 128 x 128, forward and training step with 64 and with 128: 86 heads, bf16 188 / 647 and 207 / 702 us,
+// float32 481 / 1365 and 658 / 1787; 128 heads 205 / 786 and 227 / 846, 510 / 1606 and 689 / 2030; 200 heads of 512 tokens, past
+// the border, bf16 108 / 386 and 75 / 310, float32 252 / 788 and 197 / 685.  In segments, float32 2 x 3 heads of 333 tokens,
+// 48 x 80: 36 / 93 and 41 / 105).
 DeltaShape delta_shape(int B, int H, int Hk, int T, int dk, int dv, int dtype) {
   DeltaShape s{};
   s.B = B;
@@ -35,10 +39,12 @@ DeltaShape delta_shape(int B, int H, int Hk, int T, int dk, int dv, int dtype) {
   long long most = 1;
   while (most < s.N && (most + 1) * (most + 1) <= 9LL * s.N) ++most;
   const long long heads = (long long)B * H, wide = heads * ((dv + 127) / 128);
-  s.NW = dv <= 64 || wide * most <= 128 ? 4 : 8;
-  const long long units = heads * ((dv + 16 * s.NW - 1) / (16 * s.NW));
-  long long P = 256 / units < most ? 256 / units : most;
-  if (P < 3) P = 1;
+  const auto segments = [&](long long units) {
+    const long long P = 256 / units < most ? 256 / units : most;
+    return P < 3 ? 1 : P;
+  };
+  s.NW = dv <= 64 || wide * segments(wide) <= 128 ? 4 : 8;
+  const long long P = segments(heads * ((dv + 16 * s.NW - 1) / (16 * s.NW)));
   s.L = (int)((s.N + P - 1) / P);
   s.P = (s.N + s.L - 1) / s.L;
   return s;

@@ -12,10 +12,10 @@ def shape(B, H, T, dk, dv):
     most = 1
     while most < N and (most + 1) ** 2 <= 9 * N:
         most += 1
-    NW = 4 if dv <= 64 or B * H * -(-dv // 128) * most <= 128 else 8
-    units = B * H * -(-dv // (16 * NW))
-    P = min(256 // units, most)
-    L = -(-N // (P if P >= 3 else 1))
+    segments = lambda units: min(256 // units, most) if min(256 // units, most) >= 3 else 1  # noqa: E731
+    wide = B * H * -(-dv // 128)
+    NW = 4 if dv <= 64 or wide * segments(wide) <= 128 else 8
+    L = -(-N // segments(B * H * -(-dv // (16 * NW))))
     return {"N": N, "P": -(-N // L), "NW": NW, "DKP": 32 if dk <= 32 else 64 if dk <= 64 else 128, "DVP": -(-dv // 16) * 16,
             "marks": -(-N // MARKS)}
 
@@ -60,6 +60,6 @@ def saved_bytes(B, H, Hk, T, dk, dv, dt):
 # several chunks, with 32, 64 and 128 channels, in both types; keys shared, odd widths, a last tile of few columns
 CASES = [(b, h, hk, t, dk, dv, dt, lens) for dt in (BF16, F32) for b, h, hk, t, dk, dv, lens in (
     (1, 17, 17, 700, 128, 128, None), (1, 9, 3, 700, 100, 200, (650,)), (2, 9, 9, 640, 64, 80, (640, 391)),
-    (1, 17, 17, 450, 24, 100, None), (1, 86, 86, 70, 128, 128, None), (2, 43, 43, 130, 72, 130, (130, 3)),
-    (1, 90, 45, 130, 64, 72, None), (1, 140, 70, 70, 32, 100, None), (1, 2, 1, 300, 128, 64, None), (1, 2, 2, 300, 40, 48, None),
+    (1, 17, 17, 450, 24, 100, None), (1, 86, 86, 70, 128, 128, None), (2, 65, 65, 66, 128, 128, None), (2, 35, 35, 130, 72, 130, (130, 3)),
+    (1, 90, 45, 130, 64, 72, None), (1, 130, 65, 130, 64, 72, None), (1, 140, 70, 70, 32, 100, None), (1, 2, 1, 300, 128, 64, None), (1, 2, 2, 300, 40, 48, None),
     (1, 3, 1, 500, 16, 300, (444,)), (1, 3, 3, 64, 128, 96, None), (2, 2, 2, 60, 64, 200, (60, 31)), (1, 2, 2, 33, 30, 64, None))]
