@@ -10,11 +10,13 @@
 // state from zero and its transition M (the same walk from the identity with V = 0), delta_scan_kernel chains
 // S <- M S + S_own, and the walk then starts from the true states.
 // What bounds it: a chunk's steps follow one another, so a CU's 8 waves share their time between the vector ALU (half of
-// the cycles: the splits, the scaling of states and errors, the decays), the matrix cores (28 %) and LDS (35 %); a training
-// walk also writes 115 KB a chunk and 128 columns and runs at HBM's rate, 4.6 TB/s.  bf16, 4 heads of 64k tokens, 128 x 256,
-// P = 32: gates and inverses 46 us, state pass 186, chain 39, walk 190, where q, k, v and o are 83 us of HBM.  P formed once
-// in delta_prep_kernel and loaded by the walks takes 184 of the walk and 61 of the other; 32 columns a wave or half the
-// waves, two workgroups a CU, take as long as these.
+// the cycles: the splits, the scaling of states and errors, the decays), the matrix cores (28 %, in a forward-only call more
+// since o's operands are split) and LDS (35 %); a training walk also writes 115 KB a chunk and 128 columns and runs at HBM's
+// rate, 4.8 TB/s.  bf16, 4 heads of 64k tokens, 128 x 256, P = 32, kernels traced one by one (500 us in all, where a call takes
+// 444 to 474 in a row): gates and inverses 47 us, state pass 192, chain 40, walk 222 (some 20 less with the state, W and P of o as
+// one bf16 each, which left o 2.9e-3 off in the 2-norm instead of its own rounding's 1.7e-3), where q, k, v and o are 83 us of HBM.  With
+// those operands of one part P formed once in delta_prep_kernel and loaded by the walks saved 6 us here and cost 15 there; 32
+// columns a wave or half the waves, two workgroups a CU, took as long.
 #include "gla_delta.hpp"
 #include "gla_delta_scan.hpp"
 

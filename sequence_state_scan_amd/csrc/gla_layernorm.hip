@@ -7,7 +7,9 @@
 // rounded value.  The weights' gradients are sums per workgroup, then a second kernel in a fixed order.
 // Bound by HBM: 32768 rows of 2048, bf16, without a residual 56 us, 4.8 TB/s; 16384 rows with one 46 us forward, 73 us and 5
 // for the weights' sums backward, 5.9 and 4.6 TB/s (the memory-side cache serves a part).  Rows of 2047 take 39 and 67 us
-// for 8000 where whole slots would take 27 and 33.
+// for 8000 where whole slots would take 27 and 33.  Rows above 8192 hold four slots a lane; with a float32 stream the backward
+// then has more than 256 registers' worth and keeps 13 (bf16) or 45 (float32) of them in memory: 2048 rows of 16384, bf16 with
+// float32, 147 us where its bytes take 123.
 #include "gla_layernorm.hpp"
 #include "gla_rows.hpp"
 

@@ -852,8 +852,8 @@ def gla_delta_fwd(q, k, v, g, beta, h0=None, lens=None, o=None, h_final=None, sa
     """The gated delta rule: S <- exp(g_t) S, then S <- S + beta_t k_t (v_t - S^T k_t)^T and o_t = S^T q_t, over q, k
     [B, Hk, T, dk], v [B, H, T, dv] (bf16 or float32; value head h reads key head h // (H // Hk)) and g (log-gates <= 0,
     or -inf for a reset), beta [B, H, T] (float32), from h0 [B, H, dk, dv] (float32, default zero; a reset at the first token
-    drops it whatever it holds).  lens: int32 [B], the sequences' lengths in a padded batch (o is zero behind them).  q, k and v may be views whose last dimension is
-    contiguous, g and beta any views.  dk <= 128.
+    drops it whatever it holds).  lens: int32 [B], the sequences' lengths in a padded batch (o is zero behind them).  q, k and
+    v may be views whose last dimension is contiguous, g and beta any views.  dk <= 128.
     Returns (o [B, H, T, dv], h_final [B, H, dk, dv], saved): saved is what gla_delta_bwd needs besides, a buffer of
     delta_saved_size bytes, None with keep_saved=False (a forward-only call)."""
     dims, ptrs = _delta_args(q, k, v, g, beta)

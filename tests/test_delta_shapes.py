@@ -23,3 +23,11 @@ def test_buffers_hold_their_regions_and_no_more(dt):
 
 def test_the_cases_take_every_kernel():
     assert {kind(B, H, T, dk, dv, dt) for B, H, Hk, T, dk, dv, dt, lens in CASES} == KINDS
+
+
+def test_limits_as_documented():
+    size = lambda B, H, T: gla.delta_saved_size(B, H, 1, T, 8, 8, torch.bfloat16)  # noqa: E731
+    assert size(1, (1 << 18) - 1, 16 * 64) > 0 and size(2, 1, 64 * ((1 << 21) - 1)) > 0
+    for B, H, T in ((1, 1 << 18, 1), (1 << 10, 1 << 8, 64), (2, 1, 64 * ((1 << 21) - 1) + 1), (1, 1 << 17, 64 * 32)):
+        with pytest.raises(gla.GLAError):
+            size(B, H, T)
